@@ -520,6 +520,132 @@ exl3_status exl3_debug_stall_tensor_wait(int on);
  */
 exl3_status exl3_device_status(const void *status_word, exl3_stream_t stream);
 
+/* ---- attention over a paged key/value cache held in 8 bits -------------------
+ *
+ * What a decoder needs between the q/k/v projections and the output projection
+ * (the source pages stop at the linear layers).  The cache is a pool of pages of
+ * `page_size` tokens; a request owns the pages its row of the block table
+ * names, in order.  Keys and values are int8, symmetric, with one binary32 scale
+ * for each page and head: value = q * scale, the largest |value| a page has held
+ * over 127 (the quantizer of exl3_quantize_act, its block a page of one head).
+ * One step of a server is exl3_kv_plan once, then for every layer
+ * exl3_kv_append and exl3_attention on that layer's cache.  All lengths, tables
+ * and maps are device memory: nothing of a step waits for the host, and a step
+ * can be captured in a CUDA graph.
+ */
+
+/** Most requests of one call. */
+#define EXL3_MAX_REQUESTS 8192
+
+/** One layer's cache. */
+typedef struct {
+  int8_t *k, *v;            /* [pages][kv_heads][page_size][head_dim], 16-byte aligned */
+  float *k_scale, *v_scale; /* [pages][kv_heads] */
+  int pages;
+  int kv_heads;
+  int page_size;            /* 16, 32, 64 or 128 */
+  int head_dim;             /* 64 or 128 */
+} exl3_kv_cache;
+
+/**
+ * Block tables and slot maps from the requests' lengths.  Request b holds
+ * c = ctx_len[b] >= 0 cached tokens in ceil(c / page_size) pages of its table
+ * row and brings n = new_len[b] tokens (0 allowed); new_len[b] < 0: it is
+ * finished, and its pages go back.  The free pages are a ring of
+ * `free_capacity` page numbers, free_state = {head, count}: the pages
+ * ring[head], ring[head + 1], ... (wrapping) are free.
+ *   - Requests in order take the pages they need from the ring's head.  One
+ *     whose pages go past `count`, whose row would pass table_stride or whose
+ *     tokens would pass `tokens` is refused: it gets no page and its tokens no
+ *     slot.  A refused request's need still counts for those after it (but for
+ *     the last two reasons), so no later, smaller request overtakes it.
+ *   - Pages of finished requests go to the ring's end (usable by the next call;
+ *     beyond the ring's capacity they are dropped).
+ * Outputs:
+ *   seq_len  [requests]     c + n; c if refused; 0 if finished
+ *   q_start  [requests + 1] running sum of max(n, 0), at most `tokens`: request
+ *                           b's tokens are q_start[b] .. q_start[b + 1] - 1
+ *   slot     [tokens]       page * page_size + offset of each token, -1 if refused
+ *   position [tokens]       its position in its request; -1 for tokens of no request
+ *   block_table [requests][table_stride]  the new pages are entered, nothing else changes
+ *   free_pages              the ring: finished requests' pages are entered
+ *   free_state_out [3]      {head, count} after the call, and the pages that
+ *                           refused requests lacked (0 when none was refused for pages)
+ * free_state_out must not overlap free_state, seq_len not ctx_len.  One launch.
+ * Errors: EXL3_ERR_BATCH (requests outside 0..EXL3_MAX_REQUESTS, tokens < 0),
+ * EXL3_ERR_SHAPE (page_size not one of the cache's, table_stride < 1,
+ * free_capacity < 0), EXL3_ERR_NULL, EXL3_ERR_ALIGN (an address not a multiple of
+ * its element's size).
+ */
+exl3_status exl3_kv_plan(const int32_t *ctx_len, const int32_t *new_len, int requests, int tokens,
+                         int page_size, int32_t *free_pages, int free_capacity,
+                         const int32_t *free_state, int32_t *free_state_out, int32_t *block_table,
+                         int table_stride, int32_t *seq_len, int32_t *q_start, int64_t *slot,
+                         int32_t *position, exl3_stream_t stream);
+
+/**
+ * Quantize `tokens` new keys and values into their slots (exl3_kv_plan's, or any
+ * map of the same kind: -1 skips a token; the tokens that a call puts into one
+ * page are consecutive in the call and in the page).  Per page and head:
+ *   scale' = max(scale, max|x| / 127), x the page's new values, `scale` taken as
+ *            0 when the first of them is the page's first token;
+ *   q = the nearest integer to x / scale', ties to even, 0 where scale' is 0;
+ *   the page's earlier tokens, when scale' > scale: the nearest integer to
+ *            q * (scale / scale').
+ * All quotients and products are binary32, correctly rounded.  A page whose new
+ * values hold an infinity or a NaN gets scale NaN and q 0 for all its tokens so
+ * far: attention over it gives NaN.
+ *   k, v [tokens][kv_heads][head_dim] halves, token t at k + t * k_stride halves
+ *   (strides multiples of 8, at least kv_heads * head_dim).
+ * Slots outside the cache are skipped.  One launch.  Errors: EXL3_ERR_NULL,
+ * EXL3_ERR_SHAPE (cache fields, strides), EXL3_ERR_BATCH (tokens < 0),
+ * EXL3_ERR_ALIGN.
+ */
+exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_half *k, long long k_stride,
+                           const exl3_half *v, long long v_stride, const int64_t *slot, int tokens,
+                           exl3_stream_t stream);
+
+/**
+ * Bytes of scratch for exl3_attention with up to `max_new` new tokens in any
+ * request: a status word (first 256 bytes), arrival counters, then the partial
+ * results of the work that is split between thread blocks.  It must be
+ * zero-filled once after allocation; every call leaves the counters zero again.
+ * Two calls that may run concurrently must not share one.  0 for invalid
+ * heads, head_dim or max_new < 1.
+ */
+size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_new);
+
+/**
+ * Attention of each request's newest tokens over its cache:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax over j of scale * (q[t][h] . k_j),
+ * j over the request's cached tokens up to t's own position.  Request b's
+ * rows are q_start[b] .. q_start[b + 1] - 1, the last of its seq_len[b] tokens
+ * (seq_len counts the new ones: append before); head h reads key/value head
+ * h / (q_heads / kv_heads).  A row that sees no key (seq_len 0, or more new
+ * tokens than seq_len) is 0 with lse -inf.
+ *   q   [tokens][q_heads][head_dim] halves, token t at q + t * q_stride halves
+ *   out the same with out_stride (must not overlap q); lse [tokens][q_heads]
+ *       floats or NULL: the natural log of the sum of exp(scale * (q . k_j)).
+ *   block_table [requests][table_stride]: entries past a request's pages are not
+ *       read; seq_len is cut to table_stride * page_size.  A page number outside
+ *       the pool reads as zeros.  Rows of no request are not written.
+ *   max_new: the most new tokens of any request.  It picks the kernels and
+ *       sizes the workspace; a request with more is computed all the same.
+ * The scores, the softmax statistics and the sums are binary32; the int8 keys
+ * and values enter the products exactly (as binary16 integers) and the
+ * probabilities rounded to binary16, relative to the row's largest p_j * v_scale.
+ * The result does not depend on the order in which thread blocks run.
+ * Errors: EXL3_ERR_NULL, EXL3_ERR_SHAPE (cache fields, q_heads not a multiple of
+ * kv_heads, strides, table_stride < 1), EXL3_ERR_BATCH (requests outside
+ * 0..EXL3_MAX_REQUESTS, tokens < 0, max_new < 1), EXL3_ERR_ALIGN,
+ * EXL3_ERR_WORKSPACE.
+ */
+exl3_status exl3_attention(const exl3_kv_cache *cache, const exl3_half *q, long long q_stride,
+                           int q_heads, const int32_t *q_start, const int32_t *seq_len, int requests,
+                           int tokens, int max_new, const int32_t *block_table, int table_stride,
+                           float scale, exl3_half *out, long long out_stride, float *lse,
+                           void *workspace, size_t workspace_bytes, exl3_stream_t stream);
+
 /** Size of the fixed device array that exl3_gemv_noalloc uses as scratch. */
 #define EXL3_NOALLOC_SCRATCH_BYTES (4u << 20)
 

@@ -13,6 +13,8 @@ _BINDING_NAMES = (
     "exl3_gemm_small", "exl3_gemv_noalloc", "exl3_workspace_bytes", "exl3_status_string",
     "exl3_version", "exl3_set_path", "workspace_status", "Exl3Error", "library_path", "load_library",
     "CB_3INST", "CB_1MAD",
+    "Exl3KvCache", "exl3_kv_plan", "exl3_kv_append", "exl3_attention", "exl3_attention_workspace_bytes",
+    "alloc_attention_workspace",
 )
 
 __all__ = list(_BINDING_NAMES)

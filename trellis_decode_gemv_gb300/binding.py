@@ -58,6 +58,13 @@ class Exl3LayerKC(ctypes.Structure):
     _fields_ = [("layer", Exl3Layer), ("K", _I), ("codebook", _I)]
 
 
+class Exl3KvCacheStruct(ctypes.Structure):
+    """exl3_kv_cache of the header: one layer's paged 8-bit cache."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("pages", _I), ("kv_heads", _I),
+                ("page_size", _I), ("head_dim", _I)]
+
+
+_LL = ctypes.c_longlong
 _SIGNATURES = {
     "exl3_rht_in": ([_P, _P, _P, _I, _I, _P], _I),
     "exl3_rht_out": ([_P, _P, _P, _I, _I, _P], _I),
@@ -89,6 +96,11 @@ _SIGNATURES = {
     "exl3_gemm_whole_grouped_workspace_bytes": ([ctypes.POINTER(Exl3Layer), _I, _I], _SZ),
     "exl3_gemm_whole_grouped": ([ctypes.POINTER(Exl3Layer), _I, _I, _I, _I, _P, _SZ, _P], _I),
     "exl3_gemm": ([_P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _SZ, _P], _I),
+    "exl3_kv_plan": ([_P, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P], _I),
+    "exl3_kv_append": ([ctypes.POINTER(Exl3KvCacheStruct), _P, _LL, _P, _LL, _P, _I, _P], _I),
+    "exl3_attention_workspace_bytes": ([_I, _I, _I, _I], _SZ),
+    "exl3_attention": ([ctypes.POINTER(Exl3KvCacheStruct), _P, _LL, _I, _P, _P, _I, _I, _I, _P, _I, ctypes.c_float,
+                        _P, _LL, _P, _P, _SZ, _P], _I),
     "exl3_set_path": ([_I], _I),
     "exl3_set_prefill": ([_I], _I),
     "exl3_debug_stall_tensor_wait": ([_I], _I),
@@ -715,3 +727,171 @@ def exl3_gemm(codes, K, codebook, m, n, s_in, s_out, scales, x, y=None, workspac
         _ptr(y, "y", _HALF, dev), _ptr(workspace, "workspace", (torch.uint8,), dev),
         workspace.numel(), _stream(dev)))
     return y if x.dim() == 2 else y.view(-1)
+
+
+MAX_REQUESTS = 8192
+PAGE_SIZES = (16, 32, 64, 128)
+HEAD_DIMS = (64, 128)
+_I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_F32 = (torch.float32,)
+_I8 = (torch.int8,)
+
+
+class Exl3KvCache:
+    """One layer's paged key/value cache in 8 bits, marshalled once.
+
+    k, v: int8 [pages, kv_heads, page_size, head_dim]; k_scale, v_scale: float32
+    [pages, kv_heads]; value = q * scale.  The page numbers of block tables and
+    slot maps (exl3_kv_plan) are the same for every layer's cache of a model.
+    """
+
+    def __init__(self, pages, kv_heads, page_size, head_dim, device="cuda"):
+        shape = (pages, kv_heads, page_size, head_dim)
+        self._bind(torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+    @classmethod
+    def from_tensors(cls, k, v, k_scale, v_scale):
+        """A cache over tensors that the caller holds (not copied)."""
+        self = cls.__new__(cls)
+        self._bind(k, v, k_scale, v_scale)
+        return self
+
+    def _bind(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise ValueError(f"cache tensors of shapes {tuple(k.shape)}, {tuple(v.shape)}, {tuple(k_scale.shape)}, "
+                             f"{tuple(v_scale.shape)}: expected [pages, kv_heads, page_size, head_dim] twice and "
+                             "[pages, kv_heads] twice")
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        if self.page_size not in PAGE_SIZES or self.head_dim not in HEAD_DIMS:
+            raise ValueError(f"page_size {self.page_size} and head_dim {self.head_dim}: expected one of {PAGE_SIZES} "
+                             f"and one of {HEAD_DIMS}")
+        self.device = k.device
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        dev = self.device
+        self.struct = Exl3KvCacheStruct(_ptr(k, "k", _I8), _ptr(v, "v", _I8, dev), _ptr(k_scale, "k_scale", _F32, dev),
+                                        _ptr(v_scale, "v_scale", _F32, dev), self.pages, self.kv_heads,
+                                        self.page_size, self.head_dim)
+        self._ref = ctypes.byref(self.struct)
+
+
+def exl3_kv_plan(ctx_len, new_len, tokens, page_size, free_pages, free_state, block_table, seq_len=None, q_start=None,
+                 slot=None, position=None, free_state_out=None):
+    """Block tables and slot maps on the GPU from the requests' lengths (see the
+    header): int32 ctx_len, new_len [requests], the ring free_pages and its
+    free_state [head, count, ...], block_table [requests, width] (new pages are
+    entered).  Returns (seq_len, q_start, slot, position, free_state_out);
+    free_state_out [3] is the next call's free_state."""
+    lib = load_library()
+    dev = ctx_len.device
+    n = ctx_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] < n or new_len.numel() != n or free_state.numel() < 2:
+        raise ValueError(f"{n} requests with new_len of {new_len.numel()}, block_table of {tuple(block_table.shape)} "
+                         f"and free_state of {free_state.numel()}")
+    for name, t, least in (("seq_len", seq_len, n), ("q_start", q_start, n + 1), ("slot", slot, tokens),
+                           ("position", position, tokens), ("free_state_out", free_state_out, 3)):
+        if t is not None and t.numel() < least:
+            raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
+    if seq_len is None:
+        seq_len = torch.empty(n, dtype=torch.int32, device=dev)
+    if q_start is None:
+        q_start = torch.empty(n + 1, dtype=torch.int32, device=dev)
+    if slot is None:
+        slot = torch.empty(tokens, dtype=torch.int64, device=dev)
+    if position is None:
+        position = torch.empty(tokens, dtype=torch.int32, device=dev)
+    if free_state_out is None:
+        free_state_out = torch.empty(3, dtype=torch.int32, device=dev)
+    _check(lib.exl3_kv_plan(
+        _ptr(ctx_len, "ctx_len", _I32), _ptr(new_len, "new_len", _I32, dev), n, tokens, page_size,
+        _ptr(free_pages, "free_pages", _I32, dev), free_pages.numel(), _ptr(free_state, "free_state", _I32, dev),
+        _ptr(free_state_out, "free_state_out", _I32, dev), _ptr(block_table, "block_table", _I32, dev),
+        block_table.shape[1], _ptr(seq_len, "seq_len", _I32, dev), _ptr(q_start, "q_start", _I32, dev),
+        _ptr(slot, "slot", _I64, dev), _ptr(position, "position", _I32, dev), _stream(dev)))
+    return seq_len, q_start, slot, position, free_state_out
+
+
+def _rows(t, name, dim, dev):
+    """Pointer and token stride of halves [tokens, heads, dim] whose tokens may be
+    apart (a slice of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3 or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, heads, {dim}]")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float16")
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != dim and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    # the stride of a single token says nothing
+    return t.data_ptr(), stride[0] if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def exl3_kv_append(cache, k, v, slot):
+    """Quantize new keys and values [tokens, kv_heads, head_dim] into the slots of
+    `cache` (int64 [tokens], -1: skipped)."""
+    dev = cache.device
+    kp, ks = _rows(k, "k", cache.head_dim, dev)
+    vp, vs = _rows(v, "v", cache.head_dim, dev)
+    tokens = slot.numel()
+    if k.shape[:2] != (tokens, cache.kv_heads) or v.shape[:2] != k.shape[:2]:
+        raise ValueError(f"k and v of shapes {tuple(k.shape)} and {tuple(v.shape)} for {tokens} slots and "
+                         f"{cache.kv_heads} heads")
+    _check(load_library().exl3_kv_append(cache._ref, kp, ks, vp, vs, _ptr(slot, "slot", _I64, dev), tokens,
+                                         _stream(dev)))
+
+
+def exl3_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, max_new: int) -> int:
+    return int(load_library().exl3_attention_workspace_bytes(q_heads, kv_heads, head_dim, max_new))
+
+
+def alloc_attention_workspace(q_heads: int, kv_heads: int, head_dim: int, max_new: int, device) -> torch.Tensor:
+    """A zero-filled workspace for exl3_attention."""
+    nbytes = exl3_attention_workspace_bytes(q_heads, kv_heads, head_dim, max_new)
+    if nbytes == 0:
+        raise Exl3Error(2, "invalid heads, head_dim or max_new for a workspace")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=None, out=None, lse=None,
+                   workspace=None):
+    """Attention of each request's newest tokens over `cache` (see the header):
+    q [tokens, q_heads, head_dim] halves, q_start [requests + 1] and seq_len
+    [requests] int32, block_table [requests, width] int32.  max_new: the most new
+    tokens of any request (default: all tokens).  scale: default head_dim**-0.5.
+    Returns out (like q), or (out, lse) with lse a float32 tensor [tokens,
+    q_heads] to write or True for a new one."""
+    dev = cache.device
+    qp, qs = _rows(q, "q", cache.head_dim, dev)
+    tokens, heads = q.shape[0], q.shape[1]
+    n = seq_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] < n or q_start.numel() < n + 1:
+        raise ValueError(f"{n} requests with q_start of {q_start.numel()} and block_table of {tuple(block_table.shape)}")
+    if heads % cache.kv_heads:
+        raise ValueError(f"q has {heads} heads for a cache of {cache.kv_heads}")
+    if max_new is None:
+        max_new = max(tokens, 1)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    if out is None:
+        out = torch.empty((tokens, heads, cache.head_dim), dtype=torch.float16, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    op, os_ = _rows(out, "out", cache.head_dim, dev)
+    if lse is True:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+    elif lse is not None and lse.shape != (tokens, heads):
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(tokens, heads)}")
+    if workspace is None:
+        workspace = alloc_attention_workspace(heads, cache.kv_heads, cache.head_dim, max_new, dev)
+    _check(load_library().exl3_attention(
+        cache._ref, qp, qs, heads, _ptr(q_start, "q_start", _I32, dev), _ptr(seq_len, "seq_len", _I32, dev), n, tokens,
+        max_new, _ptr(block_table, "block_table", _I32, dev), block_table.shape[1], scale, op, os_,
+        _ptr(lse, "lse", _F32, dev), _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(),
+        _stream(dev)))
+    return out if lse is None else (out, lse)
