@@ -256,3 +256,13 @@ def test_nothing_to_do():
         B.exl3_attention(cache, cuda(x["q"]).transpose(0, 1), cuda(x["q_start"]), cuda(x["seq_len"]), cuda(x["block_table"]))
     with pytest.raises(TypeError):
         B.exl3_attention(cache, cuda(x["q"]).float(), cuda(x["q_start"]), cuda(x["seq_len"]), cuda(x["block_table"]))
+
+
+@pytest.mark.parametrize("requests,new", [(33, 1), (100, 1), (300, 1), (65, 2), (40, 20)])
+def test_many_requests(requests, new):
+    """More requests than a warp has lanes, than a block has threads; some bring nothing; long ranges for every block."""
+    rng = np.random.default_rng(requests + new)
+    seq = rng.integers(0, 9000 // (new + requests // 20), requests)
+    news = np.where(rng.random(requests) < 0.1, 0, new)
+    x = make(rng, 8, 4, 64, 64, [int(s) for s in np.maximum(seq, news)], [int(n) for n in news])
+    check(x, run(x))

@@ -176,9 +176,6 @@ exl3_status run_tensor(LayerArgs a, int M, float* zacc, uint32_t* status, __half
 // 64-bit elements, a box of 32K x 8.
 // The driver's tensor-map encoder, looked up through the runtime (so that the
 // library loads, for its host-side checks, where no driver is installed).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn encode_tiled() {
   static std::atomic<EncodeTiledFn> fn{nullptr};
   EncodeTiledFn f = fn.load(std::memory_order_acquire);

@@ -2,32 +2,18 @@
 // cache.
 #include <math.h>
 
-#include "exl3_kv.cuh"
+#include "exl3_attn.cuh"
 
 namespace exl3 {
 namespace attn {
 namespace {
-
-struct AttnParams {
-  exl3_kv_cache c;
-  const __half* q;
-  long long q_stride;
-  const int32_t* q_start;
-  const int32_t* seq_len;
-  const int32_t* table;
-  __half* out;
-  long long out_stride;
-  float* lse;
-  float scale;
-  int q_heads, requests, tokens, stride;
-};
 
 constexpr int kWarps = 4;
 
 // One CTA per (token, head); its warps share the keys, each with an online
 // softmax of its own, joined at the end.  A lane holds D / 32 elements.
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p, const exl3_kv_cache c) {
   constexpr int E = D / 32;
   const int t = blockIdx.x;
   const int h = blockIdx.y;
@@ -40,11 +26,11 @@ __global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p) {
     const int mid = (lo + hi) >> 1;
     if (p.q_start[mid] <= t) lo = mid; else hi = mid;
   }
-  const int size = p.c.page_size;
-  const long long most = static_cast<long long>(p.stride) * size;
-  const long long seq = min(static_cast<long long>(max(p.seq_len[lo], 0)), most);
-  const long long last = seq - (p.q_start[lo + 1] - t);  // this row's own position
-  const int kvh = h / (p.q_heads / p.c.kv_heads);
+  const int size = c.page_size;
+  const Req r = load_req(p, lo);
+  if (r.rows == 0) return;
+  const long long last = r.seq - (r.t0 + r.n - t);  // this row's own position
+  const int kvh = h / p.group;
   float q[E], o[E], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -52,17 +38,17 @@ __global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p) {
     o[e] = 0.f;
   }
   for (long long j = warp; j <= last; j += kWarps) {
-    const int page = p.table[static_cast<size_t>(lo) * p.stride + j / size];
-    const bool in = page >= 0 && page < p.c.pages;
-    const size_t block = in ? static_cast<size_t>(page) * p.c.kv_heads + kvh : 0;
+    const int page = p.table[static_cast<size_t>(lo) * p.table_stride + j / size];
+    const bool in = page >= 0 && page < c.pages;
+    const size_t block = in ? static_cast<size_t>(page) * c.kv_heads + kvh : 0;
     const size_t at = (block * size + j % size) * D + lane * E;
     float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * static_cast<float>(p.c.k[at + e]);
+    for (int e = 0; e < E; ++e) s += q[e] * static_cast<float>(c.k[at + e]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= in ? p.c.k_scale[block] * p.scale : 0.f;
-    const float vs = in ? p.c.v_scale[block] : 0.f;
+    s *= in ? c.k_scale[block] * (p.c * kLn2) : 0.f;
+    const float vs = in ? c.v_scale[block] : 0.f;
     const float top = fmaxf(m, s);
     const float base = top == -INFINITY ? 0.f : top;
     const float keep = expf(m - base);
@@ -70,7 +56,7 @@ __global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p) {
     m = top;
     l = l * keep + w;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * vs * static_cast<float>(p.c.v[at + e]);
+    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * vs * static_cast<float>(c.v[at + e]);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
@@ -93,6 +79,22 @@ __global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p) {
 }
 
 }  // namespace
+
+exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache& c, int rows) {
+  const EncodeTiledFn encode = encode_tiled();
+  if (encode == nullptr) return EXL3_ERR_CUDA;
+  const cuuint64_t d = static_cast<cuuint64_t>(c.head_dim), size = static_cast<cuuint64_t>(c.page_size);
+  const cuuint64_t dims[3] = {d, size, static_cast<cuuint64_t>(c.pages) * static_cast<cuuint64_t>(c.kv_heads)};
+  const cuuint64_t strides[2] = {d, d * size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(rows), 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EXL3_OK : EXL3_ERR_CUDA;
+}
+
 }  // namespace attn
 }  // namespace exl3
 
@@ -101,7 +103,7 @@ using namespace exl3;
 extern "C" size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_new) {
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || max_new < 1)
     return 0;
-  return 256;
+  return attn::arrived_bytes() + 2 * attn::kMaxCtas * attn::step_slot_floats(head_dim) * sizeof(float);
 }
 
 extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_half* q, long long q_stride, int q_heads,
@@ -125,13 +127,45 @@ extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_hal
   if (workspace == nullptr ||
       workspace_bytes < exl3_attention_workspace_bytes(q_heads, cache->kv_heads, cache->head_dim, max_new))
     return EXL3_ERR_WORKSPACE;
-  attn::AttnParams p{*cache, reinterpret_cast<const __half*>(q), q_stride, q_start, seq_len, block_table,
-                     reinterpret_cast<__half*>(out), out_stride, lse, scale, q_heads, requests, tokens, table_stride};
-  const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(q_heads));
+  attn::AttnParams p{};
+  p.q = reinterpret_cast<const __half*>(q);
+  p.q_start = q_start;
+  p.seq_len = seq_len;
+  p.table = block_table;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.out = reinterpret_cast<__half*>(out);
+  p.lse = lse;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.c = scale * attn::kLog2e;
+  p.q_heads = q_heads;
+  p.kv_heads = cache->kv_heads;
+  p.group = q_heads / cache->kv_heads;
+  p.requests = requests;
+  p.tokens = tokens;
+  p.table_stride = table_stride;
+  p.pages = cache->pages;
+  while ((1 << p.page_shift) < cache->page_size) ++p.page_shift;
+  // keys are numbered in 31 bits
+  p.most = static_cast<long long>(table_stride) << p.page_shift;
+  if (p.most > 0x7FFFFF00LL) p.most = 0x7FFFFF00LL;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.arrived = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + 256);
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + attn::arrived_bytes());
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool step = static_cast<long long>(max_new) * p.group <= attn::kStepRows;
+  if (step || requests > 1) {
+    p.rows_lo = 1;
+    p.rows_hi = step ? 0x7FFFFFFF : attn::kStepRows;
+    if ((st = attn::launch_step(p, *cache, (step ? max_new : 1) * p.group > 8, cs)) != EXL3_OK || step) return st;
+  }
+  p.rows_lo = requests > 1 ? attn::kStepRows + 1 : 1;
+  p.rows_hi = 0x7FFFFFFF;
+  const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(q_heads));
   if (cache->head_dim == 64)
-    attn::row_kernel<64><<<grid, 32 * attn::kWarps, 0, cs>>>(p);
+    attn::row_kernel<64><<<grid, 32 * attn::kWarps, 0, cs>>>(p, *cache);
   else
-    attn::row_kernel<128><<<grid, 32 * attn::kWarps, 0, cs>>>(p);
+    attn::row_kernel<128><<<grid, 32 * attn::kWarps, 0, cs>>>(p, *cache);
   return launch_status();
 }

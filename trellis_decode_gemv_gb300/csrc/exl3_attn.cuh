@@ -1,0 +1,154 @@
+// Shared by the attention kernels: parameters, the numbering of the work, the
+// PTX that both use, and the join of partial results.
+//
+// Mathematics.  With k_j = ks_j * K_j and v_j = vs_j * V_j (K, V int8, one scale
+// per page and head) and c = scale * log2(e), a row's result is
+//   x_j = c ks_j (q . K_j) + log2 vs_j,   m >= max_j x_j - 8,   P_j = 2^(x_j - m),
+//   out = (sum_j P_j V_j) / l,   l = sum_j P_j / vs_j,   lse = ln 2 * m + ln l.
+// The value's scale rides in the exponent, so V enters the product as it is
+// stored and P (rounded to binary16 for the tensor cores) keeps its 11 bits
+// whatever the pages' scales are, as it would not if it were multiplied by a
+// small scale first; the sum l takes it out again, in binary32.  m, a running
+// maximum, is only moved when a score passes it by more than 2^8: P stays within
+// binary16's range, and the accumulators are rescaled rarely.
+//
+// Work.  An item is one (request, key/value head, tile of query rows); it has
+// as many units (tiles of keys) as its rows see.  The units of all items, in
+// order, are cut into equal ranges, one for each CTA, whatever the requests'
+// lengths are.  An item inside one range is finished there; one that crosses
+// ranges leaves partial results (m, l and the sums, binary32), and the CTA whose
+// arrival completes the item joins them in the order of the keys, so the result
+// does not depend on which CTA that is.  Everything is computed from the lengths
+// in device memory.
+#pragma once
+
+#include "exl3_kv.cuh"
+#include "exl3_tc.cuh"
+
+namespace exl3 {
+namespace attn {
+
+using tc::bulk_g2s;
+using tc::mbar_arrive;
+using tc::mbar_arrive_expect_tx;
+using tc::mbar_init;
+using tc::mbar_wait;
+using tc::smem_u32;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;     // log2 of the largest P
+constexpr float kTinyScale = -90.f;  // log2 that stands for a value scale of 0: its V add nothing, its P still count in l
+constexpr int kMaxCtas = 160 * 4; // ranges that the workspace holds partial results of
+
+struct AttnParams {
+  const __half* q;
+  const int32_t* q_start;
+  const int32_t* seq_len;
+  const int32_t* table;
+  const float* k_scale;
+  const float* v_scale;
+  __half* out;
+  float* lse;
+  long long q_stride, out_stride;
+  float c;                 // scale * log2(e)
+  int q_heads, kv_heads, group, requests, tokens;
+  int table_stride, pages, page_shift;
+  long long most;          // keys that a table row holds
+  int rows_lo, rows_hi;    // requests with rows in [rows_lo, rows_hi] are this launch's
+  uint32_t* status;
+  uint32_t* arrived;       // [kMaxCtas], zero between calls: arrivals at the item that begins in CTA c and ends later
+  float* partial;          // [2 * kMaxCtas] slots: 2c the item that began before CTA c's range, 2c + 1 the one that ends after it
+};
+
+// A request as the kernels see it; lengths are cut to what the table and the
+// arrays hold.
+struct Req {
+  int t0, n, rows;  // first token, new tokens, rows (new * group), 0 if another launch's
+  int seq;          // cached tokens, the new ones included
+};
+
+__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
+  Req r{0, 0, 0, 0};
+  if (b < p.requests) {
+    const int a = min(max(p.q_start[b], 0), p.tokens);
+    const int e = min(max(p.q_start[b + 1], 0), p.tokens);
+    r.t0 = a;
+    r.n = max(e - a, 0);
+    const long long rows = static_cast<long long>(r.n) * p.group;
+    r.rows = rows >= p.rows_lo && rows <= p.rows_hi ? static_cast<int>(rows) : 0;
+    r.seq = static_cast<int>(min(static_cast<long long>(max(p.seq_len[b], 0)), p.most));
+  }
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The row's result from its sums: `sees` whether it sees a key at all.
+__device__ __forceinline__ float inverse_sum(float l, bool sees) { return sees ? __fdividef(1.f, l) : 0.f; }
+
+struct PageScale {
+  float c;  // c ks
+  float lv; // log2 vs
+  float iv; // 1 / 2^lv
+};
+
+__device__ __forceinline__ PageScale page_scale(const AttnParams& p, int page, int head) {
+  PageScale s{0.f, 0.f, 1.f};  // a page outside the pool reads as zeros
+  if (page >= 0 && page < p.pages) {
+    const size_t at = static_cast<size_t>(page) * p.kv_heads + head;
+    const float vs = __ldg(p.v_scale + at);
+    s.c = __ldg(p.k_scale + at) * p.c;
+    s.lv = vs == 0.f ? kTinyScale : log2f(vs);
+    // of the rounded logarithm, so that l and the sums agree; finite, so that it spoils no row whose P is 0
+    s.iv = vs != vs ? 1.f : exp2f(-s.lv);
+  }
+  return s;
+}
+
+// Tensor copy of a box of tokens of one page and head: coordinates (0, token,
+// page * kv_heads + head).
+__device__ __forceinline__ void tensor_g2s(void* dst, const CUtensorMap* map, int token, int block, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(0), "r"(token), "r"(block), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Exact binary16 of the int8 in bytes 0, 1 (resp. 2, 3) of x, whose top bits are
+// flipped: 0x64uu is the binary16 1024 + u, and u - 128 is the value.
+__device__ __forceinline__ uint32_t half2_sub1152(uint32_t v) {
+  const uint32_t k = 0x64806480u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t flipped) { return half2_sub1152(__byte_perm(flipped, 0x64646464u, 0x4140)); }
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t flipped) { return half2_sub1152(__byte_perm(flipped, 0x64646464u, 0x4342)); }
+
+// CTA `c` of `ctas` takes the units [c * units / ctas, (c + 1) * units / ctas).
+__device__ __forceinline__ long long range_begin(long long units, int c, int ctas) {
+  return static_cast<long long>(static_cast<unsigned long long>(units) * c / ctas);
+}
+__device__ __forceinline__ int range_of(long long units, long long u, int ctas) {
+  return static_cast<int>((static_cast<unsigned long long>(u + 1) * ctas - 1) / units);
+}
+
+// The keys or values as [pages * kv_heads][page_size][head_dim] bytes, boxes of
+// `rows` tokens, 16-byte pieces swizzled.
+exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache& c, int rows);
+
+// The status word and the arrival counters come first in the workspace.
+constexpr size_t arrived_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas; }
+
+// Up to kStepRows query rows per key/value head (of more, tile by tile).
+constexpr int kStepRows = 16;
+constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kStepRows) * (head_dim + 2); }
+exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream);
+
+}  // namespace attn
+}  // namespace exl3

@@ -1,0 +1,613 @@
+// Attention of a few query rows per key/value head (single tokens, drafted tokens):
+// every cached byte is read once and used by at most 16 rows, so the cache's
+// bytes per second are the bound, and what the kernel must do besides is to turn
+// every byte into a binary16 MMA operand (1.25 to 1.5 instructions a byte) with
+// enough copies in flight.
+//
+// Three consumer warps and one producer warp.  A unit is 32 keys of an item: 32 x
+// D bytes of K and of V, one tensor copy each (two for pages of 16 tokens), into
+// a ring of stages; unit i of the CTA's range goes to stage i % kStages and to
+// consumer i % 3.  The producer walks the range ahead of the consumers: page
+// numbers and scales of up to 32 units at a time, the copies, and each item's
+// query rows (bulk copies) into a two-deep ring of their own, so nothing that
+// waits for memory is left to the consumers.
+//
+// A consumer computes S^T = K Q^T and O^T += V^T P^T with m16n8k16 MMAs: the 16
+// side is keys, then head dimensions, the 8 side the query rows (one or two
+// tiles of 8), so that four or eight heads of a group do not fill half of a
+// 16-row operand with nothing.  K is operand A of the first product: a lane's
+// bytes of a key row are contiguous (the order of the head dimension in the
+// products is free, Q is laid out the same).  V^T is operand A of the second:
+// lane (g, t) reads the 16 bytes g of keys 2t, 2t+1, 2t+8, 2t+9, and the byte
+// permutes that widen them also pair the keys.  P^T comes from S^T by one 8x8
+// transposition (movmatrix).  The tensor copies swizzle 16-byte pieces, so both
+// reads are free of bank conflicts for D = 128.
+#include "exl3_attn.cuh"
+
+namespace exl3 {
+namespace attn {
+namespace {
+
+constexpr int kConsumers = 3;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kUnit = 32;           // keys
+constexpr int kQSlots = 2;
+constexpr int kJoinBarrier = 1;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStages = 6;
+  static_assert(kStages % kConsumers == 0, "each stage belongs to one consumer, so that no parity wait skips a phase");
+  static constexpr int kHalfBytes = kUnit * D;           // K or V of a unit
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kPartStride = D + 4;
+  static constexpr int kPartBytes = kConsumers * kRows * kPartStride * 4;
+  static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
+};
+
+template <int D, int NT>
+struct Shared {
+  using C = Cfg<D, NT>;
+  unsigned char ring[C::kStages][C::kStageBytes];  // first: 1024-byte aligned
+  __half q[kQSlots][C::kRows * D];
+  float part[kConsumers][C::kRows][C::kPartStride];
+  float pm[kConsumers][C::kRows], pl[kConsumers][C::kRows];
+  float4 scale[C::kStages][2];      // per 16 keys: PageScale
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t q_full[kQSlots], q_empty[kQSlots];
+  long long warp_sum[kThreads / 32];
+  long long first_unit;             // of request first_b
+  int first_b;
+  uint32_t abort, last;
+};
+
+__device__ __forceinline__ void join_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kJoinBarrier), "n"(32 * kConsumers) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <int NT>
+__device__ __forceinline__ int req_tiles(const Req& r) { return (r.rows + 8 * NT - 1) / (8 * NT); }
+__device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq + kUnit - 1) / kUnit); }
+
+// The items of a range, one after the other.  Each lane of a warp holds one
+// request; every warp walks by itself.
+template <int NT>
+struct Walker {
+  const AttnParams& p;
+  long long u, end;   // next unit, end of the range
+  int base, b;        // request of lane 0, current request
+  Req mine;
+  // current segment
+  Req r;
+  int blocks, tiles, head, tile, lo, hi;
+  int item;
+
+  __device__ __forceinline__ Walker(const AttnParams& params, int first_b, long long first_unit, long long u0, long long u1)
+      : p(params), u(u0), end(u1), base(first_b), b(first_b) {
+    mine = load_req(p, base + (threadIdx.x & 31));
+    fetch();
+    if (u < end) {
+      const long long rem = u - first_unit;
+      item = static_cast<int>(rem / blocks);
+      lo = static_cast<int>(rem - static_cast<long long>(item) * blocks);
+      place();
+    }
+  }
+  __device__ __forceinline__ void fetch() {
+    const int src = b - base;
+    r.t0 = __shfl_sync(0xFFFFFFFFu, mine.t0, src);
+    r.n = __shfl_sync(0xFFFFFFFFu, mine.n, src);
+    r.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, src);
+    r.seq = __shfl_sync(0xFFFFFFFFu, mine.seq, src);
+    blocks = req_blocks(r);
+    tiles = req_tiles<NT>(r);
+  }
+  __device__ __forceinline__ void place() {
+    head = item / tiles;
+    tile = item - head * tiles;
+    hi = static_cast<int>(min(static_cast<long long>(blocks), lo + (end - u)));
+  }
+  __device__ __forceinline__ bool more() const { return u < end; }
+  __device__ __forceinline__ void next() {
+    u += hi - lo;
+    if (u >= end) return;
+    lo = 0;
+    if (++item >= tiles * p.kv_heads) {
+      item = 0;
+      do {
+        if (++b - base == 32) {
+          base = b;
+          mine = load_req(p, base + (threadIdx.x & 31));
+        }
+        fetch();
+      } while (r.rows == 0 && b < p.requests);
+    }
+    place();
+  }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
+    step_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                int min_units) {
+  using C = Cfg<D, NT>;
+  constexpr int kRows = C::kRows;
+  constexpr int kStages = C::kStages;
+  constexpr int KS = D / 16;  // k-steps of the first product, m-tiles of the second
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem_raw);
+  const int tid = threadIdx.x;
+  const int lane = tid & 31;
+  const int warp = tid >> 5;
+  const int cta = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < kQSlots; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], kConsumers);
+    }
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
+  // units of all requests, and the request in which this CTA's range begins
+  const int per = (p.requests + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Req r = load_req(p, b);
+    mine += static_cast<long long>(req_blocks(r)) * req_tiles<NT>(r) * p.kv_heads;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) sh.warp_sum[warp] = inc;
+  __syncthreads();
+  long long units = 0, before = inc - mine;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    before += w < warp ? sh.warp_sum[w] : 0;
+    units += sh.warp_sum[w];
+  }
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (units + min_units - 1) / min_units));
+  if (cta >= ctas) return;
+  const long long u0 = range_begin(units, cta, ctas), u1 = range_begin(units, cta + 1, ctas);
+  if (before <= u0 && u0 < before + mine) {
+    for (int b = b0; b < b1; ++b) {
+      const Req r = load_req(p, b);
+      const long long n = static_cast<long long>(req_blocks(r)) * req_tiles<NT>(r) * p.kv_heads;
+      if (u0 < before + n) {
+        sh.first_b = b;
+        sh.first_unit = before;
+        break;
+      }
+      before += n;
+    }
+  }
+  __syncthreads();
+  Walker<NT> w(p, sh.first_b, sh.first_unit, u0, u1);
+
+  if (warp == kConsumers) {
+    // ---- producer ------------------------------------------------------------------
+    const int size = 1 << p.page_shift;
+    const int copies = p.page_shift == 4 ? 2 : 1;   // per unit, of K and of V
+    const int copy_bytes = C::kHalfBytes / copies;
+    uint32_t i = 0;       // unit of the range
+    int seg = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next(), ++seg) {
+      // query rows of the item
+      const int qs = seg % kQSlots;
+      if (seg >= kQSlots) ok = mbar_wait(&sh.q_empty[qs], static_cast<uint32_t>((seg / kQSlots) - 1) & 1);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      const int row0 = w.tile * kRows;
+      const int rows = min(kRows, w.r.rows - row0);
+      if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[qs], static_cast<uint32_t>(rows) * D * 2);
+      __syncwarp();
+      const int tok0 = row0 / p.group;
+      const int tok = tok0 + lane;   // at most 16 tokens have rows in a tile
+      const int ra = max(row0, tok * p.group), rb = min(row0 + rows, (tok + 1) * p.group);
+      if (ra < rb)
+        bulk_g2s(&sh.q[qs][(ra - row0) * D],
+                 p.q + static_cast<size_t>(w.r.t0 + tok) * p.q_stride + static_cast<size_t>(w.head * p.group + (ra - tok * p.group)) * D,
+                 static_cast<uint32_t>(rb - ra) * D * 2, &sh.q_full[qs]);
+      // units, 32 at a time: lane l looks up unit g0 + l
+      const int32_t* row = p.table + static_cast<size_t>(w.b) * p.table_stride;
+      for (int g0 = w.lo; g0 < w.hi && ok; g0 += 32) {
+        const int mykey = (g0 + lane) * kUnit;
+        int page[2] = {-1, -1};
+        PageScale s[2] = {{0.f, 0.f, 1.f}, {0.f, 0.f, 1.f}};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (g0 + lane < w.hi && mykey + 16 * hf < w.r.seq && (hf == 0 || copies == 2))
+            page[hf] = __ldg(row + ((mykey + 16 * hf) >> p.page_shift));
+        }
+        s[0] = page_scale(p, page[0], w.head);
+        s[1] = copies == 2 ? page_scale(p, page[1], w.head) : s[0];
+        const int outside = p.pages * p.kv_heads;
+        const int blk0 = page[0] >= 0 && page[0] < p.pages ? page[0] * p.kv_heads + w.head : outside;
+        const int blk1 = page[1] >= 0 && page[1] < p.pages ? page[1] * p.kv_heads + w.head : outside;
+        const int n = min(32, w.hi - g0);
+        for (int j = 0; j < n; ++j, ++i) {
+          const uint32_t st = i % kStages;
+          const uint32_t use = i / kStages;
+          if (use > 0) ok = mbar_wait(&sh.empty[st], (use - 1) & 1);
+          if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+          if (lane == j) {
+            sh.scale[st][0] = make_float4(s[0].c, s[0].lv, s[0].iv, 0.f);
+            sh.scale[st][1] = make_float4(s[1].c, s[1].lv, s[1].iv, 0.f);
+            // what lies past the request's keys is not copied: any int8 is finite, and P is 0 there
+            const bool first = mykey < w.r.seq, second = copies == 2 && mykey + 16 < w.r.seq;
+            mbar_arrive_expect_tx(&sh.full[st], static_cast<uint32_t>(2 * copy_bytes * ((first ? 1 : 0) + (second ? 1 : 0))));
+            unsigned char* dst = sh.ring[st];
+            if (first) {
+              tensor_g2s(dst, &kmap, mykey & (size - 1), blk0, &sh.full[st]);
+              tensor_g2s(dst + C::kHalfBytes, &vmap, mykey & (size - 1), blk0, &sh.full[st]);
+            }
+            if (second) {
+              tensor_g2s(dst + copy_bytes, &kmap, 0, blk1, &sh.full[st]);
+              tensor_g2s(dst + C::kHalfBytes + copy_bytes, &vmap, 0, blk1, &sh.full[st]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&sh.abort, 1u);
+    // Wait (bounded) for the copies in flight.
+    for (uint32_t k = 0; k < kStages && k < i; ++k) mbar_wait(&sh.full[(i - 1 - k) % kStages], ((i - 1 - k) / kStages) & 1);
+    for (int k = 0; k < kQSlots && k < seg; ++k) mbar_wait(&sh.q_full[(seg - 1 - k) % kQSlots], static_cast<uint32_t>((seg - 1 - k) / kQSlots) & 1);
+    return;
+  }
+
+  // ---- consumers --------------------------------------------------------------------
+  const int g = lane >> 2;
+  const int t = lane & 3;
+  bool ok = true;
+  uint32_t i = 0;   // unit of the range at the segment's start
+  for (int seg = 0; w.more(); w.next(), ++seg) {
+    const int qs = seg % kQSlots;
+    if (ok) ok = mbar_wait(&sh.q_full[qs], (seg / kQSlots) & 1) && *reinterpret_cast<volatile uint32_t*>(&sh.abort) == 0u;
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    const int row0 = w.tile * kRows;
+    // Q as operand B: lane (g, t) holds row g's elements E t .. E t + E - 1, E = D / 4
+    uint32_t qf[NT][KS][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint4* src = reinterpret_cast<const uint4*>(&sh.q[qs][(nt * 8 + g) * D + t * (D / 4)]);
+#pragma unroll
+      for (int k = 0; k < KS / 2; ++k) {
+        const uint4 v = src[k];
+        qf[nt][2 * k][0] = v.x;
+        qf[nt][2 * k][1] = v.y;
+        qf[nt][2 * k + 1][0] = v.z;
+        qf[nt][2 * k + 1][1] = v.w;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_empty[qs]);
+    // keys that this lane's rows (8 nt + 2t, + 1) see; the least of the tile
+    const int seen0 = w.r.seq - w.r.n;
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[nt][e] = seen0 + (row0 + nt * 8 + 2 * t + e) / p.group + 1;
+    const int lim_min = seen0 + row0 / p.group + 1;
+
+    float o[NT][KS][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][k][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    const int skip = static_cast<int>((warp + kConsumers - i % kConsumers) % kConsumers);
+    for (int blk = w.lo + skip; blk < w.hi; blk += kConsumers) {
+      const uint32_t at = i + static_cast<uint32_t>(blk - w.lo);
+      const uint32_t st = at % kStages;
+      if (ok) ok = mbar_wait(&sh.full[st], (at / kStages) & 1) && *reinterpret_cast<volatile uint32_t*>(&sh.abort) == 0u;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) {
+        if (lane == 0) atomicOr(&sh.abort, 1u);
+        break;
+      }
+      const unsigned char* kb = sh.ring[st];
+      const unsigned char* vb = kb + C::kHalfBytes;
+      // scores of 2 x 16 keys
+      float s[2][NT][4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[hf][nt][e] = 0.f;
+        const int r0 = hf * 16 + g;
+#pragma unroll
+        for (int pc = 0; pc < D / 64; ++pc) {   // 16-byte pieces of a lane's share of a row
+          uint4 a, b;
+          if constexpr (D == 128) {
+            const int off = ((2 * t + pc) ^ g) * 16;
+            a = *reinterpret_cast<const uint4*>(kb + r0 * D + off);
+            b = *reinterpret_cast<const uint4*>(kb + (r0 + 8) * D + off);
+          } else {
+            const int off = (t ^ ((g >> 1) & 3)) * 16;
+            a = *reinterpret_cast<const uint4*>(kb + r0 * D + off);
+            b = *reinterpret_cast<const uint4*>(kb + (r0 + 8) * D + off);
+          }
+          const uint32_t aw[4] = {a.x ^ 0x80808080u, a.y ^ 0x80808080u, a.z ^ 0x80808080u, a.w ^ 0x80808080u};
+          const uint32_t bw[4] = {b.x ^ 0x80808080u, b.y ^ 0x80808080u, b.z ^ 0x80808080u, b.w ^ 0x80808080u};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = cvt_lo(aw[k]), a1 = cvt_lo(bw[k]), a2 = cvt_hi(aw[k]), a3 = cvt_hi(bw[k]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(s[hf][nt], a0, a1, a2, a3, qf[nt][4 * pc + k][0], qf[nt][4 * pc + k][1]);
+          }
+        }
+      }
+      // x = c ks s + log2 vs, masked
+      const float4 sc[2] = {sh.scale[st][0], sh.scale[st][1]};
+      const int key0 = blk * kUnit;
+      const bool mask = key0 + kUnit > lim_min;
+      bool over = false;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = fmaf(s[hf][nt][e], sc[hf].x, sc[hf].y);
+            if (mask && key0 + hf * 16 + g + (e >> 1) * 8 >= lim[nt][e & 1]) x = -INFINITY;
+            s[hf][nt][e] = x;
+            over |= x > m[nt][e & 1] + kSlack;
+          }
+      if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            top = fmaxf(top, m[nt][e]);
+            const float keep = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
+            m[nt][e] = top;
+            l[nt][e] *= keep;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[nt][k][e] *= keep;
+              o[nt][k][e + 2] *= keep;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float base0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float base1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float p0 = ex2(s[hf][nt][0] - base0), p1 = ex2(s[hf][nt][1] - base1);
+          const float p2 = ex2(s[hf][nt][2] - base0), p3 = ex2(s[hf][nt][3] - base1);
+          l[nt][0] = fmaf(p0 + p2, sc[hf].z, l[nt][0]);
+          l[nt][1] = fmaf(p1 + p3, sc[hf].z, l[nt][1]);
+          const __half2 lo = __floats2half2_rn(p0, p1), up = __floats2half2_rn(p2, p3);
+          pb[hf][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          pb[hf][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&up));
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        constexpr int W = D / 32;  // words of a lane's share of a key
+        uint32_t v[4][W];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const int r = hf * 16 + 2 * t + (kk & 1) + (kk >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vb + r * D + ((g ^ (r & 7)) * 16));
+            v[kk][0] = x.x ^ 0x80808080u;
+            v[kk][1] = x.y ^ 0x80808080u;
+            v[kk][2] = x.z ^ 0x80808080u;
+            v[kk][3] = x.w ^ 0x80808080u;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(vb + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16) + (g & 1) * 8);
+            v[kk][0] = x.x ^ 0x80808080u;
+            v[kk][1] = x.y ^ 0x80808080u;
+          }
+        }
+        if (hf == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[st]);  // the stage is in registers
+        }
+#pragma unroll
+        for (int wd = 0; wd < W; ++wd) {
+          const uint32_t x01 = __byte_perm(v[0][wd], v[1][wd], 0x5140), x23 = __byte_perm(v[0][wd], v[1][wd], 0x7362);
+          const uint32_t y01 = __byte_perm(v[2][wd], v[3][wd], 0x5140), y23 = __byte_perm(v[2][wd], v[3][wd], 0x7362);
+          {
+            const uint32_t a0 = cvt_lo(x01), a1 = cvt_hi(x01), a2 = cvt_lo(y01), a3 = cvt_hi(y01);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * wd], a0, a1, a2, a3, pb[hf][nt][0], pb[hf][nt][1]);
+          }
+          {
+            const uint32_t a0 = cvt_lo(x23), a1 = cvt_hi(x23), a2 = cvt_lo(y23), a3 = cvt_hi(y23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * wd + 1], a0, a1, a2, a3, pb[hf][nt][0], pb[hf][nt][1]);
+          }
+        }
+      }
+    }
+    i += w.hi - w.lo;
+
+    // ---- join the warps ---------------------------------------------------------
+    join_sync();  // the last join's readers are done
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        const int row = nt * 8 + 2 * t + e;
+        if (g == 0) {
+          sh.pm[warp][row] = m[nt][e];
+          sh.pl[warp][row] = sum;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          *reinterpret_cast<float2*>(&sh.part[warp][row][g * KS * 2 + 2 * k]) = make_float2(o[nt][k][e], o[nt][k][e + 2]);
+      }
+    join_sync();
+    const int rows = min(kRows, w.r.rows - row0);
+    const bool whole = w.lo == 0 && w.hi == w.blocks;
+    constexpr int kQuads = D / 4;  // a thread handles 4 elements of a row at a time
+    float* slot = p.partial + static_cast<size_t>(2 * cta + (w.lo == 0 ? 1 : 0)) * (kRows * (D + 2));
+    for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
+      const int row = x / kQuads;
+      const int q4 = x - row * kQuads;
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, sh.pm[k][row]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kConsumers; ++k) {
+        const float f = ex2(sh.pm[k][row] - base);
+        const float4 v = *reinterpret_cast<const float4*>(&sh.part[k][row][4 * q4]);
+        sum += sh.pl[k][row] * f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+      }
+      if (whole) {
+        const int rr = row0 + row;
+        const int tok = rr / p.group;
+        const int h = w.head * p.group + (rr - tok * p.group);
+        const bool sees = seen0 + tok + 1 > 0;
+        const float inv = inverse_sum(sum, sees);
+        const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
+        const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
+        *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(w.r.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * q4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&ha), *reinterpret_cast<const uint32_t*>(&hb));
+        if (p.lse != nullptr && q4 == 0)
+          p.lse[static_cast<size_t>(w.r.t0 + tok) * p.q_heads + h] = sees ? kLn2 * base + logf(sum) : -INFINITY;
+      } else {
+        __stcg(reinterpret_cast<float4*>(slot + row * D) + q4, acc);
+        if (q4 == 0) {
+          __stcg(slot + kRows * D + row, top);
+          __stcg(slot + kRows * D + kRows + row, sum);
+        }
+      }
+    }
+    if (whole) continue;
+
+    // ---- the item crosses ranges: the last to arrive joins --------------------------
+    const long long item_u = w.u - w.lo;
+    const int c0 = range_of(units, item_u, ctas), c1 = range_of(units, item_u + w.blocks - 1, ctas);
+    __threadfence();
+    join_sync();
+    if (tid == 0) {
+      const uint32_t before_me = atomicAdd(p.arrived + c0, 1u);
+      sh.last = before_me == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
+      if (sh.last != 0u) p.arrived[c0] = 0u;
+    }
+    join_sync();
+    if (sh.last == 0u) continue;
+    __threadfence();
+    constexpr size_t kSlot = static_cast<size_t>(kRows) * (D + 2);
+    for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
+      const int row = x / kQuads;
+      const int q4 = x - row * kQuads;
+      float top = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = c0; k <= c1; ++k) {
+        const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
+        const float pm = __ldcg(s + kRows * D + row);
+        const float pl = __ldcg(s + kRows * D + kRows + row);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
+        const float up = fmaxf(top, pm);
+        const float base = up == -INFINITY ? 0.f : up;
+        const float fa = ex2(top - base), fb = ex2(pm - base);
+        top = up;
+        sum = sum * fa + pl * fb;
+        acc.x = acc.x * fa + v.x * fb;
+        acc.y = acc.y * fa + v.y * fb;
+        acc.z = acc.z * fa + v.z * fb;
+        acc.w = acc.w * fa + v.w * fb;
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      const int rr = row0 + row;
+      const int tok = rr / p.group;
+      const int h = w.head * p.group + (rr - tok * p.group);
+      const bool sees = seen0 + tok + 1 > 0;
+      const float inv = inverse_sum(sum, sees);
+      const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
+      const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
+      *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(w.r.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * q4) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&ha), *reinterpret_cast<const uint32_t*>(&hb));
+      if (p.lse != nullptr && q4 == 0)
+        p.lse[static_cast<size_t>(w.r.t0 + tok) * p.q_heads + h] = sees ? kLn2 * base + logf(sum) : -INFINITY;
+    }
+  }
+  if (!ok && lane == 0) {
+    atomicOr(&sh.abort, 1u);
+    atomicOr(p.status, 1u);
+  }
+}
+
+template <int D, int NT>
+exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  const size_t smem = sizeof(Shared<D, NT>);
+  if (cudaFuncSetAttribute(step_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return EXL3_ERR_CUDA;
+  int ctas = device_sm_count() * C::kCtasPerSm;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  step_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(p, kmap, vmap, 8);
+  return launch_status();
+}
+
+}  // namespace
+
+exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream) {
+  CUtensorMap km, vm;
+  exl3_status st;
+  const int rows = c.page_size < kUnit ? c.page_size : kUnit;
+  if ((st = cache_map(&km, c.k, c, rows)) != EXL3_OK || (st = cache_map(&vm, c.v, c, rows)) != EXL3_OK) return st;
+  if (c.head_dim == 64) return wide ? launch<64, 2>(p, km, vm, stream) : launch<64, 1>(p, km, vm, stream);
+  return wide ? launch<128, 2>(p, km, vm, stream) : launch<128, 1>(p, km, vm, stream);
+}
+
+}  // namespace attn
+}  // namespace exl3

@@ -46,6 +46,12 @@ inline exl3_status launch_status() {
 // Number of SMs of the current device (queried once per device).
 int device_sm_count();
 
+// The driver's tensor-map encoder (nullptr where no driver is installed).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
+
 // Workspace layout (all offsets 256-byte aligned):
 //   counters  one uint32 per 128-row block, then one status word (non-zero
 //             after a device-side wait of the tensor-core kernel timed out);
