@@ -1,85 +1,9 @@
 // exl3_attention: attention of each request's newest tokens over its paged 8-bit
 // cache.
-#include <math.h>
-
 #include "exl3_attn.cuh"
 
 namespace exl3 {
 namespace attn {
-namespace {
-
-constexpr int kWarps = 4;
-
-// One CTA per (token, head); its warps share the keys, each with an online
-// softmax of its own, joined at the end.  A lane holds D / 32 elements.
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) row_kernel(const AttnParams p, const exl3_kv_cache c) {
-  constexpr int E = D / 32;
-  const int t = blockIdx.x;
-  const int h = blockIdx.y;
-  const int lane = threadIdx.x & 31;
-  const int warp = threadIdx.x >> 5;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  if (t >= p.q_start[p.requests] || t < p.q_start[0]) return;
-  int lo = 0, hi = p.requests;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_start[mid] <= t) lo = mid; else hi = mid;
-  }
-  const int size = c.page_size;
-  const Req r = load_req(p, lo);
-  if (r.rows == 0) return;
-  const long long last = r.seq - (r.t0 + r.n - t);  // this row's own position
-  const int kvh = h / p.group;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __half2float(p.q[static_cast<size_t>(t) * p.q_stride + h * D + lane * E + e]);
-    o[e] = 0.f;
-  }
-  for (long long j = warp; j <= last; j += kWarps) {
-    const int page = p.table[static_cast<size_t>(lo) * p.table_stride + j / size];
-    const bool in = page >= 0 && page < c.pages;
-    const size_t block = in ? static_cast<size_t>(page) * c.kv_heads + kvh : 0;
-    const size_t at = (block * size + j % size) * D + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * static_cast<float>(c.k[at + e]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= in ? c.k_scale[block] * (p.c * kLn2) : 0.f;
-    const float vs = in ? c.v_scale[block] : 0.f;
-    const float top = fmaxf(m, s);
-    const float base = top == -INFINITY ? 0.f : top;
-    const float keep = expf(m - base);
-    const float w = expf(s - base);
-    m = top;
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * vs * static_cast<float>(c.v[at + e]);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  const float base = top == -INFINITY ? 0.f : top;
-  for (int w = 0; w < kWarps; ++w) sum += sl[w] * expf(sm[w] - base);
-  for (int i = threadIdx.x; i < D; i += 32 * kWarps) {
-    float v = 0.f;
-    for (int w = 0; w < kWarps; ++w) v += so[w][i] * expf(sm[w] - base);
-    p.out[static_cast<size_t>(t) * p.out_stride + h * D + i] = __float2half_rn(last >= 0 ? v / sum : 0.f);
-  }
-  if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[static_cast<size_t>(t) * p.q_heads + h] = last >= 0 ? base + logf(sum) : -INFINITY;
-}
-
-}  // namespace
-
 exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache& c, int rows) {
   const EncodeTiledFn encode = encode_tiled();
   if (encode == nullptr) return EXL3_ERR_CUDA;
@@ -103,7 +27,10 @@ using namespace exl3;
 extern "C" size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_new) {
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || max_new < 1)
     return 0;
-  return attn::arrived_bytes() + 2 * attn::kMaxCtas * attn::step_slot_floats(head_dim) * sizeof(float);
+  const size_t step = 2 * attn::kMaxCtas * attn::step_slot_floats(head_dim);
+  const size_t prompt = 2 * attn::kMaxPromptCtas * attn::prompt_slot_floats(head_dim);
+  const bool few = static_cast<long long>(max_new) * (q_heads / kv_heads) <= attn::kStepRows;
+  return attn::arrived_bytes() + (few || step > prompt ? step : prompt) * sizeof(float);
 }
 
 extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_half* q, long long q_stride, int q_heads,
@@ -162,10 +89,5 @@ extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_hal
   }
   p.rows_lo = requests > 1 ? attn::kStepRows + 1 : 1;
   p.rows_hi = 0x7FFFFFFF;
-  const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(q_heads));
-  if (cache->head_dim == 64)
-    attn::row_kernel<64><<<grid, 32 * attn::kWarps, 0, cs>>>(p, *cache);
-  else
-    attn::row_kernel<128><<<grid, 32 * attn::kWarps, 0, cs>>>(p, *cache);
-  return launch_status();
+  return attn::launch_prompt(p, *cache, cs);
 }

@@ -39,7 +39,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;     // log2 of the largest P
 constexpr float kTinyScale = -90.f;  // log2 that stands for a value scale of 0: its V add nothing, its P still count in l
-constexpr int kMaxCtas = 160 * 4; // ranges that the workspace holds partial results of
+constexpr int kMaxCtas = 160 * 4; // ranges that the workspace has counters for
 
 struct AttnParams {
   const __half* q;
@@ -57,7 +57,7 @@ struct AttnParams {
   long long most;          // keys that a table row holds
   int rows_lo, rows_hi;    // requests with rows in [rows_lo, rows_hi] are this launch's
   uint32_t* status;
-  uint32_t* arrived;       // [kMaxCtas], zero between calls: arrivals at the item that begins in CTA c and ends later
+  uint32_t* arrived;       // [kMaxCtas], zero between calls: arrivals at the item (or MMA tile of it) that begins in CTA c and ends later
   float* partial;          // [2 * kMaxCtas] slots: 2c the item that began before CTA c's range, 2c + 1 the one that ends after it
 };
 
@@ -148,6 +148,11 @@ constexpr size_t arrived_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas; }
 // Up to kStepRows query rows per key/value head (of more, tile by tile).
 constexpr int kStepRows = 16;
 constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kStepRows) * (head_dim + 2); }
+
+// More: tiles of 256 rows.
+constexpr int kMaxPromptCtas = 160;
+constexpr size_t prompt_slot_floats(int head_dim) { return static_cast<size_t>(256) * (head_dim + 2); }
+exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStream_t stream);
 exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream);
 
 }  // namespace attn
