@@ -52,6 +52,7 @@ struct AttnParams {
   float* lse;
   long long q_stride, out_stride;
   float c;                 // scale * log2(e)
+  int negate;              // prompt kernel: c is the absolute value, Q changes its sign
   int q_heads, kv_heads, group, requests, tokens;
   int table_stride, pages, page_shift;
   long long most;          // keys that a table row holds
@@ -97,17 +98,18 @@ struct PageScale {
   float iv; // 1 / 2^lv
 };
 
-__device__ __forceinline__ PageScale page_scale(const AttnParams& p, int page, int head) {
-  PageScale s{0.f, 0.f, 1.f};  // a page outside the pool reads as zeros
-  if (page >= 0 && page < p.pages) {
-    const size_t at = static_cast<size_t>(page) * p.kv_heads + head;
-    const float vs = __ldg(p.v_scale + at);
-    s.c = __ldg(p.k_scale + at) * p.c;
-    s.lv = vs == 0.f ? kTinyScale : log2f(vs);
-    // of the rounded logarithm, so that l and the sums agree; finite, so that it spoils no row whose P is 0
-    s.iv = vs != vs ? 1.f : exp2f(-s.lv);
-  }
+__device__ __forceinline__ PageScale page_scale(const AttnParams& p, float ks, float vs) {
+  PageScale s;
+  s.c = ks * p.c;
+  s.lv = vs == 0.f ? kTinyScale : log2f(vs);
+  // of the rounded logarithm, so that l and the sums agree; finite, so that it spoils no row whose P is 0
+  s.iv = vs != vs ? 1.f : exp2f(-s.lv);
   return s;
+}
+__device__ __forceinline__ PageScale page_scale(const AttnParams& p, int page, int head) {
+  if (page < 0 || page >= p.pages) return PageScale{0.f, 0.f, 1.f};  // a page outside the pool reads as zeros
+  const size_t at = static_cast<size_t>(page) * p.kv_heads + head;
+  return page_scale(p, __ldg(p.k_scale + at), __ldg(p.v_scale + at));
 }
 
 // Tensor copy of a box of tokens of one page and head: coordinates (0, token,

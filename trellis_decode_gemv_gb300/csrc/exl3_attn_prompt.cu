@@ -11,26 +11,27 @@
 // Tensor memory holds S/P and O of both tiles: 2 x (128 + D) columns.  While the
 // softmax warps of one tile work, the MMAs of the other run.
 //
-// Warp roles (13 warps):
+// Warp roles (16 warps):
 //   0-3, 4-7  softmax of tile A and B: a thread owns a row (its TMEM lane).  They
-//             also bring the item's Q into shared memory and take O out.  S is
-//             read twice (largest score, then P): 128 scores do not fit a
-//             thread's registers beside the rest.  O is only rescaled when a
-//             score passes the running maximum by 2^8, by these threads, between
-//             the MMAs that add to it.
-//   8-11      widening: int8 keys and values from global memory through registers
-//             (the next unit's loads are in flight meanwhile) into binary16
-//             operand images, two of K and two of V.  Both are [key][D] rows of
-//             64-element, 128-byte pieces in the 128-byte swizzle: K is read as a
-//             K-major operand, V as an MN-major one, so V needs no transposition.
+//             also take O out.  O is only rescaled when a score passes the running
+//             maximum by 2^8, by these threads, between the MMAs that add to it.
+//   8-11      widening: int8 tiles in shared memory into binary16 operand images,
+//             two of K and two of V.  Both are [key][D] rows of 64-element,
+//             128-byte pieces in the 128-byte swizzle: K is read as a K-major
+//             operand, V as an MN-major one, so V needs no transposition.
 //   12        MMA issue (one lane) and TMEM allocation.
-// Pages may be smaller than a unit: scales are kept per 16 keys.
+//   13        producer: page numbers and scales (three units ahead), tensor copies
+//             of the int8 tiles.  Pages may be smaller than a unit: one copy per
+//             page, scales per 16 keys.
+//   14, 15    Q of the next item (A, B) into shared memory as soon as the last
+//             scores of the current one are computed.
 //
-// Barriers: K and V images full/empty, scales full (four slots: a slot is
-// rewritten only after the softmax of both tiles has used it), Q full, S full and
-// P full per tile, O done per tile.  Every wait is bounded; on timeout the CTA
-// sets its abort flag and the status word, every role stops waiting, the MMA lane
-// waits (bounded) for its MMAs, TMEM is freed.
+// Barriers: int8 K and V tiles full/empty, K and V images full/empty, scales full
+// (four slots: a slot is rewritten only after the softmax of both tiles has used
+// it), per tile Q full/empty, S full, P full, product done, O done.  Every wait is
+// bounded; on timeout the CTA sets its abort flag and the status word, every role
+// stops waiting, the MMA lane waits (bounded) for its MMAs and the producer for its
+// copies, TMEM is freed.
 #include "exl3_attn.cuh"
 
 namespace exl3 {
@@ -48,7 +49,9 @@ constexpr int kGroups = kKeys / 16;    // scale groups of a unit
 constexpr int kConvWarp0 = 8;
 constexpr int kConvThreads = 128;
 constexpr int kMmaWarp = 12;
-constexpr int kThreads = 32 * 13;
+constexpr int kLoadWarp = 13;
+constexpr int kQWarp0 = 14;
+constexpr int kThreads = 32 * 16;
 constexpr int kTmemCols = 512;
 constexpr int kTileBarrier = 1;        // + tile
 constexpr int kScaleSlots = 4;
@@ -58,14 +61,16 @@ struct Cfg {
   static constexpr int kPieces = D / 64;               // 64-element pieces of a row
   static constexpr int kPieceBytes = 128 * 128;        // 128 rows of one piece
   static constexpr int kImageBytes = kPieces * kPieceBytes;
-  static constexpr int kSmem = kImageBytes * 6 + 1024; // Q A, Q B, K x 2, V x 2; alignment
+  static constexpr int kByteTile = kKeys * D;
+  static constexpr int kSmem = kImageBytes * 6 + 2 * kByteTile + 1024; // Q A, Q B, K x 2, V x 2; int8 K, V; alignment
   static constexpr int kOCol = 2 * kKeys;
 };
 
 struct Control {
+  uint64_t b_full[2], b_empty[2];   // int8 tiles of K, V
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t c_full[kScaleSlots];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_done[2], mma_done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_done[2], mma_done;
   float4 scale[kScaleSlots][kGroups];
   long long warp_sum[kThreads / 32];
   long long units;
@@ -75,10 +80,11 @@ struct Control {
 
 __device__ __forceinline__ bool aborted(const Control& c) { return *reinterpret_cast<const volatile uint32_t*>(&c.abort) != 0u; }
 
-// A wait of a whole warp; false (for every lane) when it ran out or the CTA has given up.
+// A wait of a whole warp; false (for every lane) when it ran out: the CTA gives
+// up.  (That another role gave up is not looked at here: what waits for it runs
+// out in its turn, once per role.)
 __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_wait(bar, parity) && !aborted(c);
-  if (__all_sync(0xFFFFFFFFu, ok)) return true;
+  if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity))) return true;
   atomicOr(&c.abort, 1u);
   return false;
 }
@@ -105,17 +111,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[smem desc] x B[smem desc], kind::f16.
@@ -126,6 +121,24 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// One lane of a converged warp, in a form that the compiler knows to be one lane:
+// MMAs issued under `lane == 0` took 73 clocks each, not 64 (128 x 128 x 16, idle
+// SM; over 100 beside busy warps).
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0u;
+}
+
+// 16 bytes global -> shared without registers; zeros if not `valid`.
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 
 // Descriptor of an operand in the 128-byte swizzle: 8-row groups of 1024 bytes
@@ -152,22 +165,22 @@ __device__ __forceinline__ int tile_units(const AttnParams& p, const Req& r, int
 // another.
 struct Walker {
   const AttnParams& p;
-  long long u, end;
+  int left;   // units of the range from the current item's first on
   int b, rt, head, lo, hi, units;
   Req r;
-  __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, long long u0, long long u1)
-      : p(params), u(u0), end(u1), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo) {
+  __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, int count)
+      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo) {
     r = load_req(p, b);
     place();
   }
   __device__ __forceinline__ void place() {
     units = tile_units(p, r, rt);
-    hi = static_cast<int>(min(static_cast<long long>(units), lo + (end - u)));
+    hi = min(units, lo + left);
   }
-  __device__ __forceinline__ bool more() const { return u < end; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next() {
-    u += hi - lo;
-    if (u >= end) return;
+    left -= hi - lo;
+    if (left <= 0) return;
     lo = 0;
     if (++head == p.kv_heads) {
       head = 0;
@@ -207,7 +220,7 @@ __device__ __forceinline__ long long block_scan(Control& c, long long v, long lo
 
 // `first` [requests]: row tiles before each request (room borrowed from the operand images).
 __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, int32_t* first, int min_units, int& ctas,
-                                           long long& u0, long long& u1) {
+                                           int& count) {
   const int tid = threadIdx.x;
   const int per = (p.requests + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
@@ -241,8 +254,8 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, int3
   ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (units + min_units - 1) / min_units));
   const int cta = blockIdx.x;
   if (cta >= ctas) return false;
-  u0 = range_begin(units, cta, ctas);
-  u1 = range_begin(units, cta + 1, ctas);
+  const long long u0 = range_begin(units, cta, ctas);
+  count = static_cast<int>(range_begin(units, cta + 1, ctas) - u0);
   if (before <= u0 && u0 < before + sum) {
     int b = lo;
     Req r = load_req(p, b);
@@ -267,46 +280,149 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, int3
 
 // ---- widening ------------------------------------------------------------------------
 
-// The 16-byte pieces of a unit's K or V that a thread widens: piece `tid % (D/16)`
-// of the rows tid / (D/16) + i * (128 / (D/16)).
+// A unit's int8 tile (as the tensor copy swizzles it) into an operand image; a
+// thread widens piece tid % (D/16) of the rows tid / (D/16) + i * (128 / (D/16)).
 template <int D>
-struct Conv {
-  static constexpr int kChunks = D / 16;
-  static constexpr int kRowStep = kConvThreads / kChunks;
-  static constexpr int kLoads = 128 / kRowStep;
+__device__ __forceinline__ void widen(const unsigned char* tile, uint32_t image, int tid) {
+  constexpr int kChunks = D / 16;
+  constexpr int kRowStep = kConvThreads / kChunks;   // a multiple of 8: the swizzle is the same for all rows of a thread
+  const int c = tid % kChunks;
+  const int row = tid / kChunks;
+  // the lanes of a row's second piece store their halves in the other order: no bank twice
+  const int swap = D == 128 ? c >> 2 : 0;
+  const unsigned char* src = tile + row * D + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) * 16);
+  const uint32_t at = image + static_cast<uint32_t>((c >> 2) * Cfg<D>::kPieceBytes + row * 128);
+  const uint32_t first = at + static_cast<uint32_t>((2 * (c & 3) + swap) ^ (row & 7)) * 16;
+  const uint32_t second = at + static_cast<uint32_t>((2 * (c & 3) + 1 - swap) ^ (row & 7)) * 16;
+#pragma unroll 4
+  for (int i = 0; i < 128 / kRowStep; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + i * kRowStep * D);
+    const uint32_t x = v.x ^ 0x80808080u, y = v.y ^ 0x80808080u, z = v.z ^ 0x80808080u, w = v.w ^ 0x80808080u;
+    st_shared_v4((swap ? second : first) + i * kRowStep * 128, cvt_lo(x), cvt_hi(x), cvt_lo(y), cvt_hi(y));
+    st_shared_v4((swap ? first : second) + i * kRowStep * 128, cvt_lo(z), cvt_hi(z), cvt_lo(w), cvt_hi(w));
+  }
+}
 
-  // From the pages of the unit: lane l % 8 of every warp holds the byte offset of group l's first key, -1: zeros.
-  static __device__ __forceinline__ void load(const int8_t* base, long long group_at, int tid, uint4 (&v)[kLoads]) {
-    const int c = tid % kChunks;
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Largest of 16 scores.
+__device__ __forceinline__ float max16(const uint32_t* a) {
+  float m[4];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = tid / kChunks + i * kRowStep;
-      const long long at = __shfl_sync(0xFFFFFFFFu, group_at, row >> 4);
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (at >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(base + at + (row & 15) * D + c * 16));
+  for (int i = 0; i < 4; ++i)
+    m[i] = fmaxf(fmaxf(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1])),
+                 fmaxf(__uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3])));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// A row's 128 scores: the running maximum m (O and l rescaled when it moves), P in
+// place of the scores, l.  `left`: the keys of the unit that the row sees, looked
+// at only where the unit needs a mask.
+template <int D, bool MASK>
+__device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const float4* sc, int left, bool first, float& m,
+                                             float& l, uint64_t* p_full) {
+  // S is read twice, a chunk ahead of its use: 128 scores do not fit beside the rest
+  uint32_t a[2][32];
+  float top = -INFINITY;   // largest x = c ks s + log2 vs (c ks >= 0)
+  tmem_ld32(s_at, a[0]);
+#pragma unroll
+  for (int ch = 0; ch < kKeys / 32; ++ch) {
+    tmem_ld_wait();
+    tmem_ld32(s_at + 32 * ((ch + 1) % (kKeys / 32)), a[(ch + 1) & 1]);   // the last: chunk 0 again
+    uint32_t(&v)[32] = a[ch & 1];
+    if constexpr (MASK) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (32 * ch + e >= left) v[e] = 0xFF800000u;
+    }
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      const float4 f = sc[2 * ch + gr];
+      const float best = max16(v + 16 * gr);
+      const float x = fmaf(best, f.x, f.y);
+      top = fmaxf(top, MASK && best == -INFINITY ? -INFINITY : x);  // a scale of 0 would make NaN of it
     }
   }
-  static __device__ __forceinline__ void store(uint32_t image, int tid, const uint4 (&v)[kLoads]) {
-    const int c = tid % kChunks;
-    // the lanes of a row's second piece store their halves in the other order: no bank twice
-    const int swap = D == 128 ? c >> 2 : 0;
+  if (first) {
+    m = top;
+  } else {
+    const bool over = top > m + kSlack;
+    if (__any_sync(0xFFFFFFFFu, over)) {
+      const float keep = over ? ex2(m - top) : 1.f;
+      if (over) m = top;
+      l *= keep;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 16; ++ch) {
+        float o[16];
+        tc::tmem_ld16(o_at + 16 * ch, o);   // waits for the chunk of S too
+        uint32_t b[16];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = tid / kChunks + i * kRowStep;
-      const uint32_t x = v[i].x ^ 0x80808080u, y = v[i].y ^ 0x80808080u, z = v[i].z ^ 0x80808080u, w = v[i].w ^ 0x80808080u;
-      const uint32_t h[8] = {cvt_lo(x), cvt_hi(x), cvt_lo(y), cvt_hi(y), cvt_lo(z), cvt_hi(z), cvt_lo(w), cvt_hi(w)};
-      const uint32_t at = image + static_cast<uint32_t>((c >> 2) * Cfg<D>::kPieceBytes + row * 128);
-      const uint32_t first = static_cast<uint32_t>((2 * (c & 3) + swap) ^ (row & 7)) * 16;
-      const uint32_t second = static_cast<uint32_t>((2 * (c & 3) + 1 - swap) ^ (row & 7)) * 16;
-      st_shared_v4(at + first, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-      st_shared_v4(at + second, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+        for (int e = 0; e < 16; ++e) b[e] = __float_as_uint(o[e] * keep);
+        tc::tmem_st16(o_at + 16 * ch, b);
+      }
     }
   }
-};
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+  for (int ch = 0; ch < kKeys / 32; ++ch) {
+    if (ch > 0) tmem_ld32(s_at + 32 * ch, a[0]);
+    tmem_ld_wait();
+    const uint32_t(&v)[32] = a[0];
+    uint32_t pk[16];
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      const float4 f = sc[2 * ch + gr];
+      const float lv = f.y - base;
+      const uint64_t ff = pair(f.x, f.x), lvlv = pair(lv, lv);
+      uint64_t sum = 0;   // two zeros
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float p0, p1;
+        unpair(fma2(pair(__uint_as_float(v[16 * gr + e]), __uint_as_float(v[16 * gr + e + 1])), ff, lvlv), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        if constexpr (MASK) {
+          if (32 * ch + 16 * gr + e >= left) p0 = 0.f;
+          if (32 * ch + 16 * gr + e + 1 >= left) p1 = 0.f;
+        }
+        sum = add2(sum, pair(p0, p1));
+        const __half2 q = __floats2half2_rn(p0, p1);
+        pk[8 * gr + e / 2] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      float s0, s1;
+      unpair(sum, s0, s1);
+      l = fmaf(s0 + s1, f.z, l);
+    }
+    tc::tmem_st16(s_at + 16 * ch, pk);
+    if (ch & 1) {   // half of the keys: their product may begin
+      tc::tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(p_full + (ch >> 1));
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_kernel(const AttnParams p, const int8_t* __restrict__ kbase, const int8_t* __restrict__ vbase, int min_units) {
+    prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  int min_units) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_dyn[];
   __shared__ Control ctl;
@@ -316,165 +432,264 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = tid >> 5;
   const int cta = blockIdx.x;
   const uint32_t images = smem_u32(smem_raw);   // Q A, Q B, K 0, K 1, V 0, V 1
+  unsigned char* bytes = smem_raw + 6 * C::kImageBytes;   // int8 K, V
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.b_full[i], 1);
+      mbar_init(&ctl.b_empty[i], kConvThreads / 32);
       mbar_init(&ctl.k_full[i], kConvThreads / 32);
       mbar_init(&ctl.v_full[i], kConvThreads / 32);
       mbar_init(&ctl.k_empty[i], 1);
       mbar_init(&ctl.v_empty[i], 1);
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i], kTile / 32);
+      mbar_init(&ctl.p_full[i][0], kTile / 32);
+      mbar_init(&ctl.p_full[i][1], kTile / 32);
       mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.o_done[i], 1);
-      mbar_init(&ctl.q_full[i], kTile / 32);
+      mbar_init(&ctl.q_full[i], 1);
+      mbar_init(&ctl.q_empty[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&ctl.c_full[i], 1);
     mbar_init(&ctl.mma_done, 1);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  int ctas;
-  long long u0, u1;
-  if (!find_range(p, ctl, reinterpret_cast<int32_t*>(smem_raw), min_units, ctas, u0, u1)) return;
+  int ctas, count;
+  if (!find_range(p, ctl, reinterpret_cast<int32_t*>(smem_raw), min_units, ctas, count)) return;
   if (warp == kMmaWarp) tc::tmem_alloc(&ctl.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  Walker w(p, ctl, u0, u1);
+  Walker w(p, ctl, count);
 
   if (warp == kMmaWarp) {
     // ---- MMA issue ---------------------------------------------------------------------
+    // Before the first unit, and after the product of unit u - 1, the scores of unit
+    // u are issued.  The code is kept small (nothing is unrolled but the MMAs of one
+    // product): this warp's instruction fetches are on the critical path.
     constexpr uint32_t kIdescS = idesc(kKeys, false), kIdescO = idesc(D, true);
-    uint32_t n = 0;               // units of the range so far
-    uint32_t used[2] = {0, 0};    // units of tile A, B so far
-    uint32_t items[2] = {0, 0};   // items of tile A, B so far
-    uint32_t pv[2] = {0, 0};      // waits on pv_done
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint64_t q_desc = swizzled_desc(images, 16, 1024);
+    const uint64_t k_desc = swizzled_desc(images + 2 * C::kImageBytes, 16, 1024);
+    const uint64_t v_desc = swizzled_desc(images + 4 * C::kImageBytes, C::kPieceBytes, 1024);
+    uint32_t used = 0;        // bit x: parity of the products of tile x so far
+    uint32_t begun = 0;       // bit x: parity of the items of tile x so far
+    int now = 0, next = w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;  // tiles of unit u - 1, of unit u
+    int blk = w.lo;           // unit u in its item
+    bool first = false, last = true;   // unit u - 1 begins, ends its item
     bool ok = true;
-    auto scores = [&](uint32_t unit, int x) {
-      if (lane == 0) {
-        const uint64_t a = swizzled_desc(images + static_cast<uint32_t>(x) * C::kImageBytes, 16, 1024);
-        const uint64_t b = swizzled_desc(images + (2 + (unit & 1)) * C::kImageBytes, 16, 1024);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = static_cast<uint32_t>((k >> 2) * C::kPieceBytes + (k & 3) * 32) >> 4;
-          mma_ss(tmem + static_cast<uint32_t>(x * kKeys), a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
-        }
-        mma_commit(&ctl.s_full[x]);
-      }
-      __syncwarp();
-    };
-    for (; w.more() && ok; w.next()) {
-      const int tiles = w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;
-      const int steps = w.hi - w.lo;
-      for (int x = 0; x < tiles && ok; ++x) ok = warp_wait(ctl, &ctl.q_full[x], items[x]++ & 1);
-      ok = ok && warp_wait(ctl, &ctl.k_full[n & 1], (n >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      for (int x = 0; x < tiles; ++x) scores(n, x);
-      if (lane == 0) mma_commit(&ctl.k_empty[n & 1]);
-      for (int j = 0; j < steps && ok; ++j) {
-        const uint32_t unit = n + static_cast<uint32_t>(j);
-        const bool more = j + 1 < steps;
-        for (int x = 0; x < tiles; ++x) {
-          if (x == 0) ok = warp_wait(ctl, &ctl.v_full[unit & 1], (unit >> 1) & 1);
-          ok = ok && warp_wait(ctl, &ctl.p_full[x], used[x] & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t b = swizzled_desc(images + (4 + (unit & 1)) * C::kImageBytes, C::kPieceBytes, 1024);
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              tc::mma_f16_ts(tmem + static_cast<uint32_t>(C::kOCol + x * D), tmem + static_cast<uint32_t>(x * kKeys + 8 * k),
-                             b + static_cast<uint32_t>((k * 2048) >> 4), kIdescO, j > 0 || k > 0 ? 1u : 0u);
-            if (x == tiles - 1) mma_commit(&ctl.v_empty[unit & 1]);
-            mma_commit(more ? &ctl.pv_done[x] : &ctl.o_done[x]);
-          }
-          __syncwarp();
-          if (more) {
-            // the next scores go where P is: its product has to be complete
-            if (x == 0) ok = warp_wait(ctl, &ctl.k_full[(unit + 1) & 1], ((unit + 1) >> 1) & 1);
-            ok = ok && warp_wait(ctl, &ctl.pv_done[x], pv[x] & 1);
+#pragma unroll 1
+    for (uint32_t u = 0; u <= static_cast<uint32_t>(count) && ok; ++u) {
+      const uint32_t slot = u & 1, prev = slot ^ 1;
+#pragma unroll 1
+      for (int x = 0; x < 2 && ok; ++x) {
+        const uint32_t s_col = tm + static_cast<uint32_t>(x * kKeys);
+        if (x < now) {
+          ok = x > 0 || warp_wait(ctl, &ctl.v_full[prev], ((u - 1) >> 1) & 1);
+#pragma unroll 1
+          for (int h = 0; h < 2 && ok; ++h) {   // half of the keys
+            ok = warp_wait(ctl, &ctl.p_full[x][h], (used >> x) & 1);
             if (!ok) break;
-            ++pv[x];
             tc_fence_after();
-            scores(unit + 1, x);
-            if (x == tiles - 1 && lane == 0) mma_commit(&ctl.k_empty[(unit + 1) & 1]);
+            if (elect()) {
+              const uint64_t b = v_desc + ((prev * C::kImageBytes + h * 64 * 128) >> 4);
+#pragma unroll
+              for (int k = 0; k < kKeys / 32; ++k)
+                tc::mma_f16_ts(tm + static_cast<uint32_t>(C::kOCol + x * D), s_col + 32 * h + 8 * k, b + ((k * 2048) >> 4), kIdescO,
+                               !first || h > 0 || k > 0 ? 1u : 0u);
+              if (h > 0) {
+                if (last) mma_commit(&ctl.o_done[x]);
+                mma_commit(&ctl.pv_done[x]);
+              }
+            }
             __syncwarp();
           }
-          ++used[x];
+          if (!ok) break;
+        }
+        if (x < next) {
+          ok = x > 0 || warp_wait(ctl, &ctl.k_full[slot], (u >> 1) & 1);
+          if (last) {
+            ok = ok && warp_wait(ctl, &ctl.q_full[x], (begun >> x) & 1);
+            begun ^= 1u << x;
+          }
+        }
+        // the next scores go where P is: its product has to be complete
+        if (x < now) {
+          ok = ok && warp_wait(ctl, &ctl.pv_done[x], (used >> x) & 1);
+          used ^= 1u << x;
+        }
+        if (x < next && ok) {
+          tc_fence_after();
+          if (elect()) {
+            const uint64_t a = q_desc + static_cast<uint32_t>((x * C::kImageBytes) >> 4);
+            const uint64_t b = k_desc + ((slot * C::kImageBytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = static_cast<uint32_t>((k >> 2) * C::kPieceBytes + (k & 3) * 32) >> 4;
+              mma_ss(s_col, a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
+            }
+            mma_commit(&ctl.s_full[x]);
+            if (blk + 1 == w.hi) mma_commit(&ctl.q_empty[x]);
+          }
+          __syncwarp();
         }
       }
-      n += static_cast<uint32_t>(steps);
+      if (!ok) break;
+      if (elect()) {
+        if (u > 0) mma_commit(&ctl.v_empty[prev]);
+        if (next > 0) mma_commit(&ctl.k_empty[slot]);
+      }
+      __syncwarp();
+      now = next;
+      first = blk == w.lo;
+      last = ++blk == w.hi;
+      if (last) {
+        w.next();
+        blk = w.lo;
+        next = !w.more() ? 0 : w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;
+      }
     }
-    if (lane == 0) mma_commit(&ctl.mma_done);
+    if (elect()) mma_commit(&ctl.mma_done);
     __syncwarp();
     mbar_wait(&ctl.mma_done, 0);
-  } else if (warp >= kConvWarp0) {
-    // ---- widening ----------------------------------------------------------------------
-    using V = Conv<D>;
-    const int ct = tid - 32 * kConvWarp0;
+  } else if (warp == kLoadWarp) {
+    // ---- producer ----------------------------------------------------------------------
+    // lanes 0-7: the 16-key groups of the unit two ahead of the one being copied
     const int key16 = (lane & 7) * 16;
-    // three units deep: page numbers, then offsets and scales, then the bytes
-    bool live = w.more();
+    bool live = true;
     int blk = w.lo;
-    int page = -1, head = 0, token = 0;  // of the cursor's unit, this lane's 16 keys
-    auto look_up = [&]() {
-      page = -1;
-      head = 0;
+    struct Look {
+      int page, head, keys;   // page number as the table has it; the request's keys from this unit's first on
+    };
+    auto look_up = [&]() -> Look {
+      Look k{-1, 0, 0};
       if (live) {
         const int key = blk * kKeys + key16;
-        head = w.head;
-        if (key < w.r.seq) page = __ldg(p.table + static_cast<size_t>(w.b) * p.table_stride + (key >> p.page_shift));
-        if (page >= p.pages) page = -1;
-        // a page number outside the pool reads as zeros, as does what lies past the request
-        if (page >= 0) token = key & ((1 << p.page_shift) - 1);
+        k.head = w.head;
+        k.keys = w.r.seq - blk * kKeys;
+        if (key < w.r.seq) k.page = __ldg(p.table + static_cast<size_t>(w.b) * p.table_stride + (key >> p.page_shift));
         if (++blk == w.hi) {
           w.next();
           live = w.more();
           blk = w.lo;
         }
       }
+      return k;
     };
-    auto offset = [&]() -> long long {
-      return page < 0 ? -1LL : (((static_cast<long long>(page) * p.kv_heads + head) << p.page_shift) + token) * D;
+    struct Scales {
+      float k, v;
     };
-    const uint32_t count = static_cast<uint32_t>(u1 - u0);
-    uint4 kr[V::kLoads], vr[V::kLoads];
-    look_up();
-    long long at = offset();
-    PageScale sc = page_scale(p, page, head);
-    V::load(kbase, at, ct, kr);
-    V::load(vbase, at, ct, vr);
-    look_up();
-    long long at1 = offset();
-    PageScale sc1 = page_scale(p, page, head);
-    look_up();
-    for (uint32_t n = 0; n < count; ++n) {
-      const int slot = n & 1;
-      const uint32_t before = ((n >> 1) - 1) & 1;
-      if (n >= 2 && !warp_wait(ctl, &ctl.k_empty[slot], before)) break;
-      if (warp == kConvWarp0) {
-        if (lane < kGroups) ctl.scale[n % kScaleSlots][lane] = make_float4(sc.c, sc.lv, sc.iv, 0.f);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.c_full[n % kScaleSlots]);
+    auto scales_of = [&](const Look& k) -> Scales {
+      Scales s{0.f, 1.f};   // a page number outside the pool reads as zeros
+      if (k.page >= 0 && k.page < p.pages) {
+        const size_t at = static_cast<size_t>(k.page) * p.kv_heads + k.head;
+        s.k = __ldg(p.k_scale + at);
+        s.v = __ldg(p.v_scale + at);
       }
-      V::store(images + (2 + slot) * C::kImageBytes, ct, kr);
+      return s;
+    };
+    const int per_page = 1 << p.page_shift;
+    const int step = per_page >> 4;              // groups per copy
+    const int copies = kKeys >> p.page_shift;    // pages of a unit
+    const uint32_t copy_bytes = static_cast<uint32_t>(per_page * D);
+    Look l0 = look_up(), l1 = look_up();
+    Scales s0 = scales_of(l0);
+    uint32_t n = 0;
+    for (; n < static_cast<uint32_t>(count); ++n) {
+      const Look l2 = look_up();
+      const Scales s1 = scales_of(l1);
+      // the int8 tile of K is free: so is the scale slot (the unit four before is done)
+      if (n > 0 && !warp_wait(ctl, &ctl.b_empty[0], (n - 1) & 1)) break;
+      if (lane < kGroups) {
+        const PageScale ps = page_scale(p, s0.k, s0.v);
+        ctl.scale[n % kScaleSlots][lane] = make_float4(ps.c, ps.lv, ps.iv, 0.f);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.c_full[n % kScaleSlots]);
+      // one copy per page that holds keys of the request; what is not copied is
+      // whatever was there (finite, and its P are 0)
+      const int owner = lane * step;   // lane i < copies issues copy i
+      const int pg = __shfl_sync(0xFFFFFFFFu, l0.page, owner & 7);
+      const bool mine = lane < copies && lane * per_page < l0.keys;
+      const int block = pg >= 0 && pg < p.pages ? pg * p.kv_heads + l0.head : p.pages * p.kv_heads;
+      const uint32_t total = static_cast<uint32_t>(__popc(__ballot_sync(0xFFFFFFFFu, mine))) * copy_bytes;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.b_full[0], total);
+      __syncwarp();
+      if (mine) tensor_g2s(bytes + lane * copy_bytes, &kmap, 0, block, &ctl.b_full[0]);
+      if (n > 0 && !warp_wait(ctl, &ctl.b_empty[1], (n - 1) & 1)) {
+        ++n;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.b_full[1], total);
+      __syncwarp();
+      if (mine) tensor_g2s(bytes + C::kByteTile + lane * copy_bytes, &vmap, 0, block, &ctl.b_full[1]);
+      l0 = l1;
+      l1 = l2;
+      s0 = s1;
+    }
+    // Wait (bounded) for the copies in flight.
+    if (n > 0) {
+      mbar_wait(&ctl.b_full[0], (n - 1) & 1);
+      mbar_wait(&ctl.b_full[1], (n - 1) & 1);
+    }
+  } else if (warp >= kQWarp0) {
+    // ---- Q ---------------------------------------------------------------------------
+    const int x = warp - kQWarp0;
+    uint32_t items = 0;
+    for (; w.more(); w.next()) {
+      const int row0 = w.rt * kItemRows + x * kTile;
+      const int rows = w.r.rows - row0;
+      if (rows <= 0) continue;
+      if (items > 0 && !warp_wait(ctl, &ctl.q_empty[x], (items - 1) & 1)) break;
+      ++items;
+      constexpr int kChunks = D / 8;            // 16-byte pieces of a row
+      constexpr int kRowsAtOnce = 32 / kChunks; // 2 or 4
+      const int c = lane % kChunks;
+      const uint32_t image = images + static_cast<uint32_t>(x) * C::kImageBytes + static_cast<uint32_t>((c >> 3) * C::kPieceBytes);
+#pragma unroll 4
+      for (int r = lane / kChunks; r < kTile; r += kRowsAtOnce) {
+        const bool in = r < rows;
+        const int rr = in ? row0 + r : row0;
+        const int tok = rr / p.group;
+        async_copy16(image + static_cast<uint32_t>(r * 128 + (((c & 7) ^ (r & 7)) * 16)),
+                     p.q + static_cast<size_t>(w.r.t0 + tok) * p.q_stride +
+                         static_cast<size_t>(w.head * p.group + (rr - tok * p.group)) * D + c * 8,
+                     in);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (p.negate)
+        for (int r = lane / kChunks; r < kTile; r += kRowsAtOnce) {
+          uint4* at = reinterpret_cast<uint4*>(smem_raw + (image - images) + r * 128 + (((c & 7) ^ (r & 7)) * 16));
+          const uint4 v = *at;
+          *at = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+        }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.k_full[slot]);
-      V::load(kbase, at1, ct, kr);
-      if (n >= 2 && !warp_wait(ctl, &ctl.v_empty[slot], before)) break;
-      V::store(images + (4 + slot) * C::kImageBytes, ct, vr);
+      if (lane == 0) mbar_arrive(&ctl.q_full[x]);
+    }
+  } else if (warp >= kConvWarp0) {
+    // ---- widening ----------------------------------------------------------------------
+    const int ct = tid - 32 * kConvWarp0;
+    for (uint32_t n = 0; n < static_cast<uint32_t>(count); ++n) {
+      const uint32_t slot = n & 1, before = ((n >> 1) - 1) & 1;
+      if (!warp_wait(ctl, &ctl.b_full[0], n & 1) || (n >= 2 && !warp_wait(ctl, &ctl.k_empty[slot], before))) break;
+      widen<D>(bytes, images + (2 + slot) * C::kImageBytes, ct);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.v_full[slot]);
-      V::load(vbase, at1, ct, vr);
-      sc = sc1;
-      at1 = offset();
-      sc1 = page_scale(p, page, head);
-      look_up();
+      if (lane == 0) {
+        mbar_arrive(&ctl.k_full[slot]);
+        mbar_arrive(&ctl.b_empty[0]);
+      }
+      if (!warp_wait(ctl, &ctl.b_full[1], n & 1) || (n >= 2 && !warp_wait(ctl, &ctl.v_empty[slot], before))) break;
+      widen<D>(bytes + C::kByteTile, images + (4 + slot) * C::kImageBytes, ct);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.v_full[slot]);
+        mbar_arrive(&ctl.b_empty[1]);
+      }
     }
   } else {
     // ---- softmax -----------------------------------------------------------------------
@@ -496,22 +711,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = rr / p.group;
       const int h = w.head * p.group + (rr - tok * p.group);
       const bool mine = r < rows;
-      {  // this row of Q
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(w.r.t0 + tok) * p.q_stride + static_cast<size_t>(h) * D);
-        const uint32_t dst = images + static_cast<uint32_t>(x) * C::kImageBytes + static_cast<uint32_t>(r * 128);
-#pragma unroll
-        for (int half = 0; half < C::kPieces; ++half) {
-          uint4 v[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = mine ? src[half * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_shared_v4(dst + static_cast<uint32_t>(half * C::kPieceBytes + ((c ^ (r & 7)) * 16)), v[c].x, v[c].y, v[c].z, v[c].w);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.q_full[x]);
-      }
       const int lim = w.r.seq - w.r.n + tok + 1;            // keys that this row sees
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
@@ -525,78 +724,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key0 = (w.lo + j) * kKeys;
           const bool mask = key0 + kKeys > lim_min;
           const int left = lim - key0;     // keys of this unit that the row sees
-          uint32_t a[32];
-          // largest x = c ks s + log2 vs
-          float top = -INFINITY;
-#pragma unroll
-          for (int ch = 0; ch < kKeys / 32; ++ch) {
-            tmem_ld32(s_at + 32 * ch, a);
-            tmem_ld_wait();
-#pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-              const float4 f = sc[2 * ch + gr];
-              if (mask) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (32 * ch + 16 * gr + e < left) top = fmaxf(top, fmaf(__uint_as_float(a[16 * gr + e]), f.x, f.y));
-              } else {
-                float best = __uint_as_float(a[16 * gr]) * f.x;
-#pragma unroll
-                for (int e = 1; e < 16; ++e) best = fmaxf(best, __uint_as_float(a[16 * gr + e]) * f.x);
-                top = fmaxf(top, best + f.y);
-              }
-            }
-          }
-          if (j == 0) {
-            m = top;
-          } else {
-            const bool over = top > m + kSlack;
-            if (__any_sync(0xFFFFFFFFu, over)) {
-              const float keep = over ? ex2(m - top) : 1.f;
-              if (over) m = top;
-              l *= keep;
-#pragma unroll
-              for (int ch = 0; ch < D / 32; ++ch) {
-                tmem_ld32(o_at + 32 * ch, a);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * keep);
-                tmem_st32(o_at + 32 * ch, a);
-              }
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int ch = 0; ch < kKeys / 32; ++ch) {
-            tmem_ld32(s_at + 32 * ch, a);
-            tmem_ld_wait();
-            uint32_t pk[16];
-#pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-              const float4 f = sc[2 * ch + gr];
-              const float lv = f.y - base;
-              float sum = 0.f;
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float p0 = ex2(fmaf(__uint_as_float(a[16 * gr + e]), f.x, lv));
-                float p1 = ex2(fmaf(__uint_as_float(a[16 * gr + e + 1]), f.x, lv));
-                if (mask) {
-                  if (32 * ch + 16 * gr + e >= left) p0 = 0.f;
-                  if (32 * ch + 16 * gr + e + 1 >= left) p1 = 0.f;
-                }
-                sum += p0 + p1;
-                const __half2 q = __floats2half2_rn(p0, p1);
-                pk[8 * gr + e / 2] = *reinterpret_cast<const uint32_t*>(&q);
-              }
-              l = fmaf(sum, f.z, l);
-            }
-            tc::tmem_st16(s_at + 16 * ch, pk);
-          }
-          tc::tmem_st_wait();
-          tc_fence_before();
+          if (mask)
+            softmax_unit<D, true>(s_at, o_at, sc, left, j == 0, m, l, ctl.p_full[x]);
+          else
+            softmax_unit<D, false>(s_at, o_at, sc, left, j == 0, m, l, ctl.p_full[x]);
+        } else if (lane == 0) {
+          mbar_arrive(&ctl.p_full[x][0]);
+          mbar_arrive(&ctl.p_full[x][1]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[x]);
       }
       // ---- the item's sums: finished, or to be joined ---------------------------------
       ok = ok && warp_wait(ctl, &ctl.o_done[x], items & 1);
@@ -645,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __stcg(slot + static_cast<size_t>(D) * kTile + r, m);
       __stcg(slot + static_cast<size_t>(D + 1) * kTile + r, l);
-      const long long item_u = w.u - w.lo;
+      const long long item_u = range_begin(ctl.units, cta, ctas) + (count - w.left) - w.lo;
       const int c0 = range_of(ctl.units, item_u, ctas), c1 = range_of(ctl.units, item_u + w.units - 1, ctas);
       __threadfence();
       tile_sync(x);
@@ -710,19 +845,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-exl3_status launch(const AttnParams& p, const exl3_kv_cache& c, cudaStream_t stream) {
+exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
     return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
-  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, c.k, c.v, 2);
+  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, kmap, vmap, 2);
   return launch_status();
 }
 
 }  // namespace
 
 exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStream_t stream) {
-  return c.head_dim == 64 ? launch<64>(p, c, stream) : launch<128>(p, c, stream);
+  CUtensorMap km, vm;
+  exl3_status st;
+  if ((st = cache_map(&km, c.k, c, c.page_size)) != EXL3_OK || (st = cache_map(&vm, c.v, c, c.page_size)) != EXL3_OK) return st;
+  AttnParams q = p;
+  q.negate = p.c < 0.f;
+  q.c = fabsf(p.c);
+  return c.head_dim == 64 ? launch<64>(q, km, vm, stream) : launch<128>(q, km, vm, stream);
 }
 
 }  // namespace attn
