@@ -73,7 +73,8 @@ struct Control {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_done[2], mma_done;
   float4 scale[kScaleSlots][kGroups];
   long long warp_sum[kThreads / 32];
-  long long units;
+  long long units, bounds[2];
+  Req first_req;
   int first_b, first_tile, first_head, first_lo;
   uint32_t tmem_base, abort, last[2];
 };
@@ -153,12 +154,11 @@ constexpr uint32_t idesc(int n, bool transposed) {
   return (1u << 4) | (transposed ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
-__device__ __forceinline__ int row_tiles(const Req& r) { return (r.rows + kItemRows - 1) / kItemRows; }
+__device__ __forceinline__ int row_tiles(int rows) { return (rows + kItemRows - 1) / kItemRows; }
 // Units of row tile `rt`: up to the last key that its last row sees, at least one.
-__device__ __forceinline__ int tile_units(const AttnParams& p, const Req& r, int rt) {
-  const int last = (min((rt + 1) * kItemRows, r.rows) - 1) / p.group;
-  const int end = r.seq - r.n + last + 1;
-  return max(1, (end + kKeys - 1) / kKeys);
+__device__ __forceinline__ int tile_units(const AttnParams& p, int n, int seq, int rt) {
+  const int last = (min((rt + 1) * kItemRows, n * p.group) - 1) / p.group;
+  return max(1, (seq - n + last + kKeys) / kKeys);
 }
 
 // The items of a range: row tiles in order, the heads of a row tile after one
@@ -169,29 +169,30 @@ struct Walker {
   int b, rt, head, lo, hi, units;
   Req r;
   __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, int count)
-      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo) {
-    r = load_req(p, b);
-    place();
-  }
-  __device__ __forceinline__ void place() {
-    units = tile_units(p, r, rt);
+      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
+    units = tile_units(p, r.n, r.seq, rt);
+    if (lo == units) advance();
     hi = min(units, lo + left);
   }
-  __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ void next() {
-    left -= hi - lo;
-    if (left <= 0) return;
+  __device__ __forceinline__ void advance() {
     lo = 0;
     if (++head == p.kv_heads) {
       head = 0;
-      if (++rt == row_tiles(r)) {
+      if (++rt == row_tiles(r.rows)) {
         rt = 0;
         do {
           r = load_req(p, ++b);
         } while (r.rows == 0 && b < p.requests);
       }
+      units = tile_units(p, r.n, r.seq, rt);
     }
-    place();
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next() {
+    left -= hi - lo;
+    if (left <= 0) return;
+    advance();
+    hi = min(units, lo + left);
   }
 };
 
@@ -218,64 +219,86 @@ __device__ __forceinline__ long long block_scan(Control& c, long long v, long lo
   return before + inc - v;
 }
 
-// `first` [requests]: row tiles before each request (room borrowed from the operand images).
-__device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, int32_t* first, int min_units, int& ctas,
-                                           int& count) {
+// An item of at most kWhole units is not split: leaving and joining partial
+// results takes as long as about six units.  A boundary between ranges that falls
+// into such an item moves to its nearer end.
+constexpr int kWhole = 12;
+constexpr int kLeast = 6;   // units that are worth a range of their own
+
+// `room`: 12 bytes for each request (borrowed from the operand images).  False: the
+// CTA has nothing to do.
+__device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void* room, int& ctas, int& count) {
   const int tid = threadIdx.x;
+  int32_t* first = static_cast<int32_t*>(room);    // row tiles before each request
+  int2* req = reinterpret_cast<int2*>(first + ((p.requests + 1) & ~1));  // its new tokens (0: another launch's) and length
   const int per = (p.requests + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
   long long mine = 0, tiles;
-  for (int b = b0; b < b1; ++b) mine += row_tiles(load_req(p, b));
+  for (int b = b0; b < b1; ++b) {
+    const Req r = load_req(p, b);
+    req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq);
+    mine += row_tiles(r.rows);
+  }
   long long at = block_scan(c, mine, tiles);
   for (int b = b0; b < b1; ++b) {
     first[b] = static_cast<int32_t>(at);
-    at += row_tiles(load_req(p, b));
+    at += row_tiles(req[b].x * p.group);
   }
   __syncthreads();
   const int n = static_cast<int>(tiles);
   const int share = (n + kThreads - 1) / kThreads;
   const int x0 = min(tid * share, n), x1 = min(x0 + share, n);
-  int lo = 0, hi = p.requests;   // the last request that begins at or before x0
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= x0) lo = mid; else hi = mid;
+  int from = 0, to = p.requests;   // the last request that begins at or before x0
+  while (to - from > 1) {
+    const int mid = (from + to) >> 1;
+    if (first[mid] <= x0) from = mid; else to = mid;
   }
-  long long sum = 0;
-  {
-    int b = lo;
-    Req r = load_req(p, b);
-    for (int x = x0; x < x1; ++x) {
-      while (x - first[b] >= row_tiles(r)) r = load_req(p, ++b);
-      sum += static_cast<long long>(tile_units(p, r, x - first[b])) * p.kv_heads;
-    }
+  long long sum = 0, ranges = 0;
+  for (int x = x0, b = from; x < x1; ++x) {
+    while (b + 1 < p.requests && first[b + 1] <= x) ++b;
+    const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
+    sum += static_cast<long long>(len) * p.kv_heads;
+    ranges += static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads;
   }
-  long long units;
+  long long units, all_ranges;
   long long before = block_scan(c, sum, units);
-  ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (units + min_units - 1) / min_units));
+  block_scan(c, ranges, all_ranges);
+  ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all_ranges));
   const int cta = blockIdx.x;
   if (cta >= ctas) return false;
-  const long long u0 = range_begin(units, cta, ctas);
-  count = static_cast<int>(range_begin(units, cta + 1, ctas) - u0);
-  if (before <= u0 && u0 < before + sum) {
-    int b = lo;
-    Req r = load_req(p, b);
-    for (int x = x0; x < x1; ++x) {
-      while (x - first[b] >= row_tiles(r)) r = load_req(p, ++b);
-      const int len = tile_units(p, r, x - first[b]);
+  long long u[2] = {range_begin(units, cta, ctas), range_begin(units, cta + 1, ctas)};
+  if (tid == 0) {
+    c.units = units;
+    c.bounds[1] = units;   // the last range's end is in no item
+  }
+  __syncthreads();
+  if (before < units && u[1] >= before && u[0] < before + sum) {
+    for (int x = x0, b = from; x < x1; ++x) {
+      while (b + 1 < p.requests && first[b + 1] <= x) ++b;
+      const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
       const long long all = static_cast<long long>(len) * p.kv_heads;
-      if (u0 < before + all) {
-        c.first_b = b;
-        c.first_tile = x - first[b];
-        c.first_head = static_cast<int>((u0 - before) / len);
-        c.first_lo = static_cast<int>((u0 - before) - static_cast<long long>(c.first_head) * len);
-        c.units = units;
-        break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (u[e] < before || u[e] >= before + all) continue;
+        const int head = static_cast<int>((u[e] - before) / len);
+        const long long start = before + static_cast<long long>(head) * len;
+        int lo = static_cast<int>(u[e] - start);
+        if (len <= kWhole) lo = 2 * lo < len ? 0 : len;
+        c.bounds[e] = start + lo;
+        if (e == 0) {
+          c.first_b = b;
+          c.first_tile = x - first[b];
+          c.first_head = head;
+          c.first_lo = lo;
+          c.first_req = load_req(p, b);
+        }
       }
       before += all;
     }
   }
   __syncthreads();
-  return true;
+  count = static_cast<int>(c.bounds[1] - c.bounds[0]);
+  return count > 0;
 }
 
 // ---- widening ------------------------------------------------------------------------
@@ -421,8 +444,7 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  int min_units) {
+    prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_dyn[];
   __shared__ Control ctl;
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   int ctas, count;
-  if (!find_range(p, ctl, reinterpret_cast<int32_t*>(smem_raw), min_units, ctas, count)) return;
+  if (!find_range(p, ctl, smem_raw, ctas, count)) return;
   if (warp == kMmaWarp) tc::tmem_alloc(&ctl.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -600,26 +622,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; n < static_cast<uint32_t>(count); ++n) {
       const Look l2 = look_up();
       const Scales s1 = scales_of(l1);
-      // the int8 tile of K is free: so is the scale slot (the unit four before is done)
+      // one copy per page that holds keys of the request; what is not copied is
+      // whatever was there (finite, and its P are 0)
+      const int pg = __shfl_sync(0xFFFFFFFFu, l0.page, (lane * step) & 7);   // lane i < copies issues copy i
+      const bool mine = lane < copies && lane * per_page < l0.keys;
+      const int block = pg >= 0 && pg < p.pages ? pg * p.kv_heads + l0.head : p.pages * p.kv_heads;
+      const uint32_t total = static_cast<uint32_t>(__popc(__ballot_sync(0xFFFFFFFFu, mine))) * copy_bytes;
       if (n > 0 && !warp_wait(ctl, &ctl.b_empty[0], (n - 1) & 1)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.b_full[0], total);
+      __syncwarp();
+      if (mine) tensor_g2s(bytes + lane * copy_bytes, &kmap, 0, block, &ctl.b_full[0]);
+      // the unit four before is done (its K image has been written over): the slot is free
       if (lane < kGroups) {
         const PageScale ps = page_scale(p, s0.k, s0.v);
         ctl.scale[n % kScaleSlots][lane] = make_float4(ps.c, ps.lv, ps.iv, 0.f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.c_full[n % kScaleSlots]);
-      // one copy per page that holds keys of the request; what is not copied is
-      // whatever was there (finite, and its P are 0)
-      const int owner = lane * step;   // lane i < copies issues copy i
-      const int pg = __shfl_sync(0xFFFFFFFFu, l0.page, owner & 7);
-      const bool mine = lane < copies && lane * per_page < l0.keys;
-      const int block = pg >= 0 && pg < p.pages ? pg * p.kv_heads + l0.head : p.pages * p.kv_heads;
-      const uint32_t total = static_cast<uint32_t>(__popc(__ballot_sync(0xFFFFFFFFu, mine))) * copy_bytes;
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.b_full[0], total);
-      __syncwarp();
-      if (mine) tensor_g2s(bytes + lane * copy_bytes, &kmap, 0, block, &ctl.b_full[0]);
       if (n > 0 && !warp_wait(ctl, &ctl.b_empty[1], (n - 1) & 1)) {
-        ++n;
+        mbar_wait(&ctl.b_full[0], n & 1);
         break;
       }
       if (lane == 0) mbar_arrive_expect_tx(&ctl.b_full[1], total);
@@ -648,15 +669,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kRowsAtOnce = 32 / kChunks; // 2 or 4
       const int c = lane % kChunks;
       const uint32_t image = images + static_cast<uint32_t>(x) * C::kImageBytes + static_cast<uint32_t>((c >> 3) * C::kPieceBytes);
+      int tok = (row0 + lane / kChunks) / p.group;
+      int hd = row0 + lane / kChunks - tok * p.group;
+      const __half* base = p.q + static_cast<size_t>(w.r.t0) * p.q_stride + static_cast<size_t>(w.head) * p.group * D + c * 8;
 #pragma unroll 4
       for (int r = lane / kChunks; r < kTile; r += kRowsAtOnce) {
         const bool in = r < rows;
-        const int rr = in ? row0 + r : row0;
-        const int tok = rr / p.group;
-        async_copy16(image + static_cast<uint32_t>(r * 128 + (((c & 7) ^ (r & 7)) * 16)),
-                     p.q + static_cast<size_t>(w.r.t0 + tok) * p.q_stride +
-                         static_cast<size_t>(w.head * p.group + (rr - tok * p.group)) * D + c * 8,
-                     in);
+        const __half* src = base + static_cast<size_t>(tok) * p.q_stride + static_cast<size_t>(hd) * D;
+        async_copy16(image + static_cast<uint32_t>(r * 128 + (((c & 7) ^ (r & 7)) * 16)), in ? src : p.q, in);
+        hd += kRowsAtOnce;
+        while (hd >= p.group) {
+          hd -= p.group;
+          ++tok;
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (p.negate)
@@ -780,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __stcg(slot + static_cast<size_t>(D) * kTile + r, m);
       __stcg(slot + static_cast<size_t>(D + 1) * kTile + r, l);
-      const long long item_u = range_begin(ctl.units, cta, ctas) + (count - w.left) - w.lo;
+      const long long item_u = ctl.bounds[0] + (count - w.left) - w.lo;
       const int c0 = range_of(ctl.units, item_u, ctas), c1 = range_of(ctl.units, item_u + w.units - 1, ctas);
       __threadfence();
       tile_sync(x);
@@ -796,38 +821,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       auto part = [&](int k) { return p.partial + (static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * 2 + x) * kTileFloats; };
       float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
       for (int k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part(k) + static_cast<size_t>(D) * kTile + r));
       const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
       for (int k = c0; k <= c1; ++k)
         sum += __ldcg(part(k) + static_cast<size_t>(D + 1) * kTile + r) * ex2(__ldcg(part(k) + static_cast<size_t>(D) * kTile + r) - base);
       const float scale = inverse_sum(sum, sees);
 #pragma unroll 1
-      for (int ch = 0; ch < D / 16; ++ch) {
-        float4 acc[4];
+      for (int ch = 0; ch < D / 32; ++ch) {
+        float4 acc[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
         for (int k = c0; k <= c1; ++k) {
           const float* q = part(k);
+          float4 v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(8 * ch + e) * kTile + r);
           const float f = ex2(__ldcg(q + static_cast<size_t>(D) * kTile + r) - base);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(4 * ch + e) * kTile + r);
-            acc[e].x = fmaf(v.x, f, acc[e].x);
-            acc[e].y = fmaf(v.y, f, acc[e].y);
-            acc[e].z = fmaf(v.z, f, acc[e].z);
-            acc[e].w = fmaf(v.w, f, acc[e].w);
+          for (int e = 0; e < 8; ++e) {
+            acc[e].x = fmaf(v[e].x, f, acc[e].x);
+            acc[e].y = fmaf(v[e].y, f, acc[e].y);
+            acc[e].z = fmaf(v[e].z, f, acc[e].z);
+            acc[e].w = fmaf(v[e].w, f, acc[e].w);
           }
         }
-        uint32_t pk[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 q0 = __floats2half2_rn(sees ? acc[e].x * scale : 0.f, sees ? acc[e].y * scale : 0.f);
-          const __half2 q1 = __floats2half2_rn(sees ? acc[e].z * scale : 0.f, sees ? acc[e].w * scale : 0.f);
-          pk[2 * e] = *reinterpret_cast<const uint32_t*>(&q0);
-          pk[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&q1);
+        for (int e = 0; e < 8; e += 2) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 q0 = __floats2half2_rn(sees ? acc[e + i].x * scale : 0.f, sees ? acc[e + i].y * scale : 0.f);
+            const __half2 q1 = __floats2half2_rn(sees ? acc[e + i].z * scale : 0.f, sees ? acc[e + i].w * scale : 0.f);
+            pk[2 * i] = *reinterpret_cast<const uint32_t*>(&q0);
+            pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q1);
+          }
+          *reinterpret_cast<uint4*>(dst + 32 * ch + 4 * e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        *reinterpret_cast<uint4*>(dst + 16 * ch) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(dst + 16 * ch + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
       }
       if (lse != nullptr) *lse = sees ? kLn2 * base + logf(sum) : -INFINITY;
       }
@@ -850,7 +882,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
     return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
-  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, kmap, vmap, 2);
+  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, kmap, vmap);
   return launch_status();
 }
 
