@@ -4,6 +4,7 @@
 
 namespace exl3 {
 namespace attn {
+
 exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache& c, int rows) {
   const EncodeTiledFn encode = encode_tiled();
   if (encode == nullptr) return EXL3_ERR_CUDA;
@@ -16,6 +17,20 @@ exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache&
                             CU_TENSOR_MAP_INTERLEAVE_NONE,
                             c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EXL3_OK : EXL3_ERR_CUDA;
+}
+
+exl3_status query_map(CUtensorMap* map, const AttnParams& p, int head_dim, int tokens) {
+  const EncodeTiledFn encode = encode_tiled();
+  if (encode == nullptr) return EXL3_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(p.q_heads),
+                              static_cast<cuuint64_t>(p.tokens)};
+  const cuuint64_t strides[2] = {2ull * head_dim, 2ull * p.q_stride};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p.q), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? EXL3_OK : EXL3_ERR_CUDA;
 }
 

@@ -52,6 +52,7 @@ struct AttnParams {
   float* lse;
   long long q_stride, out_stride;
   float c;                 // scale * log2(e)
+  int q_box;               // prompt kernel: Q comes by tensor copies of whole tokens
   int negate;              // prompt kernel: c is the absolute value, Q changes its sign
   int q_heads, kv_heads, group, requests, tokens;
   int table_stride, pages, page_shift;
@@ -112,14 +113,18 @@ __device__ __forceinline__ PageScale page_scale(const AttnParams& p, int page, i
   return page_scale(p, __ldg(p.k_scale + at), __ldg(p.v_scale + at));
 }
 
-// Tensor copy of a box of tokens of one page and head: coordinates (0, token,
-// page * kv_heads + head).
-__device__ __forceinline__ void tensor_g2s(void* dst, const CUtensorMap* map, int token, int block, uint64_t* bar) {
+__device__ __forceinline__ void tensor_g2s_at(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           smem_u32(dst)),
-      "l"(map), "r"(0), "r"(token), "r"(block), "r"(smem_u32(bar))
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Tensor copy of a box of tokens of one page and head: coordinates (0, token,
+// page * kv_heads + head).
+__device__ __forceinline__ void tensor_g2s(void* dst, const CUtensorMap* map, int token, int block, uint64_t* bar) {
+  tensor_g2s_at(dst, map, 0, token, block, bar);
 }
 
 // Exact binary16 of the int8 in bytes 0, 1 (resp. 2, 3) of x, whose top bits are
@@ -143,6 +148,10 @@ __device__ __forceinline__ int range_of(long long units, long long u, int ctas) 
 // The keys or values as [pages * kv_heads][page_size][head_dim] bytes, boxes of
 // `rows` tokens, 16-byte pieces swizzled.
 exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache& c, int rows);
+
+// Q as [tokens][q_heads][head_dim], boxes of `tokens` tokens x a group's heads x 64
+// elements in the 128-byte swizzle.
+exl3_status query_map(CUtensorMap* map, const AttnParams& p, int head_dim, int tokens);
 
 // The status word and the arrival counters come first in the workspace.
 constexpr size_t arrived_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas; }

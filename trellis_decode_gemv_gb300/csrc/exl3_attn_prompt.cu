@@ -73,7 +73,7 @@ struct Control {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_done[2], mma_done;
   float4 scale[kScaleSlots][kGroups];
   long long warp_sum[kThreads / 32];
-  long long units, bounds[2];
+  long long cost, bounds[2], first_cost;
   Req first_req;
   int first_b, first_tile, first_head, first_lo;
   uint32_t tmem_base, abort, last[2];
@@ -161,21 +161,32 @@ __device__ __forceinline__ int tile_units(const AttnParams& p, int n, int seq, i
   return max(1, (seq - n + last + kKeys) / kKeys);
 }
 
+// An item of at most kWhole units is not split: leaving and joining partial
+// results takes as long as about six units.  A boundary between ranges that falls
+// into such an item moves to its nearer end.
+constexpr int kWhole = 12;
+constexpr int kLeast = 6;   // units that are worth a range of their own
+// Ranges are cut in equal parts of units plus kItemCost for each item: beginning and
+// ending one (Q, the first scores, the output) takes about as long as that.
+constexpr int kItemCost = 2;
+
 // The items of a range: row tiles in order, the heads of a row tile after one
 // another.
 struct Walker {
   const AttnParams& p;
-  int left;   // units of the range from the current item's first on
+  int left;        // units of the range from the current item's first on
+  long long cost;  // of all items before this one
   int b, rt, head, lo, hi, units;
   Req r;
   __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, int count)
-      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
+      : p(params), left(count), cost(c.first_cost), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
     units = tile_units(p, r.n, r.seq, rt);
     if (lo == units) advance();
     hi = min(units, lo + left);
   }
   __device__ __forceinline__ void advance() {
     lo = 0;
+    cost += units + kItemCost;
     if (++head == p.kv_heads) {
       head = 0;
       if (++rt == row_tiles(r.rows)) {
@@ -219,12 +230,6 @@ __device__ __forceinline__ long long block_scan(Control& c, long long v, long lo
   return before + inc - v;
 }
 
-// An item of at most kWhole units is not split: leaving and joining partial
-// results takes as long as about six units.  A boundary between ranges that falls
-// into such an item moves to its nearer end.
-constexpr int kWhole = 12;
-constexpr int kLeast = 6;   // units that are worth a range of their own
-
 // `room`: 12 bytes for each request (borrowed from the operand images).  False: the
 // CTA has nothing to do.
 __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void* room, int& ctas, int& count) {
@@ -253,39 +258,45 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
     const int mid = (from + to) >> 1;
     if (first[mid] <= x0) from = mid; else to = mid;
   }
-  long long sum = 0, ranges = 0;
+  long long sum = 0, real = 0, ranges = 0;   // cost, units, ranges that this thread's tiles are worth
   for (int x = x0, b = from; x < x1; ++x) {
     while (b + 1 < p.requests && first[b + 1] <= x) ++b;
     const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
-    sum += static_cast<long long>(len) * p.kv_heads;
+    sum += static_cast<long long>(len + kItemCost) * p.kv_heads;
+    real += static_cast<long long>(len) * p.kv_heads;
     ranges += static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads;
   }
-  long long units, all_ranges;
-  long long before = block_scan(c, sum, units);
+  long long cost, units, all_ranges;
+  long long before = block_scan(c, sum, cost);
+  long long before_units = block_scan(c, real, units);
   block_scan(c, ranges, all_ranges);
   ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all_ranges));
   const int cta = blockIdx.x;
   if (cta >= ctas) return false;
-  long long u[2] = {range_begin(units, cta, ctas), range_begin(units, cta + 1, ctas)};
+  const long long u[2] = {range_begin(cost, cta, ctas), range_begin(cost, cta + 1, ctas)};
   if (tid == 0) {
-    c.units = units;
+    c.cost = cost;
     c.bounds[1] = units;   // the last range's end is in no item
   }
   __syncthreads();
-  if (before < units && u[1] >= before && u[0] < before + sum) {
+  if (before < cost && u[1] >= before && u[0] < before + sum) {
     for (int x = x0, b = from; x < x1; ++x) {
       while (b + 1 < p.requests && first[b + 1] <= x) ++b;
       const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
-      const long long all = static_cast<long long>(len) * p.kv_heads;
+      const long long all = static_cast<long long>(len + kItemCost) * p.kv_heads;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (u[e] < before || u[e] >= before + all) continue;
-        const int head = static_cast<int>((u[e] - before) / len);
-        const long long start = before + static_cast<long long>(head) * len;
+        const int head = static_cast<int>((u[e] - before) / (len + kItemCost));
+        const long long start = before + static_cast<long long>(head) * (len + kItemCost);
         int lo = static_cast<int>(u[e] - start);
-        if (len <= kWhole) lo = 2 * lo < len ? 0 : len;
-        c.bounds[e] = start + lo;
+        if (len <= kWhole)
+          lo = 2 * lo < len + kItemCost ? 0 : len;
+        else
+          lo = max(0, lo - kItemCost);
+        c.bounds[e] = before_units + static_cast<long long>(head) * len + lo;
         if (e == 0) {
+          c.first_cost = start;
           c.first_b = b;
           c.first_tile = x - first[b];
           c.first_head = head;
@@ -294,6 +305,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
         }
       }
       before += all;
+      before_units += static_cast<long long>(len) * p.kv_heads;
     }
   }
   __syncthreads();
@@ -444,7 +456,8 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap qmap) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_dyn[];
   __shared__ Control ctl;
@@ -665,6 +678,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rows <= 0) continue;
       if (items > 0 && !warp_wait(ctl, &ctl.q_empty[x], (items - 1) & 1)) break;
       ++items;
+      if (p.q_box != 0) {
+        // whole tokens: the tile's rows as one box of (128 / group) tokens x group heads per 64-element piece
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl.q_full[x], C::kImageBytes);
+#pragma unroll
+          for (int pc = 0; pc < C::kPieces; ++pc)
+            tensor_g2s_at(smem_raw + x * C::kImageBytes + pc * C::kPieceBytes, &qmap, 64 * pc, w.head * p.group,
+                          w.r.t0 + row0 / p.group, &ctl.q_full[x]);
+        }
+        __syncwarp();
+        continue;
+      }
       constexpr int kChunks = D / 8;            // 16-byte pieces of a row
       constexpr int kRowsAtOnce = 32 / kChunks; // 2 or 4
       const int c = lane % kChunks;
@@ -694,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.q_full[x]);
     }
+    if (p.q_box != 0 && items > 0) mbar_wait(&ctl.q_full[x], (items - 1) & 1);  // its last copy
   } else if (warp >= kConvWarp0) {
     // ---- widening ----------------------------------------------------------------------
     const int ct = tid - 32 * kConvWarp0;
@@ -805,8 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __stcg(slot + static_cast<size_t>(D) * kTile + r, m);
       __stcg(slot + static_cast<size_t>(D + 1) * kTile + r, l);
-      const long long item_u = ctl.bounds[0] + (count - w.left) - w.lo;
-      const int c0 = range_of(ctl.units, item_u, ctas), c1 = range_of(ctl.units, item_u + w.units - 1, ctas);
+      const int c0 = range_of(ctl.cost, w.cost + kItemCost, ctas), c1 = range_of(ctl.cost, w.cost + kItemCost + w.units - 1, ctas);
       __threadfence();
       tile_sync(x);
       if (r == 0) {
@@ -877,12 +902,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
+                   cudaStream_t stream) {
   if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
     return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
-  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, kmap, vmap);
+  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, kmap, vmap, qmap);
   return launch_status();
 }
 
@@ -895,7 +921,12 @@ exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStrea
   AttnParams q = p;
   q.negate = p.c < 0.f;
   q.c = fabsf(p.c);
-  return c.head_dim == 64 ? launch<64>(q, km, vm, stream) : launch<128>(q, km, vm, stream);
+  // a tile of whole tokens can be copied as one box; the other groups (and a
+  // negative scale) take the rows one by one (8 K clocks, the box 2 K)
+  q.q_box = kTile % p.group == 0 && !q.negate ? 1 : 0;
+  CUtensorMap qm = km;
+  if (q.q_box != 0 && (st = query_map(&qm, p, c.head_dim, kTile / p.group)) != EXL3_OK) return st;
+  return c.head_dim == 64 ? launch<64>(q, km, vm, qm, stream) : launch<128>(q, km, vm, qm, stream);
 }
 
 }  // namespace attn
