@@ -11,19 +11,21 @@
 // Tensor memory holds S/P and O of both tiles: 2 x (128 + D) columns.  While the
 // softmax warps of one tile work, the MMAs of the other run.
 //
-// Warp roles (16 warps):
-//   0-3, 4-7  softmax of tile A and B: a thread owns a row (its TMEM lane).  They
-//             also take O out.  O is only rescaled when a score passes the running
-//             maximum by 2^8, by these threads, between the MMAs that add to it.
-//   8-11      widening: int8 tiles in shared memory into binary16 operand images,
+// Warp roles (24 warps):
+//   0-7, 8-15 softmax of tile A and B: two threads share a row (its TMEM lane), one
+//             for each 64 keys of a unit and each half of O's columns; their warps
+//             exchange the row's largest score.  They also take O out.  O is only
+//             rescaled when a score passes the running maximum by 2^8, by these
+//             threads, between the MMAs that add to it.
+//   16-19     widening: int8 tiles in shared memory into binary16 operand images,
 //             two of K and two of V.  Both are [key][D] rows of 64-element,
 //             128-byte pieces in the 128-byte swizzle: K is read as a K-major
 //             operand, V as an MN-major one, so V needs no transposition.
-//   12        MMA issue (one lane) and TMEM allocation.
-//   13        producer: page numbers and scales (three units ahead), tensor copies
+//   20        MMA issue (one lane) and TMEM allocation.
+//   21        producer: page numbers and scales (three units ahead), tensor copies
 //             of the int8 tiles.  Pages may be smaller than a unit: one copy per
 //             page, scales per 16 keys.
-//   14, 15    Q of the next item (A, B) into shared memory as soon as the last
+//   22, 23    Q of the next item (A, B) into shared memory as soon as the last
 //             scores of the current one are computed.
 //
 // Barriers: int8 K and V tiles full/empty, K and V images full/empty, scales full
@@ -46,14 +48,17 @@ constexpr int kTile = 128;             // rows of an MMA tile
 constexpr int kItemRows = 2 * kTile;
 constexpr int kKeys = 128;             // keys of a unit
 constexpr int kGroups = kKeys / 16;    // scale groups of a unit
-constexpr int kConvWarp0 = 8;
+constexpr int kMmaWarp = 0;
+constexpr int kLoadWarp = 1;
+constexpr int kQWarp0 = 2;
+constexpr int kSoftmaxWarp0 = 4;
+constexpr int kConvWarp0 = 20;
 constexpr int kConvThreads = 128;
-constexpr int kMmaWarp = 12;
-constexpr int kLoadWarp = 13;
-constexpr int kQWarp0 = 14;
-constexpr int kThreads = 32 * 16;
+constexpr int kThreads = 32 * 24;
 constexpr int kTmemCols = 512;
-constexpr int kTileBarrier = 1;        // + tile
+constexpr int kTileBarrier = 1;        // + tile: its 256 softmax threads
+constexpr int kPairBarrier = 3;        // + 4 * tile + quarter: the two warps of 32 rows
+constexpr int kHalf = kKeys / 2;       // keys of a softmax thread
 constexpr int kScaleSlots = 4;
 
 template <int D>
@@ -62,7 +67,7 @@ struct Cfg {
   static constexpr int kPieceBytes = 128 * 128;        // 128 rows of one piece
   static constexpr int kImageBytes = kPieces * kPieceBytes;
   static constexpr int kByteTile = kKeys * D;
-  static constexpr int kSmem = kImageBytes * 6 + 2 * kByteTile + 1024; // Q A, Q B, K x 2, V x 2; int8 K, V; alignment
+  static constexpr int kTiles = kImageBytes * 6 + 2 * kByteTile; // Q A, Q B, K x 2, V x 2; int8 K, V
   static constexpr int kOCol = 2 * kKeys;
 };
 
@@ -72,8 +77,10 @@ struct Control {
   uint64_t c_full[kScaleSlots];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_done[2], mma_done;
   float4 scale[kScaleSlots][kGroups];
-  long long warp_sum[kThreads / 32];
-  long long cost, bounds[2], first_cost;
+  alignas(8) float top[2][2][kTile];          // per tile and half of the keys: a row's largest score; at an item's end its sum
+  long long bounds[2];
+  // ranges over which an item is spread: the one that began before this range, the one that ends after it
+  int spread0[2], spread1[2];
   Req first_req;
   int first_b, first_tile, first_head, first_lo;
   uint32_t tmem_base, abort, last[2];
@@ -91,13 +98,23 @@ __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t pa
 }
 
 __device__ __forceinline__ void tile_sync(int tile) {
-  asm volatile("bar.sync %0, %1;" ::"r"(kTileBarrier + tile), "n"(kTile) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(kTileBarrier + tile), "n"(2 * kTile) : "memory");
 }
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(kPairBarrier + id), "n"(64) : "memory"); }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -137,6 +154,24 @@ __device__ __forceinline__ bool elect() {
   return r != 0u;
 }
 
+// A wait that polls without suspending the thread (a suspended one took 200 to 400
+// clocks to come back), for the one thread that feeds the tensor pipe.
+__device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  for (uint32_t it = 0; it < 16u * tc::kSpinLimit; ++it) {   // a second or so
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
 // 16 bytes global -> shared without registers; zeros if not `valid`.
 __device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -174,19 +209,17 @@ constexpr int kItemCost = 2;
 // another.
 struct Walker {
   const AttnParams& p;
-  int left;        // units of the range from the current item's first on
-  long long cost;  // of all items before this one
+  int left;   // units of the range from the current item's first on
   int b, rt, head, lo, hi, units;
   Req r;
   __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, int count)
-      : p(params), left(count), cost(c.first_cost), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
+      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
     units = tile_units(p, r.n, r.seq, rt);
     if (lo == units) advance();
     hi = min(units, lo + left);
   }
   __device__ __forceinline__ void advance() {
     lo = 0;
-    cost += units + kItemCost;
     if (++head == p.kv_heads) {
       head = 0;
       if (++rt == row_tiles(r.rows)) {
@@ -210,6 +243,7 @@ struct Walker {
 // ---- prelude: units of all items, and where this CTA's range begins -----------------
 
 __device__ __forceinline__ long long block_scan(Control& c, long long v, long long& total) {
+  long long* warp_sum = reinterpret_cast<long long*>(c.top);   // not in use yet
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   long long inc = v;
@@ -218,13 +252,13 @@ __device__ __forceinline__ long long block_scan(Control& c, long long v, long lo
     const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
     if (lane >= d) inc += o;
   }
-  if (lane == 31) c.warp_sum[warp] = inc;
+  if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
   long long before = 0;
   total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    before += w < warp ? c.warp_sum[w] : 0;
-    total += c.warp_sum[w];
+    before += w < warp ? warp_sum[w] : 0;
+    total += warp_sum[w];
   }
   __syncthreads();
   return before + inc - v;
@@ -275,7 +309,6 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   if (cta >= ctas) return false;
   const long long u[2] = {range_begin(cost, cta, ctas), range_begin(cost, cta + 1, ctas)};
   if (tid == 0) {
-    c.cost = cost;
     c.bounds[1] = units;   // the last range's end is in no item
   }
   __syncthreads();
@@ -295,8 +328,9 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
         else
           lo = max(0, lo - kItemCost);
         c.bounds[e] = before_units + static_cast<long long>(head) * len + lo;
+        c.spread0[e] = range_of(cost, start + kItemCost, ctas);
+        c.spread1[e] = range_of(cost, start + kItemCost + len - 1, ctas);
         if (e == 0) {
-          c.first_cost = start;
           c.first_b = b;
           c.first_tile = x - first[b];
           c.first_head = head;
@@ -315,26 +349,32 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
 
 // ---- widening ------------------------------------------------------------------------
 
-// A unit's int8 tile (as the tensor copy swizzles it) into an operand image; a
-// thread widens piece tid % (D/16) of the rows tid / (D/16) + i * (128 / (D/16)).
+// A unit's int8 tile (as the tensor copy swizzles it) into an operand image.  A
+// warp takes 8 rows x 64 elements at a time: lane (k, b, c) piece c of row k, or of
+// row k ^ 5 for b = 1.  The eight lanes of a shared-memory phase then hold two rows
+// whose swizzles differ in bits 0 and 2, and neither the 16-byte loads nor the two
+// 16-byte stores touch a bank twice.
 template <int D>
 __device__ __forceinline__ void widen(const unsigned char* tile, uint32_t image, int tid) {
-  constexpr int kChunks = D / 16;
-  constexpr int kRowStep = kConvThreads / kChunks;   // a multiple of 8: the swizzle is the same for all rows of a thread
-  const int c = tid % kChunks;
-  const int row = tid / kChunks;
-  // the lanes of a row's second piece store their halves in the other order: no bank twice
-  const int swap = D == 128 ? c >> 2 : 0;
-  const unsigned char* src = tile + row * D + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) * 16);
-  const uint32_t at = image + static_cast<uint32_t>((c >> 2) * Cfg<D>::kPieceBytes + row * 128);
-  const uint32_t first = at + static_cast<uint32_t>((2 * (c & 3) + swap) ^ (row & 7)) * 16;
-  const uint32_t second = at + static_cast<uint32_t>((2 * (c & 3) + 1 - swap) ^ (row & 7)) * 16;
-#pragma unroll 4
-  for (int i = 0; i < 128 / kRowStep; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src + i * kRowStep * D);
-    const uint32_t x = v.x ^ 0x80808080u, y = v.y ^ 0x80808080u, z = v.z ^ 0x80808080u, w = v.w ^ 0x80808080u;
-    st_shared_v4((swap ? second : first) + i * kRowStep * 128, cvt_lo(x), cvt_hi(x), cvt_lo(y), cvt_hi(y));
-    st_shared_v4((swap ? first : second) + i * kRowStep * 128, cvt_lo(z), cvt_hi(z), cvt_lo(w), cvt_hi(w));
+  constexpr int kPieces = Cfg<D>::kPieces;
+  const int lane = tid & 31;
+  const int c = lane & 3;
+  const int row = (lane >> 3) ^ (lane & 4 ? 5 : 0);      // of 8
+  const int at = (tid >> 5) * 8 + row;                   // warp w: row groups w, w + 4, ...
+  const unsigned char* src = tile + at * D;
+  const uint32_t dst = image + static_cast<uint32_t>(at * 128);
+  const uint32_t first = dst + static_cast<uint32_t>((2 * c) ^ row) * 16, second = dst + static_cast<uint32_t>((2 * c + 1) ^ row) * 16;
+#pragma unroll
+  for (int pc = 0; pc < kPieces; ++pc) {
+    const unsigned char* from = src + ((c + 4 * pc) ^ (D == 128 ? row : row >> 1)) * 16;
+#pragma unroll 2
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(from + i * 32 * D);
+      const uint32_t x = v.x ^ 0x80808080u, y = v.y ^ 0x80808080u, z = v.z ^ 0x80808080u, w = v.w ^ 0x80808080u;
+      const uint32_t off = static_cast<uint32_t>(pc * Cfg<D>::kPieceBytes + i * 32 * 128);
+      st_shared_v4(first + off, cvt_lo(x), cvt_hi(x), cvt_lo(y), cvt_hi(y));
+      st_shared_v4(second + off, cvt_lo(z), cvt_hi(z), cvt_lo(w), cvt_hi(w));
+    }
   }
 }
 
@@ -366,108 +406,245 @@ __device__ __forceinline__ float max16(const uint32_t* a) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// A row's 128 scores: the running maximum m (O and l rescaled when it moves), P in
-// place of the scores, l.  `left`: the keys of the unit that the row sees, looked
-// at only where the unit needs a mask.
+// Largest x = c ks s + log2 vs (c ks >= 0) of 16 scores of one scale; `left`: how
+// many of them the row sees (MASK).
+template <bool MASK>
+__device__ __forceinline__ float max_of(const uint32_t* v, const float4& f, int left) {
+  if constexpr (MASK) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, e < left ? fmaf(__uint_as_float(v[e]), f.x, f.y) : -INFINITY);
+    return top;
+  } else {
+    return fmaf(max16(v), f.x, f.y);
+  }
+}
+
+// P of 16 scores of one scale to tensor memory, their sum / vs onto l.
+template <bool MASK>
+__device__ __forceinline__ void exp_of(const uint32_t* v, const float4& f, int left, float base, float& l, uint32_t p_at) {
+  uint32_t pk[8];
+  const float lv = f.y - base;
+  const uint64_t ff = pair(f.x, f.x), lvlv = pair(lv, lv);
+  uint64_t sum = 0;   // two zeros
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    float p0, p1;
+    unpair(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ff, lvlv), p0, p1);
+    if constexpr (MASK) {
+      p0 = e < left ? p0 : -INFINITY;
+      p1 = e + 1 < left ? p1 : -INFINITY;
+    }
+    p0 = ex2(p0);
+    p1 = ex2(p1);
+    sum = add2(sum, pair(p0, p1));
+    const __half2 q = __floats2half2_rn(p0, p1);
+    pk[e / 2] = *reinterpret_cast<const uint32_t*>(&q);
+  }
+  float s0, s1;
+  unpair(sum, s0, s1);
+  l = fmaf(s0 + s1, f.z, l);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(p_at), "r"(pk[0]),
+               "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7])
+               : "memory");
+}
+
+// Where P of 16-key group i of a half lies, from the half's first score on: over
+// scores that are in registers by then.
+__device__ __forceinline__ constexpr uint32_t p_column(int i) { return static_cast<uint32_t>((i >> 1) * 32 + (i & 1) * 8); }
+
+// 64 of a row's scores (the row's other 64 are another warp's): the running maximum
+// m (O and l rescaled when it moves), P in place of the scores, l.  `left`: the
+// keys of these 64 that the row sees, looked at only where the unit needs a mask.
+// `s_at` the scores, `o_at` this thread's half of O; `mine` the row's place in the
+// exchange of the two warps, `other` the other warp's.  A warp whose wait ran out
+// takes part in the exchange with NaN, and both give up.  S is read twice, 32 scores
+// at a time, in loops that are not unrolled: the code of all roles has to stay in the
+// instruction cache (unrolled, the kernel took 1.6 times as long).
 template <int D, bool MASK>
 __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const float4* sc, int left, bool first, float& m,
-                                             float& l, uint64_t* p_full) {
-  // S is read twice, a chunk ahead of its use: 128 scores do not fit beside the rest
-  uint32_t a[2][32];
-  float top = -INFINITY;   // largest x = c ks s + log2 vs (c ks >= 0)
-  tmem_ld32(s_at, a[0]);
-#pragma unroll
-  for (int ch = 0; ch < kKeys / 32; ++ch) {
-    tmem_ld_wait();
-    tmem_ld32(s_at + 32 * ((ch + 1) % (kKeys / 32)), a[(ch + 1) & 1]);   // the last: chunk 0 again
-    uint32_t(&v)[32] = a[ch & 1];
-    if constexpr (MASK) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (32 * ch + e >= left) v[e] = 0xFF800000u;
-    }
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-      const float4 f = sc[2 * ch + gr];
-      const float best = max16(v + 16 * gr);
-      const float x = fmaf(best, f.x, f.y);
-      top = fmaxf(top, MASK && best == -INFINITY ? -INFINITY : x);  // a scale of 0 would make NaN of it
+                                             float& l, uint32_t mine, uint32_t other, int pair_id, bool& ok) {
+  uint32_t a[32];
+  float top = __int_as_float(0x7FC00000);
+  if (ok) {
+    top = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < 4; i += 2) {
+      tmem_ld32(s_at + 16 * i, a);
+      tmem_ld_wait();
+      top = fmaxf(top, fmaxf(max_of<MASK>(a, sc[i], left - 16 * i), max_of<MASK>(a + 16, sc[i + 1], left - 16 * i - 16)));
     }
   }
+  st_shared_f32(mine, ok ? fmaxf(top, -INFINITY) : top);   // scores that are all NaN count as none
+  pair_sync(pair_id);
+  const float its = ld_shared_f32(other);
+  ok = __all_sync(0xFFFFFFFFu, ok && its == its);
+  if (!ok) return;
+  top = fmaxf(top, its);   // not NaN: `its` is not
   if (first) {
     m = top;
   } else {
     const bool over = top > m + kSlack;
-    if (__any_sync(0xFFFFFFFFu, over)) {
+    if (__any_sync(0xFFFFFFFFu, over)) {   // in both warps of the rows
       const float keep = over ? ex2(m - top) : 1.f;
       if (over) m = top;
       l *= keep;
 #pragma unroll 1
-      for (int ch = 0; ch < D / 16; ++ch) {
+      for (int ch = 0; ch < D / 32; ++ch) {
         float o[16];
-        tc::tmem_ld16(o_at + 16 * ch, o);   // waits for the chunk of S too
+        tc::tmem_ld16(o_at + 16 * ch, o);
         uint32_t b[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) b[e] = __float_as_uint(o[e] * keep);
         tc::tmem_st16(o_at + 16 * ch, b);
       }
+      tc::tmem_st_wait();
+      tc_fence_before();
+      pair_sync(pair_id);   // all of O, before either warp lets the next product begin
     }
   }
   const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-  for (int ch = 0; ch < kKeys / 32; ++ch) {
-    if (ch > 0) tmem_ld32(s_at + 32 * ch, a[0]);
+  for (int i = 0; i < 4; i += 2) {
+    tmem_ld32(s_at + 16 * i, a);
     tmem_ld_wait();
-    const uint32_t(&v)[32] = a[0];
-    uint32_t pk[16];
+    exp_of<MASK>(a, sc[i], left - 16 * i, base, l, s_at + p_column(i));
+    exp_of<MASK>(a + 16, sc[i + 1], left - 16 * i - 16, base, l, s_at + p_column(i + 1));
+  }
+  tc::tmem_st_wait();
+  tc_fence_before();
+}
+
+// Columns of a row of the output.
+template <int N>
+__device__ __forceinline__ void store_row(__half* dst, const uint32_t (&a)[N], float inv, bool sees) {
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-      const float4 f = sc[2 * ch + gr];
-      const float lv = f.y - base;
-      const uint64_t ff = pair(f.x, f.x), lvlv = pair(lv, lv);
-      uint64_t sum = 0;   // two zeros
+  for (int e = 0; e < N; e += 8) {
+    uint32_t pk[4];
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        float p0, p1;
-        unpair(fma2(pair(__uint_as_float(v[16 * gr + e]), __uint_as_float(v[16 * gr + e + 1])), ff, lvlv), p0, p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        if constexpr (MASK) {
-          if (32 * ch + 16 * gr + e >= left) p0 = 0.f;
-          if (32 * ch + 16 * gr + e + 1 >= left) p1 = 0.f;
-        }
-        sum = add2(sum, pair(p0, p1));
-        const __half2 q = __floats2half2_rn(p0, p1);
-        pk[8 * gr + e / 2] = *reinterpret_cast<const uint32_t*>(&q);
+    for (int i = 0; i < 4; ++i) {
+      const float v0 = sees ? __uint_as_float(a[e + 2 * i]) * inv : 0.f;
+      const float v1 = sees ? __uint_as_float(a[e + 2 * i + 1]) * inv : 0.f;
+      const __half2 q = __floats2half2_rn(v0, v1);
+      pk[i] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    *reinterpret_cast<uint4*>(dst + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  }
+}
+
+// The end of an item: its row sums taken out of tensor memory and finished, or left
+// for the range whose arrival completes the item.  Not inlined: its registers are
+// not the unit loop's.
+template <int D>
+__device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req req, int head, int base, int lo, bool whole,
+                                         bool busy, bool ok, uint32_t o_at, float m, float l) {
+  const int r = threadIdx.x & (kTile - 1);
+  const int sw = (threadIdx.x >> 5) - kSoftmaxWarp0;
+  const int x = sw >> 3, half = (sw >> 2) & 1, pair_id = 4 * x + (sw & 3);
+  const uint32_t mine_top = smem_u32(&ctl.top[x][half][r]), other_top = smem_u32(&ctl.top[x][half ^ 1][r]);
+  if (busy) {
+    st_shared_f32(mine_top, l);
+    pair_sync(pair_id);
+    l += ld_shared_f32(other_top);
+    pair_sync(pair_id);   // before either writes there again
+  }
+  const bool mine = base + r < req.rows;
+  const int rr = base + r;
+  const int tok = rr / p.group;
+  const int lim = req.seq - req.n + tok + 1;
+  const bool sees = lim > 0;
+  const int h = head * p.group + (rr - tok * p.group);
+  __half* dst = p.out + static_cast<size_t>(req.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + half * (D / 2);
+  constexpr size_t kTileFloats = static_cast<size_t>(kTile) * (D + 2);
+  constexpr size_t kMAt = static_cast<size_t>(D) * kTile, kLAt = static_cast<size_t>(D + 1) * kTile;
+  float* slot = p.partial + (static_cast<size_t>(2 * blockIdx.x + (lo == 0 ? 1 : 0)) * 2 + x) * kTileFloats;
+  const int quad0 = half * (D / 8);   // this half's first four columns
+  if (ok && busy) {
+    const float inv = inverse_sum(l, sees);
+#pragma unroll 1
+    for (int ch = 0; ch < D / 64; ++ch) {
+      uint32_t a[32];
+      tmem_ld32(o_at + 32 * ch, a);
+      tmem_ld_wait();
+      if (whole) {
+        if (mine) store_row(dst + 32 * ch, a, inv, sees);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          __stcg(reinterpret_cast<float4*>(slot) + static_cast<size_t>(quad0 + 8 * ch + e / 4) * kTile + r,
+                 make_float4(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])));
       }
-      float s0, s1;
-      unpair(sum, s0, s1);
-      l = fmaf(s0 + s1, f.z, l);
     }
-    tc::tmem_st16(s_at + 16 * ch, pk);
-    if (ch & 1) {   // half of the keys: their product may begin
-      tc::tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(p_full + (ch >> 1));
+    tc_fence_before();
+  }
+  float* lse = p.lse != nullptr && half == 0 ? p.lse + static_cast<size_t>(req.t0 + tok) * p.q_heads + h : nullptr;
+  if (whole) {
+    if (ok && mine && lse != nullptr) *lse = sees ? kLn2 * (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
+    return;
+  }
+  if (half == 0) {
+    __stcg(slot + kMAt + r, m);
+    __stcg(slot + kLAt + r, l);
+  }
+  const int c0 = ctl.spread0[lo == 0 ? 1 : 0], c1 = ctl.spread1[lo == 0 ? 1 : 0];
+  __threadfence();
+  tile_sync(x);
+  if (r == 0 && half == 0) {
+    const bool last = atomicAdd(p.arrived + 2 * c0 + x, 1u) == static_cast<uint32_t>(c1 - c0);
+    ctl.last[x] = last ? 1u : 0u;
+    if (last) p.arrived[2 * c0 + x] = 0u;
+  }
+  tile_sync(x);
+  const bool last = ctl.last[x] != 0u;
+  tile_sync(x);  // before the flag is written again
+  if (last && mine) {
+    __threadfence();
+    auto part = [&](int k) { return p.partial + (static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * 2 + x) * kTileFloats; };
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part(k) + kMAt + r));
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int k = c0; k <= c1; ++k) sum += __ldcg(part(k) + kLAt + r) * ex2(__ldcg(part(k) + kMAt + r) - base);
+    const float inv = inverse_sum(sum, sees);
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {   // 16 columns
+      uint32_t acc[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = 0u;
+#pragma unroll 1
+      for (int k = c0; k <= c1; ++k) {
+        const float* q = part(k);
+        float4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(quad0 + 4 * ch + e) * kTile + r);
+        const float f = ex2(__ldcg(q + kMAt + r) - base);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[4 * e] = __float_as_uint(fmaf(v[e].x, f, __uint_as_float(acc[4 * e])));
+          acc[4 * e + 1] = __float_as_uint(fmaf(v[e].y, f, __uint_as_float(acc[4 * e + 1])));
+          acc[4 * e + 2] = __float_as_uint(fmaf(v[e].z, f, __uint_as_float(acc[4 * e + 2])));
+          acc[4 * e + 3] = __float_as_uint(fmaf(v[e].w, f, __uint_as_float(acc[4 * e + 3])));
+        }
+      }
+      store_row(dst + 16 * ch, acc, inv, sees);
     }
+    if (lse != nullptr) *lse = sees ? kLn2 * base + logf(sum) : -INFINITY;
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+    prompt_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap qmap) {
   using C = Cfg<D>;
-  extern __shared__ unsigned char smem_dyn[];
-  __shared__ Control ctl;
-  unsigned char* smem_raw = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);  // swizzle atoms
+  extern __shared__ __align__(1024) unsigned char smem_raw[];   // the images: swizzle atoms
   const int tid = threadIdx.x;
   const int lane = tid & 31;
   const int warp = tid >> 5;
-  const int cta = blockIdx.x;
   const uint32_t images = smem_u32(smem_raw);   // Q A, Q B, K 0, K 1, V 0, V 1
   unsigned char* bytes = smem_raw + 6 * C::kImageBytes;   // int8 K, V
+  Control& ctl = *reinterpret_cast<Control*>(bytes + 2 * C::kByteTile);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -478,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.k_empty[i], 1);
       mbar_init(&ctl.v_empty[i], 1);
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i][0], kTile / 32);
+      mbar_init(&ctl.p_full[i][0], kTile / 32);   // the four warps of 64 keys
       mbar_init(&ctl.p_full[i][1], kTile / 32);
       mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.o_done[i], 1);
@@ -500,64 +677,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walker w(p, ctl, count);
 
   if (warp == kMmaWarp) {
-    // ---- MMA issue ---------------------------------------------------------------------
+    // ---- MMA issue: one lane runs the whole loop -----------------------------------------
     // Before the first unit, and after the product of unit u - 1, the scores of unit
     // u are issued.  The code is kept small (nothing is unrolled but the MMAs of one
-    // product): this warp's instruction fetches are on the critical path.
-    constexpr uint32_t kIdescS = idesc(kKeys, false), kIdescO = idesc(D, true);
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    const uint64_t q_desc = swizzled_desc(images, 16, 1024);
-    const uint64_t k_desc = swizzled_desc(images + 2 * C::kImageBytes, 16, 1024);
-    const uint64_t v_desc = swizzled_desc(images + 4 * C::kImageBytes, C::kPieceBytes, 1024);
-    uint32_t used = 0;        // bit x: parity of the products of tile x so far
-    uint32_t begun = 0;       // bit x: parity of the items of tile x so far
-    int now = 0, next = w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;  // tiles of unit u - 1, of unit u
-    int blk = w.lo;           // unit u in its item
-    bool first = false, last = true;   // unit u - 1 begins, ends its item
-    bool ok = true;
+    // product) and what can be waited for early is: this thread is on the critical
+    // path whenever the tensor pipe runs dry.
+    if (elect()) {
+      constexpr uint32_t kIdescS = idesc(kKeys, false), kIdescO = idesc(D, true);
+      const uint64_t q_desc = swizzled_desc(images, 16, 1024);
+      const uint64_t k_desc = swizzled_desc(images + 2 * C::kImageBytes, 16, 1024);
+      const uint64_t v_desc = swizzled_desc(images + 4 * C::kImageBytes, C::kPieceBytes, 1024);
+      uint32_t used = 0;        // bit x: parity of the products of tile x so far
+      uint32_t begun = 0;       // bit x: parity of the items of tile x so far
+      int now = 0, next = w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;  // tiles of unit u - 1, of unit u
+      int blk = w.lo;           // unit u in its item
+      bool first = false, last = true;   // unit u - 1 begins, ends its item
+      bool ok = true;
 #pragma unroll 1
-    for (uint32_t u = 0; u <= static_cast<uint32_t>(count) && ok; ++u) {
-      const uint32_t slot = u & 1, prev = slot ^ 1;
+      for (uint32_t u = 0; u <= static_cast<uint32_t>(count) && ok; ++u) {
+        const uint32_t slot = u & 1, prev = slot ^ 1;
+        ok = (now == 0 || poll_wait(&ctl.v_full[prev], ((u - 1) >> 1) & 1)) &&
+             (next == 0 || poll_wait(&ctl.k_full[slot], (u >> 1) & 1));
 #pragma unroll 1
-      for (int x = 0; x < 2 && ok; ++x) {
-        const uint32_t s_col = tm + static_cast<uint32_t>(x * kKeys);
-        if (x < now) {
-          ok = x > 0 || warp_wait(ctl, &ctl.v_full[prev], ((u - 1) >> 1) & 1);
+        for (int x = 0; x < 2 && ok; ++x) {
+          const uint32_t s_col = tmem + static_cast<uint32_t>(x * kKeys);
+          if (x < now) {
+            const uint64_t b = v_desc + ((prev * C::kImageBytes) >> 4);
 #pragma unroll 1
-          for (int h = 0; h < 2 && ok; ++h) {   // half of the keys
-            ok = warp_wait(ctl, &ctl.p_full[x][h], (used >> x) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect()) {
-              const uint64_t b = v_desc + ((prev * C::kImageBytes + h * 64 * 128) >> 4);
+            for (int h = 0; h < 2 && ok; ++h) {   // half of the keys
+              ok = poll_wait(&ctl.p_full[x][h], (used >> x) & 1);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < kKeys / 32; ++k)
-                tc::mma_f16_ts(tm + static_cast<uint32_t>(C::kOCol + x * D), s_col + 32 * h + 8 * k, b + ((k * 2048) >> 4), kIdescO,
+              for (int k = 0; k < kHalf / 16; ++k)
+                tc::mma_f16_ts(tmem + static_cast<uint32_t>(C::kOCol + x * D), s_col + kHalf * h + p_column(k),
+                               b + static_cast<uint32_t>((h * kHalf * 128 + k * 2048) >> 4), kIdescO,
                                !first || h > 0 || k > 0 ? 1u : 0u);
-              if (h > 0) {
-                if (last) mma_commit(&ctl.o_done[x]);
-                mma_commit(&ctl.pv_done[x]);
-              }
             }
-            __syncwarp();
+            if (!ok) break;
+            if (last) mma_commit(&ctl.o_done[x]);
+            mma_commit(&ctl.pv_done[x]);
           }
-          if (!ok) break;
-        }
-        if (x < next) {
-          ok = x > 0 || warp_wait(ctl, &ctl.k_full[slot], (u >> 1) & 1);
-          if (last) {
-            ok = ok && warp_wait(ctl, &ctl.q_full[x], (begun >> x) & 1);
+          if (x < next && last) {
+            ok = poll_wait(&ctl.q_full[x], (begun >> x) & 1);
             begun ^= 1u << x;
           }
-        }
-        // the next scores go where P is: its product has to be complete
-        if (x < now) {
-          ok = ok && warp_wait(ctl, &ctl.pv_done[x], (used >> x) & 1);
-          used ^= 1u << x;
-        }
-        if (x < next && ok) {
-          tc_fence_after();
-          if (elect()) {
+          // the next scores go where P is: its product has to be complete
+          if (x < now) {
+            ok = ok && poll_wait(&ctl.pv_done[x], (used >> x) & 1);
+            used ^= 1u << x;
+          }
+          if (x < next && ok) {
+            tc_fence_after();
             const uint64_t a = q_desc + static_cast<uint32_t>((x * C::kImageBytes) >> 4);
             const uint64_t b = k_desc + ((slot * C::kImageBytes) >> 4);
 #pragma unroll
@@ -568,27 +739,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&ctl.s_full[x]);
             if (blk + 1 == w.hi) mma_commit(&ctl.q_empty[x]);
           }
-          __syncwarp();
+        }
+        if (!ok) break;
+        if (now > 0) mma_commit(&ctl.v_empty[prev]);
+        if (next > 0) mma_commit(&ctl.k_empty[slot]);
+        now = next;
+        first = blk == w.lo;
+        last = ++blk == w.hi;
+        if (last) {
+          w.next();
+          blk = w.lo;
+          next = !w.more() ? 0 : w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;
         }
       }
-      if (!ok) break;
-      if (elect()) {
-        if (u > 0) mma_commit(&ctl.v_empty[prev]);
-        if (next > 0) mma_commit(&ctl.k_empty[slot]);
-      }
-      __syncwarp();
-      now = next;
-      first = blk == w.lo;
-      last = ++blk == w.hi;
-      if (last) {
-        w.next();
-        blk = w.lo;
-        next = !w.more() ? 0 : w.r.rows - w.rt * kItemRows > kTile ? 2 : 1;
-      }
+      if (!ok) atomicOr(&ctl.abort, 1u);
+      mma_commit(&ctl.mma_done);
+      mbar_wait(&ctl.mma_done, 0);
     }
-    if (elect()) mma_commit(&ctl.mma_done);
     __syncwarp();
-    mbar_wait(&ctl.mma_done, 0);
   } else if (warp == kLoadWarp) {
     // ---- producer ----------------------------------------------------------------------
     // lanes 0-7: the 16-key groups of the unit two ahead of the one being copied
@@ -668,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&ctl.b_full[0], (n - 1) & 1);
       mbar_wait(&ctl.b_full[1], (n - 1) & 1);
     }
-  } else if (warp >= kQWarp0) {
+  } else if (warp < kSoftmaxWarp0) {
     // ---- Q ---------------------------------------------------------------------------
     const int x = warp - kQWarp0;
     uint32_t items = 0;
@@ -744,11 +912,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- softmax -----------------------------------------------------------------------
-    const int x = warp >> 2;
+    const int x = (warp - kSoftmaxWarp0) >> 3;
+    const int half = ((warp - kSoftmaxWarp0) >> 2) & 1;       // of the keys; of O's columns
     const int r = tid & (kTile - 1);        // row of the tile = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + static_cast<uint32_t>(x * kKeys);
-    const uint32_t o_at = tmem + lanes + static_cast<uint32_t>(C::kOCol + x * D);
+    const uint32_t s_at = tmem + lanes + static_cast<uint32_t>(x * kKeys + half * kHalf);
+    const uint32_t o_at = tmem + lanes + static_cast<uint32_t>(C::kOCol + x * D + half * (D / 2));
+    const uint32_t mine_top = smem_u32(&ctl.top[x][half][r]), other_top = smem_u32(&ctl.top[x][half ^ 1][r]);
+    const int pair_id = 4 * x + (warp & 3);
     uint32_t n = 0, used = 0, items = 0;
     bool ok = true;
     for (; w.more(); w.next()) {
@@ -758,136 +929,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         n += static_cast<uint32_t>(steps);
         continue;
       }
-      const int rr = w.rt * kItemRows + x * kTile + r;
-      const int tok = rr / p.group;
-      const int h = w.head * p.group + (rr - tok * p.group);
-      const bool mine = r < rows;
-      const int lim = w.r.seq - w.r.n + tok + 1;            // keys that this row sees
+      const int lim = w.r.seq - w.r.n + (w.rt * kItemRows + x * kTile + r) / p.group + 1;   // keys that this row sees
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++n, ++used) {
         ok = ok && warp_wait(ctl, &ctl.s_full[x], used & 1) && warp_wait(ctl, &ctl.c_full[n % kScaleSlots], (n / kScaleSlots) & 1);
-        if (!ok) continue;
         if (busy) {
-          tc_fence_after();
-          const float4* sc = ctl.scale[n % kScaleSlots];
+          if (ok) tc_fence_after();
+          const float4* sc = &ctl.scale[n % kScaleSlots][half * (kGroups / 2)];
           const int key0 = (w.lo + j) * kKeys;
-          const bool mask = key0 + kKeys > lim_min;
-          const int left = lim - key0;     // keys of this unit that the row sees
-          if (mask)
-            softmax_unit<D, true>(s_at, o_at, sc, left, j == 0, m, l, ctl.p_full[x]);
+          const int left = lim - key0 - half * kHalf;     // of this half of the unit
+          if (key0 + kKeys > lim_min)
+            softmax_unit<D, true>(s_at, o_at, sc, left, j == 0, m, l, mine_top, other_top, pair_id, ok);
           else
-            softmax_unit<D, false>(s_at, o_at, sc, left, j == 0, m, l, ctl.p_full[x]);
-        } else if (lane == 0) {
-          mbar_arrive(&ctl.p_full[x][0]);
-          mbar_arrive(&ctl.p_full[x][1]);
+            softmax_unit<D, false>(s_at, o_at, sc, left, j == 0, m, l, mine_top, other_top, pair_id, ok);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[x][half]);
       }
       // ---- the item's sums: finished, or to be joined ---------------------------------
       ok = ok && warp_wait(ctl, &ctl.o_done[x], items & 1);
       ++items;
       if (ok) tc_fence_after();
-      const bool whole = w.lo == 0 && w.hi == w.units;
-      const bool sees = lim > 0;
-      __half* dst = p.out + static_cast<size_t>(w.r.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D;
-      float* lse = p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(w.r.t0 + tok) * p.q_heads + h;
-      constexpr size_t kTileFloats = static_cast<size_t>(kTile) * (D + 2);
-      float* slot = p.partial + (static_cast<size_t>(2 * cta + (w.lo == 0 ? 1 : 0)) * 2 + x) * kTileFloats;
-      const float inv = inverse_sum(l, sees);
-      if (ok && busy) {
-#pragma unroll
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t a[32];
-          tmem_ld32(o_at + 32 * ch, a);
-          tmem_ld_wait();
-          if (whole) {
-            if (mine) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t pk[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float v0 = sees ? __uint_as_float(a[e + 2 * i]) * inv : 0.f;
-                  const float v1 = sees ? __uint_as_float(a[e + 2 * i + 1]) * inv : 0.f;
-                  const __half2 q = __floats2half2_rn(v0, v1);
-                  pk[i] = *reinterpret_cast<const uint32_t*>(&q);
-                }
-                *reinterpret_cast<uint4*>(dst + 32 * ch + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              __stcg(reinterpret_cast<float4*>(slot) + static_cast<size_t>(8 * ch + e / 4) * kTile + r,
-                     make_float4(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])));
-          }
-        }
-        tc_fence_before();
-      }
-      if (whole) {
-        if (ok && mine && lse != nullptr) *lse = sees ? kLn2 * (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
-        continue;
-      }
-      __stcg(slot + static_cast<size_t>(D) * kTile + r, m);
-      __stcg(slot + static_cast<size_t>(D + 1) * kTile + r, l);
-      const int c0 = range_of(ctl.cost, w.cost + kItemCost, ctas), c1 = range_of(ctl.cost, w.cost + kItemCost + w.units - 1, ctas);
-      __threadfence();
-      tile_sync(x);
-      if (r == 0) {
-        const bool last = atomicAdd(p.arrived + 2 * c0 + x, 1u) == static_cast<uint32_t>(c1 - c0);
-        ctl.last[x] = last ? 1u : 0u;
-        if (last) p.arrived[2 * c0 + x] = 0u;
-      }
-      tile_sync(x);
-      const bool last = ctl.last[x] != 0u;
-      tile_sync(x);  // before the flag is written again
-      if (last && mine) {
-      __threadfence();
-      auto part = [&](int k) { return p.partial + (static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * 2 + x) * kTileFloats; };
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-      for (int k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part(k) + static_cast<size_t>(D) * kTile + r));
-      const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-      for (int k = c0; k <= c1; ++k)
-        sum += __ldcg(part(k) + static_cast<size_t>(D + 1) * kTile + r) * ex2(__ldcg(part(k) + static_cast<size_t>(D) * kTile + r) - base);
-      const float scale = inverse_sum(sum, sees);
-#pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        float4 acc[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int k = c0; k <= c1; ++k) {
-          const float* q = part(k);
-          float4 v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(8 * ch + e) * kTile + r);
-          const float f = ex2(__ldcg(q + static_cast<size_t>(D) * kTile + r) - base);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            acc[e].x = fmaf(v[e].x, f, acc[e].x);
-            acc[e].y = fmaf(v[e].y, f, acc[e].y);
-            acc[e].z = fmaf(v[e].z, f, acc[e].z);
-            acc[e].w = fmaf(v[e].w, f, acc[e].w);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const __half2 q0 = __floats2half2_rn(sees ? acc[e + i].x * scale : 0.f, sees ? acc[e + i].y * scale : 0.f);
-            const __half2 q1 = __floats2half2_rn(sees ? acc[e + i].z * scale : 0.f, sees ? acc[e + i].w * scale : 0.f);
-            pk[2 * i] = *reinterpret_cast<const uint32_t*>(&q0);
-            pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q1);
-          }
-          *reinterpret_cast<uint4*>(dst + 32 * ch + 4 * e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
-      }
-      if (lse != nullptr) *lse = sees ? kLn2 * base + logf(sum) : -INFINITY;
-      }
+      const int base = w.rt * kItemRows + x * kTile;
+      finish_item<D>(p, ctl, w.r, w.head, base, w.lo, w.lo == 0 && w.hi == w.units, busy, ok, o_at, m, l);
       __syncwarp();
     }
   }
@@ -904,11 +970,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                    cudaStream_t stream) {
-  if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem) != cudaSuccess)
+  constexpr int kSmem = Cfg<D>::kTiles + static_cast<int>(sizeof(Control));
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
+  if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
-  prompt_kernel<D><<<ctas, kThreads, Cfg<D>::kSmem, stream>>>(p, kmap, vmap, qmap);
+  prompt_kernel<D><<<ctas, kThreads, kSmem, stream>>>(p, kmap, vmap, qmap);
   return launch_status();
 }
 
