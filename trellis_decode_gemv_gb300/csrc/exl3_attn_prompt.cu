@@ -28,7 +28,8 @@
 //   22, 23    Q of the next item (A, B) into shared memory as soon as the last
 //             scores of the current one are computed.
 //
-// Barriers: int8 K and V tiles full/empty, K and V images full/empty, scales full
+// Barriers: int8 K and V tiles full/empty, K and V images full, the MMAs
+// that read them done, scales full
 // (four slots: a slot is rewritten only after the softmax of both tiles has used
 // it), per tile Q full/empty, S full, P full, product done, O done.  Every wait is
 // bounded; on timeout the CTA sets its abort flag and the status word, every role
@@ -73,7 +74,8 @@ struct Cfg {
 
 struct Control {
   uint64_t b_full[2], b_empty[2];   // int8 tiles of K, V
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t k_full[2], v_full[2];
+  uint64_t step_done[2];            // S of unit u and the product of unit u - 1, at u % 2
   uint64_t c_full[kScaleSlots];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], o_done[2], mma_done;
   float4 scale[kScaleSlots][kGroups];
@@ -652,8 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.b_empty[i], kConvThreads / 32);
       mbar_init(&ctl.k_full[i], kConvThreads / 32);
       mbar_init(&ctl.v_full[i], kConvThreads / 32);
-      mbar_init(&ctl.k_empty[i], 1);
-      mbar_init(&ctl.v_empty[i], 1);
+      mbar_init(&ctl.step_done[i], 1);
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i][0], kTile / 32);   // the four warps of 64 keys
       mbar_init(&ctl.p_full[i][1], kTile / 32);
@@ -696,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (uint32_t u = 0; u <= static_cast<uint32_t>(count) && ok; ++u) {
         const uint32_t slot = u & 1, prev = slot ^ 1;
-        ok = (now == 0 || poll_wait(&ctl.v_full[prev], ((u - 1) >> 1) & 1)) &&
-             (next == 0 || poll_wait(&ctl.k_full[slot], (u >> 1) & 1));
+        // K of unit u is widened after V of unit u - 1: one wait for both
+        ok = next > 0 ? poll_wait(&ctl.k_full[slot], (u >> 1) & 1) : poll_wait(&ctl.v_full[prev], ((u - 1) >> 1) & 1);
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
           const uint32_t s_col = tmem + static_cast<uint32_t>(x * kKeys);
@@ -741,8 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        if (now > 0) mma_commit(&ctl.v_empty[prev]);
-        if (next > 0) mma_commit(&ctl.k_empty[slot]);
+        mma_commit(&ctl.step_done[slot]);
         now = next;
         first = blk == w.lo;
         last = ++blk == w.hi;
@@ -892,8 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- widening ----------------------------------------------------------------------
     const int ct = tid - 32 * kConvWarp0;
     for (uint32_t n = 0; n < static_cast<uint32_t>(count); ++n) {
-      const uint32_t slot = n & 1, before = ((n >> 1) - 1) & 1;
-      if (!warp_wait(ctl, &ctl.b_full[0], n & 1) || (n >= 2 && !warp_wait(ctl, &ctl.k_empty[slot], before))) break;
+      const uint32_t slot = n & 1;
+      if (!warp_wait(ctl, &ctl.b_full[0], n & 1) || (n >= 2 && !warp_wait(ctl, &ctl.step_done[slot], ((n - 2) >> 1) & 1))) break;
       widen<D>(bytes, images + (2 + slot) * C::kImageBytes, ct);
       fence_proxy_async();
       __syncwarp();
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&ctl.k_full[slot]);
         mbar_arrive(&ctl.b_empty[0]);
       }
-      if (!warp_wait(ctl, &ctl.b_full[1], n & 1) || (n >= 2 && !warp_wait(ctl, &ctl.v_empty[slot], before))) break;
+      if (!warp_wait(ctl, &ctl.b_full[1], n & 1) || (n >= 2 && !warp_wait(ctl, &ctl.step_done[slot ^ 1], ((n - 1) >> 1) & 1))) break;
       widen<D>(bytes + C::kByteTile, images + (4 + slot) * C::kImageBytes, ct);
       fence_proxy_async();
       __syncwarp();
@@ -934,7 +934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++n, ++used) {
-        ok = ok && warp_wait(ctl, &ctl.s_full[x], used & 1) && warp_wait(ctl, &ctl.c_full[n % kScaleSlots], (n / kScaleSlots) & 1);
+        // the scales are there when the scores are: the second wait only orders their reads
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&ctl.s_full[x], used & 1) &&
+                                         poll_wait(&ctl.c_full[n % kScaleSlots], (n / kScaleSlots) & 1));
+        if (!ok && lane == 0) atomicOr(&ctl.abort, 1u);
         if (busy) {
           if (ok) tc_fence_after();
           const float4* sc = &ctl.scale[n % kScaleSlots][half * (kGroups / 2)];
