@@ -107,12 +107,6 @@ __device__ __forceinline__ PageScale page_scale(const AttnParams& p, float ks, f
   s.iv = vs != vs ? 1.f : exp2f(-s.lv);
   return s;
 }
-__device__ __forceinline__ PageScale page_scale(const AttnParams& p, int page, int head) {
-  if (page < 0 || page >= p.pages) return PageScale{0.f, 0.f, 1.f};  // a page outside the pool reads as zeros
-  const size_t at = static_cast<size_t>(page) * p.kv_heads + head;
-  return page_scale(p, __ldg(p.k_scale + at), __ldg(p.v_scale + at));
-}
-
 __device__ __forceinline__ void tensor_g2s_at(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(

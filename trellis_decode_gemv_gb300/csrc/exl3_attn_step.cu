@@ -41,26 +41,8 @@ struct Cfg {
   static_assert(kStages % kConsumers == 0, "each stage belongs to one consumer, so that no parity wait skips a phase");
   static constexpr int kHalfBytes = kUnit * D;           // K or V of a unit
   static constexpr int kStageBytes = 2 * kHalfBytes;
-  static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kPartStride = D + 4;
-  static constexpr int kPartBytes = kConsumers * kRows * kPartStride * 4;
   static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
-};
-
-template <int D, int NT>
-struct Shared {
-  using C = Cfg<D, NT>;
-  unsigned char ring[C::kStages][C::kStageBytes];  // first: 1024-byte aligned
-  __half q[kQSlots][C::kRows * D];
-  float part[kConsumers][C::kRows][C::kPartStride];
-  float pm[kConsumers][C::kRows], pl[kConsumers][C::kRows];
-  float4 scale[C::kStages][2];      // per 16 keys: PageScale
-  uint64_t full[C::kStages], empty[C::kStages];
-  uint64_t q_full[kQSlots], q_empty[kQSlots];
-  long long warp_sum[kThreads / 32];
-  long long first_unit;             // of request first_b
-  int first_b;
-  uint32_t abort, last;
 };
 
 __device__ __forceinline__ void join_sync() {
@@ -85,29 +67,62 @@ template <int NT>
 __device__ __forceinline__ int req_tiles(const Req& r) { return (r.rows + 8 * NT - 1) / (8 * NT); }
 __device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq + kUnit - 1) / kUnit); }
 
+// Ranges are cut in equal parts of units plus kItemCost for each item (Q, the join of
+// the warps).  An item of at most kWhole units is not split: a boundary that falls
+// into it moves to its nearer end.
+constexpr int kItemCost = 1;
+constexpr int kWhole = 24;
+constexpr int kLeast = 12;   // units that are worth a range of their own
+
+// What a request's items cost together, and the ranges that they are worth.
+template <int NT>
+__device__ __forceinline__ void req_cost(const AttnParams& p, const Req& r, long long& cost, long long& ranges) {
+  const int blocks = req_blocks(r);
+  const long long items = static_cast<long long>(req_tiles<NT>(r)) * p.kv_heads;
+  cost += items * (blocks + kItemCost);
+  ranges += items * (blocks <= kWhole ? 1 : (blocks + kLeast - 1) / kLeast);
+}
+
+// A boundary between ranges: unit `lo` of item `item` of request `b`; c0, c1 the first
+// and last range that the item is spread over.
+struct Edge {
+  int b, item, lo, c0, c1;
+};
+
+// The boundary at cost u, in request b, whose items begin at cost `before`.
+__device__ __forceinline__ Edge edge_at(const Req& r, int b, long long u, long long before, long long total, int ctas) {
+  const int blocks = req_blocks(r);
+  const int each = blocks + kItemCost;
+  Edge e;
+  e.b = b;
+  e.item = static_cast<int>((u - before) / each);
+  const long long start = before + static_cast<long long>(e.item) * each;
+  const int off = static_cast<int>(u - start);
+  e.lo = blocks <= kWhole ? (2 * off < each ? 0 : blocks) : max(0, off - kItemCost);
+  e.c0 = range_of(total, start + kItemCost, ctas);
+  e.c1 = range_of(total, start + each - 1, ctas);
+  return e;
+}
+
 // The items of a range, one after the other.  Each lane of a warp holds one
 // request; every warp walks by itself.
 template <int NT>
 struct Walker {
   const AttnParams& p;
-  long long u, end;   // next unit, end of the range
   int base, b;        // request of lane 0, current request
   Req mine;
+  int item;
+  int end_b, end_item, end_lo;
   // current segment
   Req r;
   int blocks, tiles, head, tile, lo, hi;
-  int item;
 
-  __device__ __forceinline__ Walker(const AttnParams& params, int first_b, long long first_unit, long long u0, long long u1)
-      : p(params), u(u0), end(u1), base(first_b), b(first_b) {
+  __device__ __forceinline__ Walker(const AttnParams& params, const Edge& from, const Edge& to)
+      : p(params), base(from.b), b(from.b), item(from.item), end_b(to.b), end_item(to.item), end_lo(to.lo), lo(from.lo) {
     mine = load_req(p, base + (threadIdx.x & 31));
     fetch();
-    if (u < end) {
-      const long long rem = u - first_unit;
-      item = static_cast<int>(rem / blocks);
-      lo = static_cast<int>(rem - static_cast<long long>(item) * blocks);
-      place();
-    }
+    if (lo == blocks) advance();
+    place();
   }
   __device__ __forceinline__ void fetch() {
     const int src = b - base;
@@ -119,14 +134,11 @@ struct Walker {
     tiles = req_tiles<NT>(r);
   }
   __device__ __forceinline__ void place() {
-    head = item / tiles;
-    tile = item - head * tiles;
-    hi = static_cast<int>(min(static_cast<long long>(blocks), lo + (end - u)));
+    head = tiles > 1 ? item / tiles : item;
+    tile = item - head * max(tiles, 1);
+    hi = b > end_b || (b == end_b && item > end_item) ? lo : b == end_b && item == end_item ? min(blocks, end_lo) : blocks;
   }
-  __device__ __forceinline__ bool more() const { return u < end; }
-  __device__ __forceinline__ void next() {
-    u += hi - lo;
-    if (u >= end) return;
+  __device__ __forceinline__ void advance() {
     lo = 0;
     if (++item >= tiles * p.kv_heads) {
       item = 0;
@@ -138,14 +150,71 @@ struct Walker {
         fetch();
       } while (r.rows == 0 && b < p.requests);
     }
+  }
+  __device__ __forceinline__ bool more() const { return hi > lo; }
+  __device__ __forceinline__ void next() {
+    advance();
     place();
   }
 };
 
 template <int D, int NT>
+struct Shared {
+  using C = Cfg<D, NT>;
+  unsigned char ring[C::kStages][C::kStageBytes];  // first: 1024-byte aligned
+  __half q[kQSlots][C::kRows * D];
+  float part[kConsumers][C::kRows][C::kPartStride];
+  float pm[kConsumers][C::kRows], pl[kConsumers][C::kRows];
+  float4 scale[C::kStages][2];      // per 16 keys: PageScale
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t q_full[kQSlots], q_empty[kQSlots];
+  long long warp_sum[kThreads / 32], warp_ranges[kThreads / 32];
+  Edge edge[2];
+  uint32_t abort, last;
+};
+
+// The consumers' sums of a row, 4 columns of it: with the row's maximum and sum.
+template <int D, int NT>
+__device__ __forceinline__ float4 join_warps(const Shared<D, NT>& sh, int row, int q4, float& top, float& sum) {
+  top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, sh.pm[k][row]);
+  const float base = top == -INFINITY ? 0.f : top;
+  sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kConsumers; ++k) {
+    const float f = ex2(sh.pm[k][row] - base);
+    const float4 v = *reinterpret_cast<const float4*>(&sh.part[k][row][4 * q4]);
+    sum += sh.pl[k][row] * f;
+    acc.x += v.x * f;
+    acc.y += v.y * f;
+    acc.z += v.z * f;
+    acc.w += v.w * f;
+  }
+  return acc;
+}
+
+// 4 columns of row `rr` of a request's item, finished.
+template <int D>
+__device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, int head, int rr, int q4, const float4& acc, float top,
+                                          float sum) {
+  const int tok = rr / p.group;
+  const int h = head * p.group + (rr - tok * p.group);
+  const bool sees = r.seq - r.n + tok + 1 > 0;
+  const float inv = inverse_sum(sum, sees);
+  const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
+  const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
+  *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(r.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * q4) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&ha), *reinterpret_cast<const uint32_t*>(&hb));
+  if (p.lse != nullptr && q4 == 0)
+    p.lse[static_cast<size_t>(r.t0 + tok) * p.q_heads + h] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
+}
+
+template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
-    step_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                int min_units) {
+    step_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, NT>;
   constexpr int kRows = C::kRows;
   constexpr int kStages = C::kStages;
@@ -159,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], 2);   // the copies, the scales
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < kQSlots; ++i) {
@@ -170,45 +239,82 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
-  // units of all requests, and the request in which this CTA's range begins
-  const int per = (p.requests + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Req r = load_req(p, b);
-    mine += static_cast<long long>(req_blocks(r)) * req_tiles<NT>(r) * p.kv_heads;
-  }
-  long long inc = mine;
+  // This CTA's range.  Up to 32 requests every warp finds it by itself.
+  Edge from, to;
+  int ctas;
+  if (p.requests <= 32) {
+    const Req r = load_req(p, lane);
+    long long cost = 0, ranges = 0;
+    req_cost<NT>(p, r, cost, ranges);
+    long long inc = cost;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
-  }
-  if (lane == 31) sh.warp_sum[warp] = inc;
-  __syncthreads();
-  long long units = 0, before = inc - mine;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    before += w < warp ? sh.warp_sum[w] : 0;
-    units += sh.warp_sum[w];
-  }
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (units + min_units - 1) / min_units));
-  if (cta >= ctas) return;
-  const long long u0 = range_begin(units, cta, ctas), u1 = range_begin(units, cta + 1, ctas);
-  if (before <= u0 && u0 < before + mine) {
-    for (int b = b0; b < b1; ++b) {
-      const Req r = load_req(p, b);
-      const long long n = static_cast<long long>(req_blocks(r)) * req_tiles<NT>(r) * p.kv_heads;
-      if (u0 < before + n) {
-        sh.first_b = b;
-        sh.first_unit = before;
-        break;
-      }
-      before += n;
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+      ranges += __shfl_xor_sync(0xFFFFFFFFu, ranges, d);
     }
+    const long long total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), ranges));
+    if (cta >= ctas) return;
+    __syncthreads();   // the barriers
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long u = range_begin(total, cta + e, ctas);
+      const int b = __popc(__ballot_sync(0xFFFFFFFFu, inc <= u));   // the request that holds u
+      Req q;
+      q.t0 = 0;
+      q.n = 0;
+      q.rows = 1;
+      q.seq = __shfl_sync(0xFFFFFFFFu, r.seq, b & 31);
+      const long long before = __shfl_sync(0xFFFFFFFFu, inc - cost, b & 31);
+      Edge x{p.requests, 0, 0, 0, 0};
+      if (b < 32) x = edge_at(q, b, u, before, total, ctas);
+      if (e == 0) from = x; else to = x;
+    }
+  } else {
+    const int per = (p.requests + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
+    long long mine = 0, ranges = 0;
+    for (int b = b0; b < b1; ++b) req_cost<NT>(p, load_req(p, b), mine, ranges);
+    long long inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += o;
+      ranges += __shfl_xor_sync(0xFFFFFFFFu, ranges, d);
+    }
+    if (lane == 31) {
+      sh.warp_sum[warp] = inc;
+      sh.warp_ranges[warp] = ranges;
+    }
+    if (tid == 0) sh.edge[1] = Edge{p.requests, 0, 0, 0, 0};   // the last range's end is in no item
+    __syncthreads();
+    long long total = 0, before = inc - mine, all_ranges = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      before += w < warp ? sh.warp_sum[w] : 0;
+      total += sh.warp_sum[w];
+      all_ranges += sh.warp_ranges[w];
+    }
+    ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all_ranges));
+    if (cta >= ctas) return;
+    const long long u[2] = {range_begin(total, cta, ctas), range_begin(total, cta + 1, ctas)};
+    if (u[1] >= before && u[0] < before + mine) {
+      for (int b = b0; b < b1; ++b) {
+        const Req r = load_req(p, b);
+        long long n = 0, unused = 0;
+        req_cost<NT>(p, r, n, unused);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (u[e] >= before && u[e] < before + n) sh.edge[e] = edge_at(r, b, u[e], before, total, ctas);
+        before += n;
+      }
+    }
+    __syncthreads();
+    from = sh.edge[0];
+    to = sh.edge[1];
   }
-  __syncthreads();
-  Walker<NT> w(p, sh.first_b, sh.first_unit, u0, u1);
+  Walker<NT> w(p, from, to);
 
   if (warp == kConsumers) {
     // ---- producer ------------------------------------------------------------------
@@ -239,14 +345,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
       for (int g0 = w.lo; g0 < w.hi && ok; g0 += 32) {
         const int mykey = (g0 + lane) * kUnit;
         int page[2] = {-1, -1};
-        PageScale s[2] = {{0.f, 0.f, 1.f}, {0.f, 0.f, 1.f}};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           if (g0 + lane < w.hi && mykey + 16 * hf < w.r.seq && (hf == 0 || copies == 2))
             page[hf] = __ldg(row + ((mykey + 16 * hf) >> p.page_shift));
         }
-        s[0] = page_scale(p, page[0], w.head);
-        s[1] = copies == 2 ? page_scale(p, page[1], w.head) : s[0];
+        float ks[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};   // a page outside the pool reads as zeros
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          if (page[hf] >= 0 && page[hf] < p.pages) {
+            const size_t at = static_cast<size_t>(page[hf]) * p.kv_heads + w.head;
+            ks[hf] = __ldg(p.k_scale + at);
+            vs[hf] = __ldg(p.v_scale + at);
+          }
         const int outside = p.pages * p.kv_heads;
         const int blk0 = page[0] >= 0 && page[0] < p.pages ? page[0] * p.kv_heads + w.head : outside;
         const int blk1 = page[1] >= 0 && page[1] < p.pages ? page[1] * p.kv_heads + w.head : outside;
@@ -257,8 +368,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
           if (use > 0) ok = mbar_wait(&sh.empty[st], (use - 1) & 1);
           if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
           if (lane == j) {
-            sh.scale[st][0] = make_float4(s[0].c, s[0].lv, s[0].iv, 0.f);
-            sh.scale[st][1] = make_float4(s[1].c, s[1].lv, s[1].iv, 0.f);
             // what lies past the request's keys is not copied: any int8 is finite, and P is 0 there
             const bool first = mykey < w.r.seq, second = copies == 2 && mykey + 16 < w.r.seq;
             mbar_arrive_expect_tx(&sh.full[st], static_cast<uint32_t>(2 * copy_bytes * ((first ? 1 : 0) + (second ? 1 : 0))));
@@ -271,6 +380,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
               tensor_g2s(dst + copy_bytes, &kmap, 0, blk1, &sh.full[st]);
               tensor_g2s(dst + C::kHalfBytes + copy_bytes, &vmap, 0, blk1, &sh.full[st]);
             }
+            const PageScale s0 = page_scale(p, ks[0], vs[0]), s1 = copies == 2 ? page_scale(p, ks[1], vs[1]) : s0;
+            sh.scale[st][0] = make_float4(s0.c, s0.lv, s0.iv, 0.f);
+            sh.scale[st][1] = make_float4(s1.c, s1.lv, s1.iv, 0.f);
+            mbar_arrive(&sh.full[st]);
           }
           __syncwarp();
         }
@@ -493,34 +606,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
       const int row = x / kQuads;
       const int q4 = x - row * kQuads;
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, sh.pm[k][row]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kConsumers; ++k) {
-        const float f = ex2(sh.pm[k][row] - base);
-        const float4 v = *reinterpret_cast<const float4*>(&sh.part[k][row][4 * q4]);
-        sum += sh.pl[k][row] * f;
-        acc.x += v.x * f;
-        acc.y += v.y * f;
-        acc.z += v.z * f;
-        acc.w += v.w * f;
-      }
+      float top, sum;
+      const float4 acc = join_warps(sh, row, q4, top, sum);
       if (whole) {
-        const int rr = row0 + row;
-        const int tok = rr / p.group;
-        const int h = w.head * p.group + (rr - tok * p.group);
-        const bool sees = seen0 + tok + 1 > 0;
-        const float inv = inverse_sum(sum, sees);
-        const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
-        const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
-        *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(w.r.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * q4) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&ha), *reinterpret_cast<const uint32_t*>(&hb));
-        if (p.lse != nullptr && q4 == 0)
-          p.lse[static_cast<size_t>(w.r.t0 + tok) * p.q_heads + h] = sees ? kLn2 * base + logf(sum) : -INFINITY;
+        store_out<D>(p, w.r, w.head, row0 + row, q4, acc, top, sum);
       } else {
         __stcg(reinterpret_cast<float4*>(slot + row * D) + q4, acc);
         if (q4 == 0) {
@@ -532,8 +621,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     if (whole) continue;
 
     // ---- the item crosses ranges: the last to arrive joins --------------------------
-    const long long item_u = w.u - w.lo;
-    const int c0 = range_of(units, item_u, ctas), c1 = range_of(units, item_u + w.blocks - 1, ctas);
+    const int c0 = w.lo == 0 ? to.c0 : from.c0, c1 = w.lo == 0 ? to.c1 : from.c1;
     __threadfence();
     join_sync();
     if (tid == 0) {
@@ -544,40 +632,66 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     join_sync();
     if (sh.last == 0u) continue;
     __threadfence();
+    // Every warp adds up its share of the partial results, all rows at once (a lane
+    // holds 4 columns of several rows); then the warps are joined as above.
     constexpr size_t kSlot = static_cast<size_t>(kRows) * (D + 2);
-    for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
-      const int row = x / kQuads;
-      const int q4 = x - row * kQuads;
-      float top = -INFINITY, sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int k = c0; k <= c1; ++k) {
-        const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
-        const float pm = __ldcg(s + kRows * D + row);
-        const float pl = __ldcg(s + kRows * D + kRows + row);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
-        const float up = fmaxf(top, pm);
-        const float base = up == -INFINITY ? 0.f : up;
-        const float fa = ex2(top - base), fb = ex2(pm - base);
-        top = up;
-        sum = sum * fa + pl * fb;
-        acc.x = acc.x * fa + v.x * fb;
-        acc.y = acc.y * fa + v.y * fb;
-        acc.z = acc.z * fa + v.z * fb;
-        acc.w = acc.w * fa + v.w * fb;
+    constexpr int kLanes = D / 4;              // lanes of a row
+    constexpr int kAtOnce = 32 / kLanes;       // rows at a time
+    constexpr int kMine = kRows / kAtOnce;     // rows of a lane
+    const int q4 = lane % kLanes;
+    const int row_of = lane / kLanes;
+    float top[kMine], sum[kMine];
+    float4 acc[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      top[i] = -INFINITY;
+      sum[i] = 0.f;
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int k = c0 + warp; k <= c1; k += kConsumers) {
+      const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
+      float pm[kMine], pl[kMine];
+      float4 v[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int row = i * kAtOnce + row_of;
+        pm[i] = -INFINITY;
+        pl[i] = 0.f;
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < rows) {
+          pm[i] = __ldcg(s + kRows * D + row);
+          pl[i] = __ldcg(s + kRows * D + kRows + row);
+          v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
+        }
       }
-      const float base = top == -INFINITY ? 0.f : top;
-      const int rr = row0 + row;
-      const int tok = rr / p.group;
-      const int h = w.head * p.group + (rr - tok * p.group);
-      const bool sees = seen0 + tok + 1 > 0;
-      const float inv = inverse_sum(sum, sees);
-      const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
-      const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
-      *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(w.r.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * q4) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&ha), *reinterpret_cast<const uint32_t*>(&hb));
-      if (p.lse != nullptr && q4 == 0)
-        p.lse[static_cast<size_t>(w.r.t0 + tok) * p.q_heads + h] = sees ? kLn2 * base + logf(sum) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const float up = fmaxf(top[i], pm[i]);
+        const float base = up == -INFINITY ? 0.f : up;
+        const float fa = ex2(top[i] - base), fb = ex2(pm[i] - base);
+        top[i] = up;
+        sum[i] = sum[i] * fa + pl[i] * fb;
+        acc[i].x = acc[i].x * fa + v[i].x * fb;
+        acc[i].y = acc[i].y * fa + v[i].y * fb;
+        acc[i].z = acc[i].z * fa + v[i].z * fb;
+        acc[i].w = acc[i].w * fa + v[i].w * fb;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int row = i * kAtOnce + row_of;
+      *reinterpret_cast<float4*>(&sh.part[warp][row][4 * q4]) = acc[i];
+      if (q4 == 0) {
+        sh.pm[warp][row] = top[i];
+        sh.pl[warp][row] = sum[i];
+      }
+    }
+    join_sync();
+    for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
+      float mx, total;
+      const float4 v = join_warps(sh, x / kQuads, x % kQuads, mx, total);
+      store_out<D>(p, w.r, w.head, row0 + x / kQuads, x % kQuads, v, mx, total);
     }
   }
   if (!ok && lane == 0) {
@@ -594,7 +708,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
     return EXL3_ERR_CUDA;
   int ctas = device_sm_count() * C::kCtasPerSm;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  step_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(p, kmap, vmap, 8);
+  step_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(p, kmap, vmap);
   return launch_status();
 }
 
