@@ -4,8 +4,8 @@
 // every byte into a binary16 MMA operand (1.25 to 1.5 instructions a byte) with
 // enough copies in flight.
 //
-// Three consumer warps and one producer warp.  A unit is 32 keys of an item: 32 x
-// D bytes of K and of V, one tensor copy each (two for pages of 16 tokens), into
+// Three consumer warps and one producer warp.  A unit is 4 KB of K and of V of an
+// item (32 or 64 keys), one tensor copy each (or one per page, if those are smaller), into
 // a ring of stages; unit i of the CTA's range goes to stage i % kStages and to
 // consumer i % 3.  The producer walks the range ahead of the consumers: page
 // numbers and scales of up to 32 units at a time, the copies, and each item's
@@ -30,7 +30,11 @@ namespace {
 
 constexpr int kConsumers = 3;
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kUnit = 32;           // keys
+// Keys of a unit: 4 KB of K and of V, whatever the head dimension (32 keys of 64
+// elements are too little for what a unit costs besides: 68 us for 64 requests of
+// 4096 keys and 8 heads, where 64 keys take 57).
+template <int D>
+constexpr int unit_keys() { return 4096 / D; }
 constexpr int kQSlots = 2;
 constexpr int kJoinBarrier = 1;
 
@@ -39,6 +43,8 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStages = 6;
   static_assert(kStages % kConsumers == 0, "each stage belongs to one consumer, so that no parity wait skips a phase");
+  static constexpr int kUnit = unit_keys<D>();
+  static constexpr int kGroups = kUnit / 16;             // of 16 keys, one scale each
   static constexpr int kHalfBytes = kUnit * D;           // K or V of a unit
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kPartStride = D + 4;
@@ -65,7 +71,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 template <int NT>
 __device__ __forceinline__ int req_tiles(const Req& r) { return (r.rows + 8 * NT - 1) / (8 * NT); }
-__device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq + kUnit - 1) / kUnit); }
+template <int D>
+__device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq + unit_keys<D>() - 1) / unit_keys<D>()); }
 
 // Ranges are cut in equal parts of units plus kItemCost for each item (Q, the join of
 // the warps).  An item of at most kWhole units is not split: a boundary that falls
@@ -75,9 +82,9 @@ constexpr int kWhole = 24;
 constexpr int kLeast = 12;   // units that are worth a range of their own
 
 // What a request's items cost together, and the ranges that they are worth.
-template <int NT>
+template <int D, int NT>
 __device__ __forceinline__ void req_cost(const AttnParams& p, const Req& r, long long& cost, long long& ranges) {
-  const int blocks = req_blocks(r);
+  const int blocks = req_blocks<D>(r);
   const long long items = static_cast<long long>(req_tiles<NT>(r)) * p.kv_heads;
   cost += items * (blocks + kItemCost);
   ranges += items * (blocks <= kWhole ? 1 : (blocks + kLeast - 1) / kLeast);
@@ -90,8 +97,9 @@ struct Edge {
 };
 
 // The boundary at cost u, in request b, whose items begin at cost `before`.
+template <int D>
 __device__ __forceinline__ Edge edge_at(const Req& r, int b, long long u, long long before, long long total, int ctas) {
-  const int blocks = req_blocks(r);
+  const int blocks = req_blocks<D>(r);
   const int each = blocks + kItemCost;
   Edge e;
   e.b = b;
@@ -106,7 +114,7 @@ __device__ __forceinline__ Edge edge_at(const Req& r, int b, long long u, long l
 
 // The items of a range, one after the other.  Each lane of a warp holds one
 // request; every warp walks by itself.
-template <int NT>
+template <int D, int NT>
 struct Walker {
   const AttnParams& p;
   int base, b;        // request of lane 0, current request
@@ -130,7 +138,7 @@ struct Walker {
     r.n = __shfl_sync(0xFFFFFFFFu, mine.n, src);
     r.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, src);
     r.seq = __shfl_sync(0xFFFFFFFFu, mine.seq, src);
-    blocks = req_blocks(r);
+    blocks = req_blocks<D>(r);
     tiles = req_tiles<NT>(r);
   }
   __device__ __forceinline__ void place() {
@@ -165,7 +173,7 @@ struct Shared {
   __half q[kQSlots][C::kRows * D];
   float part[kConsumers][C::kRows][C::kPartStride];
   float pm[kConsumers][C::kRows], pl[kConsumers][C::kRows];
-  float4 scale[C::kStages][2];      // per 16 keys: PageScale
+  float4 scale[C::kStages][C::kGroups];   // per 16 keys: PageScale
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[kQSlots], q_empty[kQSlots];
   long long warp_sum[kThreads / 32], warp_ranges[kThreads / 32];
@@ -218,6 +226,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
   using C = Cfg<D, NT>;
   constexpr int kRows = C::kRows;
   constexpr int kStages = C::kStages;
+  constexpr int kUnit = C::kUnit;
+  constexpr int kGroups = C::kGroups;
   constexpr int KS = D / 16;  // k-steps of the first product, m-tiles of the second
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem_raw);
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
   if (p.requests <= 32) {
     const Req r = load_req(p, lane);
     long long cost = 0, ranges = 0;
-    req_cost<NT>(p, r, cost, ranges);
+    req_cost<D, NT>(p, r, cost, ranges);
     long long inc = cost;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -268,14 +278,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
       q.seq = __shfl_sync(0xFFFFFFFFu, r.seq, b & 31);
       const long long before = __shfl_sync(0xFFFFFFFFu, inc - cost, b & 31);
       Edge x{p.requests, 0, 0, 0, 0};
-      if (b < 32) x = edge_at(q, b, u, before, total, ctas);
+      if (b < 32) x = edge_at<D>(q, b, u, before, total, ctas);
       if (e == 0) from = x; else to = x;
     }
   } else {
     const int per = (p.requests + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
     long long mine = 0, ranges = 0;
-    for (int b = b0; b < b1; ++b) req_cost<NT>(p, load_req(p, b), mine, ranges);
+    for (int b = b0; b < b1; ++b) req_cost<D, NT>(p, load_req(p, b), mine, ranges);
     long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -303,10 +313,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
       for (int b = b0; b < b1; ++b) {
         const Req r = load_req(p, b);
         long long n = 0, unused = 0;
-        req_cost<NT>(p, r, n, unused);
+        req_cost<D, NT>(p, r, n, unused);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          if (u[e] >= before && u[e] < before + n) sh.edge[e] = edge_at(r, b, u[e], before, total, ctas);
+          if (u[e] >= before && u[e] < before + n) sh.edge[e] = edge_at<D>(r, b, u[e], before, total, ctas);
         before += n;
       }
     }
@@ -314,13 +324,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     from = sh.edge[0];
     to = sh.edge[1];
   }
-  Walker<NT> w(p, from, to);
+  Walker<D, NT> w(p, from, to);
 
   if (warp == kConsumers) {
     // ---- producer ------------------------------------------------------------------
     const int size = 1 << p.page_shift;
-    const int copies = p.page_shift == 4 ? 2 : 1;   // per unit, of K and of V
-    const int copy_bytes = C::kHalfBytes / copies;
+    const int copy_keys = min(size, kUnit);          // a unit is one copy, or one per page
+    const uint32_t copy_bytes = static_cast<uint32_t>(copy_keys * D);
     uint32_t i = 0;       // unit of the range
     int seg = 0;
     bool ok = true;
@@ -344,23 +354,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
       const int32_t* row = p.table + static_cast<size_t>(w.b) * p.table_stride;
       for (int g0 = w.lo; g0 < w.hi && ok; g0 += 32) {
         const int mykey = (g0 + lane) * kUnit;
-        int page[2] = {-1, -1};
+        int block[kGroups];                            // of the tensor map, per 16 keys
+        float ks[kGroups], vs[kGroups];
+        PageScale scale[kGroups];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (g0 + lane < w.hi && mykey + 16 * hf < w.r.seq && (hf == 0 || copies == 2))
-            page[hf] = __ldg(row + ((mykey + 16 * hf) >> p.page_shift));
+        for (int gr = 0; gr < kGroups; ++gr) {
+          const int key = mykey + 16 * gr;
+          int page = -1;
+          if (g0 + lane < w.hi && key < w.r.seq) page = __ldg(row + (key >> p.page_shift));
+          const bool in = page >= 0 && page < p.pages;   // a page outside the pool reads as zeros
+          block[gr] = in ? page * p.kv_heads + w.head : p.pages * p.kv_heads;
+          const size_t at = static_cast<size_t>(in ? block[gr] : 0);
+          ks[gr] = in ? __ldg(p.k_scale + at) : 0.f;
+          vs[gr] = in ? __ldg(p.v_scale + at) : 1.f;
         }
-        float ks[2] = {0.f, 0.f}, vs[2] = {1.f, 1.f};   // a page outside the pool reads as zeros
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          if (page[hf] >= 0 && page[hf] < p.pages) {
-            const size_t at = static_cast<size_t>(page[hf]) * p.kv_heads + w.head;
-            ks[hf] = __ldg(p.k_scale + at);
-            vs[hf] = __ldg(p.v_scale + at);
-          }
-        const int outside = p.pages * p.kv_heads;
-        const int blk0 = page[0] >= 0 && page[0] < p.pages ? page[0] * p.kv_heads + w.head : outside;
-        const int blk1 = page[1] >= 0 && page[1] < p.pages ? page[1] * p.kv_heads + w.head : outside;
         const int n = min(32, w.hi - g0);
         for (int j = 0; j < n; ++j, ++i) {
           const uint32_t st = i % kStages;
@@ -369,20 +376,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
           if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
           if (lane == j) {
             // what lies past the request's keys is not copied: any int8 is finite, and P is 0 there
-            const bool first = mykey < w.r.seq, second = copies == 2 && mykey + 16 < w.r.seq;
-            mbar_arrive_expect_tx(&sh.full[st], static_cast<uint32_t>(2 * copy_bytes * ((first ? 1 : 0) + (second ? 1 : 0))));
-            unsigned char* dst = sh.ring[st];
-            if (first) {
-              tensor_g2s(dst, &kmap, mykey & (size - 1), blk0, &sh.full[st]);
-              tensor_g2s(dst + C::kHalfBytes, &vmap, mykey & (size - 1), blk0, &sh.full[st]);
+            const int left = min(kUnit, w.r.seq - mykey);
+            const uint32_t parts = left > 0 ? static_cast<uint32_t>((left + copy_keys - 1) / copy_keys) : 0u;
+            mbar_arrive_expect_tx(&sh.full[st], 2 * copy_bytes * parts);
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+              const int key = 16 * gr;
+              if ((key & (copy_keys - 1)) != 0 || key >= left) continue;
+              unsigned char* dst = sh.ring[st] + key * D;
+              tensor_g2s(dst, &kmap, (mykey + key) & (size - 1), block[gr], &sh.full[st]);
+              tensor_g2s(dst + C::kHalfBytes, &vmap, (mykey + key) & (size - 1), block[gr], &sh.full[st]);
             }
-            if (second) {
-              tensor_g2s(dst + copy_bytes, &kmap, 0, blk1, &sh.full[st]);
-              tensor_g2s(dst + C::kHalfBytes + copy_bytes, &vmap, 0, blk1, &sh.full[st]);
-            }
-            const PageScale s0 = page_scale(p, ks[0], vs[0]), s1 = copies == 2 ? page_scale(p, ks[1], vs[1]) : s0;
-            sh.scale[st][0] = make_float4(s0.c, s0.lv, s0.iv, 0.f);
-            sh.scale[st][1] = make_float4(s1.c, s1.lv, s1.iv, 0.f);
+          }
+          if (j == 0) {   // the first copies do not wait for the scales
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) scale[gr] = page_scale(p, ks[gr], vs[gr]);
+          }
+          if (lane == j) {
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) sh.scale[st][gr] = make_float4(scale[gr].c, scale[gr].lv, scale[gr].iv, 0.f);
             mbar_arrive(&sh.full[st]);
           }
           __syncwarp();
@@ -455,10 +467,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
       }
       const unsigned char* kb = sh.ring[st];
       const unsigned char* vb = kb + C::kHalfBytes;
-      // scores of 2 x 16 keys
-      float s[2][NT][4];
+      float s[kGroups][NT][4];   // scores
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < kGroups; ++hf) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -487,12 +498,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         }
       }
       // x = c ks s + log2 vs, masked
-      const float4 sc[2] = {sh.scale[st][0], sh.scale[st][1]};
+      float4 sc[kGroups];
+#pragma unroll
+      for (int hf = 0; hf < kGroups; ++hf) sc[hf] = sh.scale[st][hf];
       const int key0 = blk * kUnit;
       const bool mask = key0 + kUnit > lim_min;
       bool over = false;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int hf = 0; hf < kGroups; ++hf)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -507,7 +520,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+            float top = -INFINITY;
+#pragma unroll
+            for (int hf = 0; hf < kGroups; ++hf) top = fmaxf(top, fmaxf(s[hf][nt][e], s[hf][nt][e + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
             top = fmaxf(top, m[nt][e]);
@@ -521,13 +536,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
             }
           }
       }
-      uint32_t pb[2][NT][2];
+      uint32_t pb[kGroups][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float base0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
         const float base1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < kGroups; ++hf) {
           const float p0 = ex2(s[hf][nt][0] - base0), p1 = ex2(s[hf][nt][1] - base1);
           const float p2 = ex2(s[hf][nt][2] - base0), p3 = ex2(s[hf][nt][3] - base1);
           l[nt][0] = fmaf(p0 + p2, sc[hf].z, l[nt][0]);
@@ -539,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
       }
       // O^T += V^T P^T
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < kGroups; ++hf) {
         constexpr int W = D / 32;  // words of a lane's share of a key
         uint32_t v[4][W];
 #pragma unroll
@@ -557,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
             v[kk][1] = x.y ^ 0x80808080u;
           }
         }
-        if (hf == 1) {
+        if (hf == kGroups - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.empty[st]);  // the stage is in registers
         }
@@ -717,7 +732,8 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
 exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream) {
   CUtensorMap km, vm;
   exl3_status st;
-  const int rows = c.page_size < kUnit ? c.page_size : kUnit;
+  const int unit = c.head_dim == 64 ? unit_keys<64>() : unit_keys<128>();
+  const int rows = c.page_size < unit ? c.page_size : unit;
   if ((st = cache_map(&km, c.k, c, rows)) != EXL3_OK || (st = cache_map(&vm, c.v, c, rows)) != EXL3_OK) return st;
   if (c.head_dim == 64) return wide ? launch<64, 2>(p, km, vm, stream) : launch<64, 1>(p, km, vm, stream);
   return wide ? launch<128, 2>(p, km, vm, stream) : launch<128, 1>(p, km, vm, stream);
