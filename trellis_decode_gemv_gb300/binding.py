@@ -144,6 +144,9 @@ def _check(status: int):
 def _ptr(t: torch.Tensor | None, name: str, dtypes, device=None) -> int | None:
     if t is None:
         return None
+    if (t.__class__ is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -161,7 +164,13 @@ _HALF = (torch.float16,)
 _WORDS = (torch.int32, getattr(torch, "uint32", torch.int32))
 
 
+# The current stream's handle without a Stream object around it (0.2 us, not 2).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -791,20 +800,27 @@ def exl3_kv_plan(ctx_len, new_len, tokens, page_size, free_pages, free_state, bl
     if block_table.dim() != 2 or block_table.shape[0] < n or new_len.numel() != n or free_state.numel() < 2:
         raise ValueError(f"{n} requests with new_len of {new_len.numel()}, block_table of {tuple(block_table.shape)} "
                          f"and free_state of {free_state.numel()}")
-    for name, t, least in (("seq_len", seq_len, n), ("q_start", q_start, n + 1), ("slot", slot, tokens),
-                           ("position", position, tokens), ("free_state_out", free_state_out, 3)):
-        if t is not None and t.numel() < least:
-            raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
-    if seq_len is None:
-        seq_len = torch.empty(n, dtype=torch.int32, device=dev)
-    if q_start is None:
-        q_start = torch.empty(n + 1, dtype=torch.int32, device=dev)
+    if seq_len is None and q_start is None and position is None and free_state_out is None:
+        # one allocation for all of them
+        seq_len, q_start, position, free_state_out = torch.empty(
+            2 * n + 4 + tokens, dtype=torch.int32, device=dev).split((n, n + 1, tokens, 3))
+    else:
+        for name, t, least in (("seq_len", seq_len, n), ("q_start", q_start, n + 1), ("position", position, tokens),
+                               ("free_state_out", free_state_out, 3)):
+            if t is not None and t.numel() < least:
+                raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
+        if seq_len is None:
+            seq_len = torch.empty(n, dtype=torch.int32, device=dev)
+        if q_start is None:
+            q_start = torch.empty(n + 1, dtype=torch.int32, device=dev)
+        if position is None:
+            position = torch.empty(tokens, dtype=torch.int32, device=dev)
+        if free_state_out is None:
+            free_state_out = torch.empty(3, dtype=torch.int32, device=dev)
     if slot is None:
         slot = torch.empty(tokens, dtype=torch.int64, device=dev)
-    if position is None:
-        position = torch.empty(tokens, dtype=torch.int32, device=dev)
-    if free_state_out is None:
-        free_state_out = torch.empty(3, dtype=torch.int32, device=dev)
+    elif slot.numel() < tokens:
+        raise ValueError(f"slot holds {slot.numel()} elements, expected {tokens}")
     _check(lib.exl3_kv_plan(
         _ptr(ctx_len, "ctx_len", _I32), _ptr(new_len, "new_len", _I32, dev), n, tokens, page_size,
         _ptr(free_pages, "free_pages", _I32, dev), free_pages.numel(), _ptr(free_state, "free_state", _I32, dev),
@@ -819,17 +835,19 @@ def _rows(t, name, dim, dev):
     apart (a slice of a fused projection's output)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3 or t.shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, heads, {dim}]")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens, heads, {dim}]")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype != torch.float16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float16")
+    tokens, heads, _ = shape
     stride = t.stride()
-    if stride[2] != 1 or (stride[1] != dim and t.shape[1] > 1):
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     # the stride of a single token says nothing
-    return t.data_ptr(), stride[0] if t.shape[0] > 1 else t.shape[1] * dim
+    return t.data_ptr(), stride[0] if tokens > 1 else heads * dim
 
 
 def exl3_kv_append(cache, k, v, slot):
@@ -867,8 +885,9 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
     Returns out (like q), or (out, lse) with lse a float32 tensor [tokens,
     q_heads] to write or True for a new one."""
     dev = cache.device
-    qp, qs = _rows(q, "q", cache.head_dim, dev)
-    tokens, heads = q.shape[0], q.shape[1]
+    dim = cache.head_dim
+    qp, qs = _rows(q, "q", dim, dev)
+    tokens, heads, _ = q.shape
     n = seq_len.numel()
     if block_table.dim() != 2 or block_table.shape[0] < n or q_start.numel() < n + 1:
         raise ValueError(f"{n} requests with q_start of {q_start.numel()} and block_table of {tuple(block_table.shape)}")
@@ -877,18 +896,20 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
     if max_new is None:
         max_new = max(tokens, 1)
     if scale is None:
-        scale = cache.head_dim ** -0.5
+        scale = dim ** -0.5
     if out is None:
-        out = torch.empty((tokens, heads, cache.head_dim), dtype=torch.float16, device=dev)
+        out = torch.empty((tokens, heads, dim), dtype=torch.float16, device=dev)
+        op, os_ = out.data_ptr(), heads * dim
     elif out.shape != q.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    op, os_ = _rows(out, "out", cache.head_dim, dev)
+    else:
+        op, os_ = _rows(out, "out", dim, dev)
     if lse is True:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
     elif lse is not None and lse.shape != (tokens, heads):
         raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(tokens, heads)}")
     if workspace is None:
-        workspace = alloc_attention_workspace(heads, cache.kv_heads, cache.head_dim, max_new, dev)
+        workspace = alloc_attention_workspace(heads, cache.kv_heads, dim, max_new, dev)
     _check(load_library().exl3_attention(
         cache._ref, qp, qs, heads, _ptr(q_start, "q_start", _I32, dev), _ptr(seq_len, "seq_len", _I32, dev), n, tokens,
         max_new, _ptr(block_table, "block_table", _I32, dev), block_table.shape[1], scale, op, os_,

@@ -976,8 +976,8 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   constexpr int kSmem = Cfg<D>::kTiles + static_cast<int>(sizeof(Control));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
-  if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return EXL3_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (!allow_smem(prompt_kernel<D>, kSmem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
   prompt_kernel<D><<<ctas, kThreads, kSmem, stream>>>(p, kmap, vmap, qmap);

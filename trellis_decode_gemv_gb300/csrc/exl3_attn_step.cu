@@ -525,9 +525,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
             for (int hf = 0; hf < kGroups; ++hf) top = fmaxf(top, fmaxf(s[hf][nt][e], s[hf][nt][e + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            top = fmaxf(top, m[nt][e]);
-            const float keep = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - top);
-            m[nt][e] = top;
+            // a row moves its own maximum only: what the other rows of the tile hold (nothing
+            // of any request, past the item's rows) does not change its bits
+            const bool moves = top > m[nt][e] + kSlack;
+            const float keep = moves ? ex2(m[nt][e] - top) : 1.f;   // 0 from a maximum of -inf
+            if (moves) m[nt][e] = top;
             l[nt][e] *= keep;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -719,8 +721,8 @@ template <int D, int NT>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   const size_t smem = sizeof(Shared<D, NT>);
-  if (cudaFuncSetAttribute(step_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return EXL3_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (!allow_smem(step_kernel<D, NT>, smem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count() * C::kCtasPerSm;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   step_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(p, kmap, vmap);

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/exl3.h"
 
 namespace exl3 {
@@ -45,6 +47,19 @@ inline exl3_status launch_status() {
 
 // Number of SMs of the current device (queried once per device).
 int device_sm_count();
+
+// Allows `kernel` its dynamic shared memory on the current device, once for each
+// device (`done` a static of the caller, one bit a device).
+template <typename F>
+inline bool allow_smem(F* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0ull) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 // The driver's tensor-map encoder (nullptr where no driver is installed).
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -189,7 +189,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 
 // ---- append ----------------------------------------------------------------------
 
-constexpr int kAppendThreads = 128;
+// One CTA per (window of tokens, head): the runs (the tokens of this call that go
+// into one page) that begin in the window, one after the other; four warps take the
+// keys, four the values.  A run's values are read once, 16 bytes a lane, and stay in
+// registers between the maximum and the rounding (at most 16 rows of 8 values a
+// lane); the bound is reading 2 bytes and writing 1 per value.
+constexpr int kAppendThreads = 256;
+constexpr int kSideThreads = kAppendThreads / 2;
 
 struct AppendParams {
   exl3_kv_cache c;
@@ -197,66 +203,145 @@ struct AppendParams {
   long long stride[2];
   const int64_t* slot;
   int tokens;
-  int page_shift;
+  int window;          // tokens, a power of two, at most a page
 };
 
-// q = the nearest integer to the binary32 quotient x / s.
-__device__ __forceinline__ int quantize(float x, float s) {
-  return s > 0.f ? __float2int_rn(__fdiv_rn(x, s)) : 0;
+// q = the nearest integer to the binary32 quotient x / s, as the byte at the bottom
+// of the result.  The product with 1 / s is within 2^-15 of the quotient (|q| <= 127),
+// so it rounds to the same integer except next to a tie, and only there (`tie`) the
+// quotient itself is needed.
+__device__ __forceinline__ uint32_t quantize(float x, float inv, bool& tie) {
+  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: the sum's last bits are the integer
+  const float y = __fmul_rn(x, inv);
+  const float z = __fadd_rn(y, kMagic);
+  tie |= fabsf(__fsub_rn(y, __fsub_rn(z, kMagic))) > 0.4999f;
+  return __float_as_uint(z);
 }
 
-// One CTA per (token, head): the CTA of a run's first token (a run: the tokens of
-// this call that go into one page) handles the run.
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  const int t0 = blockIdx.x;
-  const int h = blockIdx.y;
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+__device__ __forceinline__ uint2 quantize8(const uint4& v, float s, float inv) {
+  float x[8];
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+  bool tie = false;
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = quantize(x[i], inv, tie);
+  if (tie) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x[i], s)));
+  }
+  return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+}
+
+template <int D, int SIZE>
+__global__ void __launch_bounds__(kAppendThreads, SIZE <= 32 ? 6 : SIZE == 64 ? 4 : 2) append_kernel(const AppendParams p) {
+  constexpr int kLanes = D / 8;                       // lanes of a row
+  constexpr int kRowsAtOnce = kSideThreads / kLanes;  // 8 or 16
+  constexpr int kMost = SIZE / kRowsAtOnce;           // rows of a lane
+  constexpr int kSideWarps = kSideThreads / 32;
+  static_assert(kMost >= 1 && 2 * SIZE <= kAppendThreads, "a window and the page that its last run reaches into");
+  __shared__ long long slots[kAppendThreads];         // of the tokens from the window's first on
+  __shared__ uint32_t joined[kAppendThreads / 32 + 1];// bit t: token t follows token t - 1 in its page
+  __shared__ uint32_t tops[2][kAppendThreads / 32];
   const int tid = threadIdx.x;
-  const int size = 1 << p.page_shift;
-  const int dim = p.c.head_dim;
-  const long long slots = static_cast<long long>(p.c.pages) << p.page_shift;
-  const long long s0 = p.slot[t0];
-  if (s0 < 0 || s0 >= slots) return;
-  const int off = static_cast<int>(s0 & (size - 1));
-  if (t0 > 0 && off != 0 && p.slot[t0 - 1] == s0 - 1) return;
-  __shared__ int ends;
-  __shared__ uint32_t top;
-  if (tid == 0) ends = size - off;
+  const int side = tid / kSideThreads;                // keys, values
+  const int st = tid % kSideThreads;
+  const long long total = static_cast<long long>(p.c.pages) * SIZE;
+  const int w0 = static_cast<int>(blockIdx.x) * p.window;
+  const int h = blockIdx.y;
+  const long long stride = p.stride[side];
+  const __half* x = p.x[side] + static_cast<size_t>(w0) * stride + static_cast<size_t>(h) * D + (st % kLanes) * 8;
+  const int here = min(p.window, p.tokens - w0);
+  {
+    const int t = w0 + tid;
+    const long long s = t < p.tokens ? p.slot[t] : -1;
+    const long long before = t > 0 && t <= p.tokens ? p.slot[t - 1] : -1;
+    slots[tid] = s;
+    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, s >= 0 && before == s - 1 && (s & (SIZE - 1)) != 0);
+    if ((tid & 31) == 0) joined[tid >> 5] = bits;
+    if (tid == 0) joined[kAppendThreads / 32] = 0u;
+  }
   __syncthreads();
-  for (int j = tid; j < size - off; j += kAppendThreads)
-    if (t0 + j >= p.tokens || p.slot[t0 + j] != s0 + j) atomicMin(&ends, j);
-  __syncthreads();
-  const int n = ends;
-  const long long page = s0 >> p.page_shift;
-  const size_t block = static_cast<size_t>(page) * p.c.kv_heads + h;
-  for (int which = 0; which < 2; ++which) {
-    const __half* x = p.x[which] + static_cast<size_t>(t0) * p.stride[which] + static_cast<size_t>(h) * dim;
-    int8_t* q = (which == 0 ? p.c.k : p.c.v) + block * size * dim;
-    float* scale = (which == 0 ? p.c.k_scale : p.c.v_scale) + block;
-    if (tid == 0) top = 0;
-    __syncthreads();
-    uint32_t m = 0;  // |x| as binary16 bits order as numbers do
-    for (int i = tid; i < n * dim; i += kAppendThreads) {
-      const int r = i / dim;
-      m = max(m, static_cast<uint32_t>(__half_as_ushort(x[static_cast<size_t>(r) * p.stride[which] + (i - r * dim)])) & 0x7FFFu);
+  int parity = 0;
+  for (int i = 0, n; i < here; i += n) {
+    // the tokens from i on that share its page
+    n = 1;
+    {
+      int at = i + 1;
+      uint32_t word = ~joined[at >> 5] & (0xFFFFFFFFu << (at & 31));
+      while (word == 0u) {   // ends: the last word is zero, and a page before it
+        at = (at | 31) + 1;
+        word = ~joined[at >> 5];
+      }
+      n = (at & ~31) + __ffs(static_cast<int>(word)) - 1 - i;
     }
-    atomicMax(&top, m);
+    const long long s0 = slots[i];
+    if (s0 < 0 || s0 >= total) continue;
+    if ((joined[i >> 5] >> (i & 31)) & 1u) continue;   // the run began before this window: its CTA takes it
+    const int off = static_cast<int>(s0 & (SIZE - 1));
+    const size_t block = static_cast<size_t>(s0 / SIZE) * p.c.kv_heads + h;
+    int8_t* page = (side == 0 ? p.c.k : p.c.v) + block * SIZE * D;
+    float* scale = (side == 0 ? p.c.k_scale : p.c.v_scale) + block;
     const float old = off > 0 ? *scale : 0.f;
+    const __half* row = x + static_cast<size_t>(i + st / kLanes) * stride;
+    uint4 v[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      v[k] = st / kLanes + k * kRowsAtOnce < n ? __ldg(reinterpret_cast<const uint4*>(row + static_cast<size_t>(k * kRowsAtOnce) * stride))
+                                               : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t m = 0;   // |x| as binary16 bits order as numbers do
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu), __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    if ((tid & 31) == 0) tops[parity][tid >> 5] = m;
     __syncthreads();
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < kSideWarps; ++k) top = max(top, tops[parity][side * kSideWarps + k]);
+    parity ^= 1;   // the next run's maxima do not meet this one's readers
     float fresh = __fdiv_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(top))), 127.f);
-    fresh = top >= 0x7C00u || old != old ? __int_as_float(0x7FC00000) : fmaxf(old, fresh);
-    if (fresh != old) {
+    const bool bad = top >= 0x7C00u || old != old;
+    fresh = bad ? __int_as_float(0x7FC00000) : fmaxf(old, fresh);
+    const float inv = fresh > 1e-30f ? __frcp_rn(fresh) : 0.f;   // below, every new value is 0
+    if (off > 0 && fresh != old) {
+      // the page's earlier tokens under the larger scale
       const float ratio = fresh > 0.f ? __fdiv_rn(old, fresh) : 0.f;
-      for (int i = tid; i < off * dim; i += kAppendThreads)
-        q[i] = static_cast<int8_t>(__float2int_rn(__fmul_rn(static_cast<float>(q[i]), ratio)));
+      for (int k = st; k < off * (D / 4); k += kSideThreads) {
+        char4* at = reinterpret_cast<char4*>(page) + k;
+        char4 q = *at;
+        q.x = static_cast<signed char>(__float2int_rn(__fmul_rn(static_cast<float>(q.x), ratio)));
+        q.y = static_cast<signed char>(__float2int_rn(__fmul_rn(static_cast<float>(q.y), ratio)));
+        q.z = static_cast<signed char>(__float2int_rn(__fmul_rn(static_cast<float>(q.z), ratio)));
+        q.w = static_cast<signed char>(__float2int_rn(__fmul_rn(static_cast<float>(q.w), ratio)));
+        *at = q;
+      }
     }
-    for (int i = tid; i < n * dim; i += kAppendThreads) {
-      const int r = i / dim;
-      q[off * dim + i] = static_cast<int8_t>(
-          quantize(__half2float(x[static_cast<size_t>(r) * p.stride[which] + (i - r * dim)]), fresh));
-    }
-    __syncthreads();
-    if (tid == 0) *scale = fresh;
-    __syncthreads();
+    int8_t* to = page + (off + st / kLanes) * D + (st % kLanes) * 8;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      if (st / kLanes + k * kRowsAtOnce < n)
+        *reinterpret_cast<uint2*>(to + k * kRowsAtOnce * D) = bad ? make_uint2(0u, 0u) : quantize8(v[k], fresh, inv);
+    if (st == 0) *scale = fresh;
+  }
+}
+
+template <int D>
+void launch_append(const AppendParams& p, dim3 grid, cudaStream_t cs) {
+  switch (p.c.page_size) {
+    case 16: append_kernel<D, 16><<<grid, kAppendThreads, 0, cs>>>(p); break;
+    case 32: append_kernel<D, 32><<<grid, kAppendThreads, 0, cs>>>(p); break;
+    case 64: append_kernel<D, 64><<<grid, kAppendThreads, 0, cs>>>(p); break;
+    default: append_kernel<D, 128><<<grid, kAppendThreads, 0, cs>>>(p); break;
   }
 }
 
@@ -289,10 +374,9 @@ extern "C" exl3_status exl3_kv_plan(const int32_t* ctx_len, const int32_t* new_l
   kv::PlanParams p{ctx_len, new_len, free_pages, free_state, free_state_out, block_table, seq_len, q_start,
                    slot,    position, requests,  tokens,     kv::log2_page(page_size), free_capacity, table_stride};
   const size_t smem = sizeof(int32_t) * (2 * static_cast<size_t>(requests) + 1);
-  if (smem > 48 * 1024 - 256 &&
-      cudaFuncSetAttribute(kv::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-          cudaSuccess)
-    return EXL3_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  constexpr size_t kMost = sizeof(int32_t) * (2 * EXL3_MAX_REQUESTS + 1);
+  if (smem > 48 * 1024 - 256 && !allow_smem(kv::plan_kernel, kMost, allowed)) return EXL3_ERR_CUDA;
   const int sms = device_sm_count();
   const int want = (tokens + kv::kPlanTokensPerCta - 1) / kv::kPlanTokensPerCta;
   const int grid = want < 1 ? 1 : want > sms ? sms : want;
@@ -318,8 +402,17 @@ extern "C" exl3_status exl3_kv_append(const exl3_kv_cache* cache, const exl3_hal
                      {k_stride, v_stride},
                      slot,
                      tokens,
-                     kv::log2_page(cache->page_size)};
-  kv::append_kernel<<<dim3(static_cast<unsigned>(tokens), static_cast<unsigned>(cache->kv_heads)), kv::kAppendThreads,
-                      0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+                     1};
+  // Windows of a page where that leaves enough CTAs for the SMs (prompts), down to
+  // single tokens where it does not (a step's tokens, each in a page of its own).
+  p.window = cache->page_size;
+  const long long enough = 8LL * device_sm_count();
+  while (p.window > 1 && static_cast<long long>(tokens) * cache->kv_heads < enough * p.window) p.window >>= 1;
+  const dim3 grid(static_cast<unsigned>((tokens + p.window - 1) / p.window), static_cast<unsigned>(cache->kv_heads));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->head_dim == 64)
+    kv::launch_append<64>(p, grid, cs);
+  else
+    kv::launch_append<128>(p, grid, cs);
   return launch_status();
 }
