@@ -800,27 +800,18 @@ def exl3_kv_plan(ctx_len, new_len, tokens, page_size, free_pages, free_state, bl
     if block_table.dim() != 2 or block_table.shape[0] < n or new_len.numel() != n or free_state.numel() < 2:
         raise ValueError(f"{n} requests with new_len of {new_len.numel()}, block_table of {tuple(block_table.shape)} "
                          f"and free_state of {free_state.numel()}")
-    if seq_len is None and q_start is None and position is None and free_state_out is None:
-        # one allocation for all of them
-        seq_len, q_start, position, free_state_out = torch.empty(
-            2 * n + 4 + tokens, dtype=torch.int32, device=dev).split((n, n + 1, tokens, 3))
-    else:
-        for name, t, least in (("seq_len", seq_len, n), ("q_start", q_start, n + 1), ("position", position, tokens),
-                               ("free_state_out", free_state_out, 3)):
-            if t is not None and t.numel() < least:
-                raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
-        if seq_len is None:
-            seq_len = torch.empty(n, dtype=torch.int32, device=dev)
-        if q_start is None:
-            q_start = torch.empty(n + 1, dtype=torch.int32, device=dev)
-        if position is None:
-            position = torch.empty(tokens, dtype=torch.int32, device=dev)
-        if free_state_out is None:
-            free_state_out = torch.empty(3, dtype=torch.int32, device=dev)
-    if slot is None:
-        slot = torch.empty(tokens, dtype=torch.int64, device=dev)
-    elif slot.numel() < tokens:
-        raise ValueError(f"slot holds {slot.numel()} elements, expected {tokens}")
+    def room(name, t, count):
+        if t is None:
+            return ctx_len.new_empty(count)
+        if t.numel() < count:
+            raise ValueError(f"{name} holds {t.numel()} elements, expected {count}")
+        return t
+
+    seq_len = room("seq_len", seq_len, n)
+    q_start = room("q_start", q_start, n + 1)
+    slot = room("slot", torch.empty(tokens, dtype=torch.int64, device=dev) if slot is None else slot, tokens)
+    position = room("position", position, tokens)
+    free_state_out = room("free_state_out", free_state_out, 3)
     _check(lib.exl3_kv_plan(
         _ptr(ctx_len, "ctx_len", _I32), _ptr(new_len, "new_len", _I32, dev), n, tokens, page_size,
         _ptr(free_pages, "free_pages", _I32, dev), free_pages.numel(), _ptr(free_state, "free_state", _I32, dev),

@@ -48,7 +48,7 @@ struct Cfg {
   static constexpr int kHalfBytes = kUnit * D;           // K or V of a unit
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kPartStride = D + 4;
-  static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
+  static constexpr int kCtasPerSm = 3;
 };
 
 __device__ __forceinline__ void join_sync() {
@@ -125,9 +125,9 @@ struct Walker {
   Req r;
   int blocks, tiles, head, tile, lo, hi;
 
-  __device__ __forceinline__ Walker(const AttnParams& params, const Edge& from, const Edge& to)
-      : p(params), base(from.b), b(from.b), item(from.item), end_b(to.b), end_item(to.item), end_lo(to.lo), lo(from.lo) {
-    mine = load_req(p, base + (threadIdx.x & 31));
+  // `lanes` holds the requests from `first` on
+  __device__ __forceinline__ Walker(const AttnParams& params, const Edge& from, const Edge& to, int first, const Req& lanes)
+      : p(params), base(first), b(from.b), mine(lanes), item(from.item), end_b(to.b), end_item(to.item), end_lo(to.lo), lo(from.lo) {
     fetch();
     if (lo == blocks) advance();
     place();
@@ -171,8 +171,8 @@ struct Shared {
   using C = Cfg<D, NT>;
   unsigned char ring[C::kStages][C::kStageBytes];  // first: 1024-byte aligned
   __half q[kQSlots][C::kRows * D];
-  float part[kConsumers][C::kRows][C::kPartStride];
-  float pm[kConsumers][C::kRows], pl[kConsumers][C::kRows];
+  float part[kConsumers][8][C::kPartStride];
+  float pm[kConsumers][8], pl[kConsumers][8];
   float4 scale[C::kStages][C::kGroups];   // per 16 keys: PageScale
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t q_full[kQSlots], q_empty[kQSlots];
@@ -251,9 +251,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
 
   // This CTA's range.  Up to 32 requests every warp finds it by itself.
   Edge from, to;
-  int ctas;
+  int ctas, first = 0;
+  Req lanes;
   if (p.requests <= 32) {
     const Req r = load_req(p, lane);
+    lanes = r;
     long long cost = 0, ranges = 0;
     req_cost<D, NT>(p, r, cost, ranges);
     long long inc = cost;
@@ -323,8 +325,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     __syncthreads();
     from = sh.edge[0];
     to = sh.edge[1];
+    first = from.b;
+    lanes = load_req(p, first + lane);
   }
-  Walker<D, NT> w(p, from, to);
+  Walker<D, NT> w(p, from, to, first, lanes);
 
   if (warp == kConsumers) {
     // ---- producer ------------------------------------------------------------------
@@ -598,40 +602,40 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     i += w.hi - w.lo;
 
     // ---- join the warps ---------------------------------------------------------
-    join_sync();  // the last join's readers are done
+    const int rows = min(kRows, w.r.rows - row0);
+    const bool whole = w.lo == 0 && w.hi == w.blocks;
+    constexpr int kQuads = D / 4;  // a thread handles 4 elements of a row at a time
+    float* slot = p.partial + static_cast<size_t>(2 * cta + (w.lo == 0 ? 1 : 0)) * (kRows * (D + 2));
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {   // 8 rows at a time
+      join_sync();  // the readers of the rows before are done
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float sum = l[nt][e];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        const int row = nt * 8 + 2 * t + e;
         if (g == 0) {
-          sh.pm[warp][row] = m[nt][e];
-          sh.pl[warp][row] = sum;
+          sh.pm[warp][2 * t + e] = m[nt][e];
+          sh.pl[warp][2 * t + e] = sum;
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-          *reinterpret_cast<float2*>(&sh.part[warp][row][g * KS * 2 + 2 * k]) = make_float2(o[nt][k][e], o[nt][k][e + 2]);
+          *reinterpret_cast<float2*>(&sh.part[warp][2 * t + e][g * KS * 2 + 2 * k]) = make_float2(o[nt][k][e], o[nt][k][e + 2]);
       }
-    join_sync();
-    const int rows = min(kRows, w.r.rows - row0);
-    const bool whole = w.lo == 0 && w.hi == w.blocks;
-    constexpr int kQuads = D / 4;  // a thread handles 4 elements of a row at a time
-    float* slot = p.partial + static_cast<size_t>(2 * cta + (w.lo == 0 ? 1 : 0)) * (kRows * (D + 2));
-    for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
-      const int row = x / kQuads;
-      const int q4 = x - row * kQuads;
-      float top, sum;
-      const float4 acc = join_warps(sh, row, q4, top, sum);
-      if (whole) {
-        store_out<D>(p, w.r, w.head, row0 + row, q4, acc, top, sum);
-      } else {
-        __stcg(reinterpret_cast<float4*>(slot + row * D) + q4, acc);
-        if (q4 == 0) {
-          __stcg(slot + kRows * D + row, top);
-          __stcg(slot + kRows * D + kRows + row, sum);
+      join_sync();
+      for (int x = tid; x < (rows - 8 * nt) * kQuads && x < 8 * kQuads; x += 32 * kConsumers) {
+        const int row = x / kQuads;
+        const int q4 = x - row * kQuads;
+        float top, sum;
+        const float4 acc = join_warps(sh, row, q4, top, sum);
+        if (whole) {
+          store_out<D>(p, w.r, w.head, row0 + 8 * nt + row, q4, acc, top, sum);
+        } else {
+          __stcg(reinterpret_cast<float4*>(slot + (8 * nt + row) * D) + q4, acc);
+          if (q4 == 0) {
+            __stcg(slot + kRows * D + 8 * nt + row, top);
+            __stcg(slot + kRows * D + kRows + 8 * nt + row, sum);
+          }
         }
       }
     }
@@ -649,66 +653,70 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     join_sync();
     if (sh.last == 0u) continue;
     __threadfence();
-    // Every warp adds up its share of the partial results, all rows at once (a lane
+    // Every warp adds up its share of the partial results, 8 rows at a time (a lane
     // holds 4 columns of several rows); then the warps are joined as above.
     constexpr size_t kSlot = static_cast<size_t>(kRows) * (D + 2);
     constexpr int kLanes = D / 4;              // lanes of a row
     constexpr int kAtOnce = 32 / kLanes;       // rows at a time
-    constexpr int kMine = kRows / kAtOnce;     // rows of a lane
+    constexpr int kMine = 8 / kAtOnce;         // rows of a lane
     const int q4 = lane % kLanes;
-    const int row_of = lane / kLanes;
-    float top[kMine], sum[kMine];
-    float4 acc[kMine];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      top[i] = -INFINITY;
-      sum[i] = 0.f;
-      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll 2
-    for (int k = c0 + warp; k <= c1; k += kConsumers) {
-      const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
-      float pm[kMine], pl[kMine];
-      float4 v[kMine];
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      const int row_of = r0 + lane / kLanes;
+      float top[kMine], sum[kMine];
+      float4 acc[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int row = i * kAtOnce + row_of;
-        pm[i] = -INFINITY;
-        pl[i] = 0.f;
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < rows) {
-          pm[i] = __ldcg(s + kRows * D + row);
-          pl[i] = __ldcg(s + kRows * D + kRows + row);
-          v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
+        top[i] = -INFINITY;
+        sum[i] = 0.f;
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 2
+      for (int k = c0 + warp; k <= c1; k += kConsumers) {
+        const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
+        float pm[kMine], pl[kMine];
+        float4 v[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int row = i * kAtOnce + row_of;
+          pm[i] = -INFINITY;
+          pl[i] = 0.f;
+          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row < rows) {
+            pm[i] = __ldcg(s + kRows * D + row);
+            pl[i] = __ldcg(s + kRows * D + kRows + row);
+            v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const float up = fmaxf(top[i], pm[i]);
+          const float base = up == -INFINITY ? 0.f : up;
+          const float fa = ex2(top[i] - base), fb = ex2(pm[i] - base);
+          top[i] = up;
+          sum[i] = sum[i] * fa + pl[i] * fb;
+          acc[i].x = acc[i].x * fa + v[i].x * fb;
+          acc[i].y = acc[i].y * fa + v[i].y * fb;
+          acc[i].z = acc[i].z * fa + v[i].z * fb;
+          acc[i].w = acc[i].w * fa + v[i].w * fb;
         }
       }
+      join_sync();
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const float up = fmaxf(top[i], pm[i]);
-        const float base = up == -INFINITY ? 0.f : up;
-        const float fa = ex2(top[i] - base), fb = ex2(pm[i] - base);
-        top[i] = up;
-        sum[i] = sum[i] * fa + pl[i] * fb;
-        acc[i].x = acc[i].x * fa + v[i].x * fb;
-        acc[i].y = acc[i].y * fa + v[i].y * fb;
-        acc[i].z = acc[i].z * fa + v[i].z * fb;
-        acc[i].w = acc[i].w * fa + v[i].w * fb;
+        const int row = i * kAtOnce + lane / kLanes;
+        *reinterpret_cast<float4*>(&sh.part[warp][row][4 * q4]) = acc[i];
+        if (q4 == 0) {
+          sh.pm[warp][row] = top[i];
+          sh.pl[warp][row] = sum[i];
+        }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int row = i * kAtOnce + row_of;
-      *reinterpret_cast<float4*>(&sh.part[warp][row][4 * q4]) = acc[i];
-      if (q4 == 0) {
-        sh.pm[warp][row] = top[i];
-        sh.pl[warp][row] = sum[i];
+      join_sync();
+      for (int x = tid; x < (rows - r0) * kQuads && x < 8 * kQuads; x += 32 * kConsumers) {
+        float mx, total;
+        const float4 v = join_warps(sh, x / kQuads, x % kQuads, mx, total);
+        store_out<D>(p, w.r, w.head, row0 + r0 + x / kQuads, x % kQuads, v, mx, total);
       }
-    }
-    join_sync();
-    for (int x = tid; x < rows * kQuads; x += 32 * kConsumers) {
-      float mx, total;
-      const float4 v = join_warps(sh, x / kQuads, x % kQuads, mx, total);
-      store_out<D>(p, w.r, w.head, row0 + x / kQuads, x % kQuads, v, mx, total);
     }
   }
   if (!ok && lane == 0) {
