@@ -266,3 +266,35 @@ def test_many_requests(requests, new):
     news = np.where(rng.random(requests) < 0.1, 0, new)
     x = make(rng, 8, 4, 64, 64, [int(s) for s in np.maximum(seq, news)], [int(n) for n in news])
     check(x, run(x))
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 1, 128), (7, 1, 64), (40, 1, 64)])
+@pytest.mark.parametrize("seq,new", [([1200, 2, 3000], [40, 1, 65]), ([2600], [30]), ([1025, 1024, 1153, 900], [16, 16, 20, 64])])
+def test_items_spread_over_many_blocks(heads, kv_heads, dim, seq, new):
+    """Few rows over long contexts: every tile's keys are split between many thread blocks."""
+    x = make(np.random.default_rng(sum(seq) + heads), heads, kv_heads, dim, 128, seq, new)
+    check(x, run(x))
+
+
+def test_in_a_graph_with_lengths_that_change():
+    """A captured call reads lengths, tables and queries from device memory at every replay."""
+    rng = np.random.default_rng(21)
+    x = make(rng, 8, 2, 64, 32, [700, 333, 90], [1, 1, 1])
+    y = dict(x, seq_len=np.array([650, 1, 64], np.int32), q=np.roll(x["q"], 1, 0))
+    cache = B.Exl3KvCache.from_tensors(cuda(x["k"]), cuda(x["v"]), cuda(x["k_scale"]), cuda(x["v_scale"]))
+    q, start, seq, table = cuda(x["q"]), cuda(x["q_start"]), cuda(x["seq_len"]), cuda(x["block_table"])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = B.alloc_attention_workspace(8, 2, 64, 1, "cuda")
+
+    def call():
+        B.exl3_attention(cache, q, start, seq, table, max_new=1, scale=x["scale"], out=out, lse=lse, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for z in (y, x, y):
+        q.copy_(cuda(z["q"]))
+        seq.copy_(cuda(z["seq_len"]))
+        graph.replay()
+        check(z, (out, lse))

@@ -45,7 +45,7 @@ extern "C" size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int 
   const size_t step = 2 * attn::kMaxCtas * attn::step_slot_floats(head_dim);
   const size_t prompt = 2 * attn::kMaxPromptCtas * attn::prompt_slot_floats(head_dim);
   const bool few = static_cast<long long>(max_new) * (q_heads / kv_heads) <= attn::kStepRows;
-  return attn::arrived_bytes() + (few || step > prompt ? step : prompt) * sizeof(float);
+  return attn::head_bytes() + (few || step > prompt ? step : prompt) * sizeof(float);
 }
 
 extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_half* q, long long q_stride, int q_heads,
@@ -94,7 +94,8 @@ extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_hal
   if (p.most > 0x7FFFFF00LL) p.most = 0x7FFFFF00LL;
   p.status = static_cast<uint32_t*>(workspace);
   p.arrived = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + 256);
-  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + attn::arrived_bytes());
+  p.split = reinterpret_cast<attn::SplitItem*>(p.arrived + attn::kMaxCtas);
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + attn::head_bytes());
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool step = static_cast<long long>(max_new) * p.group <= attn::kStepRows;
   if (step || requests > 1) {

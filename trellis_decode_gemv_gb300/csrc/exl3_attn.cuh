@@ -16,9 +16,9 @@
 // as many units (tiles of keys) as its rows see.  The units of all items, in
 // order, are cut into equal ranges, one for each CTA, whatever the requests'
 // lengths are.  An item inside one range is finished there; one that crosses
-// ranges leaves partial results (m, l and the sums, binary32), and the CTA whose
-// arrival completes the item joins them in the order of the keys, so the result
-// does not depend on which CTA that is.  Everything is computed from the lengths
+// ranges leaves partial results (m, l and the sums, binary32), which the CTA whose
+// arrival completes the item (few rows) or a second kernel (many rows) joins in the
+// order of the keys, so the result does not depend on the order of the CTAs.  Everything is computed from the lengths
 // in device memory.
 #pragma once
 
@@ -41,6 +41,14 @@ constexpr float kSlack = 8.f;     // log2 of the largest P
 constexpr float kTinyScale = -90.f;  // log2 that stands for a value scale of 0: its V add nothing, its P still count in l
 constexpr int kMaxCtas = 160 * 4; // ranges that the workspace has counters for
 
+// An item of the many-rows kernel that begins in a range and ends in a later one.
+struct SplitItem {
+  int t0, n, seq, rows;   // its request
+  int base, head;         // its first row, its key/value head
+  int last;               // the range in which it ends, -1: no such item
+  int unused;
+};
+
 struct AttnParams {
   const __half* q;
   const int32_t* q_start;
@@ -59,7 +67,8 @@ struct AttnParams {
   long long most;          // keys that a table row holds
   int rows_lo, rows_hi;    // requests with rows in [rows_lo, rows_hi] are this launch's
   uint32_t* status;
-  uint32_t* arrived;       // [kMaxCtas], zero between calls: arrivals at the item (or MMA tile of it) that begins in CTA c and ends later
+  uint32_t* arrived;       // [kMaxCtas], zero between calls: few rows, arrivals at the item that begins in CTA c and ends later
+  SplitItem* split;        // [kMaxPromptCtas]: many rows, that item
   float* partial;          // [2 * kMaxCtas] slots: 2c the item that began before CTA c's range, 2c + 1 the one that ends after it
 };
 
@@ -147,8 +156,9 @@ exl3_status cache_map(CUtensorMap* map, const int8_t* base, const exl3_kv_cache&
 // elements in the 128-byte swizzle.
 exl3_status query_map(CUtensorMap* map, const AttnParams& p, int head_dim, int tokens);
 
-// The status word and the arrival counters come first in the workspace.
-constexpr size_t arrived_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas; }
+// The status word, the arrival counters and the split items come first in the workspace.
+constexpr int kMaxPromptCtas = 160;
+constexpr size_t head_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas + sizeof(SplitItem) * kMaxPromptCtas; }
 
 // Up to kStepRows query rows per key/value head, in tiles of at most kStepTile that
 // each read the cache (the later ones from L2).  Against the other kernel, whose
@@ -159,7 +169,6 @@ constexpr int kStepTile = 16;
 constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kStepTile) * (head_dim + 2); }
 
 // More: tiles of 256 rows.
-constexpr int kMaxPromptCtas = 160;
 constexpr size_t prompt_slot_floats(int head_dim) { return static_cast<size_t>(256) * (head_dim + 2); }
 exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStream_t stream);
 exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream);

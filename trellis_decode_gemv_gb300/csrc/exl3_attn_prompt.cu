@@ -57,8 +57,7 @@ constexpr int kConvWarp0 = 20;
 constexpr int kConvThreads = 128;
 constexpr int kThreads = 32 * 24;
 constexpr int kTmemCols = 512;
-constexpr int kTileBarrier = 1;        // + tile: its 256 softmax threads
-constexpr int kPairBarrier = 3;        // + 4 * tile + quarter: the two warps of 32 rows
+constexpr int kPairBarrier = 1;        // + 4 * tile + quarter: the two warps of 32 rows
 constexpr int kHalf = kKeys / 2;       // keys of a softmax thread
 constexpr int kScaleSlots = 4;
 
@@ -81,11 +80,10 @@ struct Control {
   float4 scale[kScaleSlots][kGroups];
   alignas(8) float top[2][2][kTile];          // per tile and half of the keys: a row's largest score; at an item's end its sum
   long long bounds[2];
-  // ranges over which an item is spread: the one that began before this range, the one that ends after it
-  int spread0[2], spread1[2];
+  int last_range;                  // of the item that ends after this range
   Req first_req;
   int first_b, first_tile, first_head, first_lo;
-  uint32_t tmem_base, abort, last[2];
+  uint32_t tmem_base, abort;
 };
 
 __device__ __forceinline__ bool aborted(const Control& c) { return *reinterpret_cast<const volatile uint32_t*>(&c.abort) != 0u; }
@@ -99,9 +97,6 @@ __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t pa
   return false;
 }
 
-__device__ __forceinline__ void tile_sync(int tile) {
-  asm volatile("bar.sync %0, %1;" ::"r"(kTileBarrier + tile), "n"(2 * kTile) : "memory");
-}
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(kPairBarrier + id), "n"(64) : "memory"); }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -201,7 +196,7 @@ __device__ __forceinline__ int tile_units(const AttnParams& p, int n, int seq, i
 // An item of at most kWhole units is not split: leaving and joining partial
 // results takes as long as about six units.  A boundary between ranges that falls
 // into such an item moves to its nearer end.
-constexpr int kWhole = 12;
+constexpr int kWhole = 8;
 constexpr int kLeast = 6;   // units that are worth a range of their own
 // Ranges are cut in equal parts of units plus kItemCost for each item: beginning and
 // ending one (Q, the first scores, the output) takes about as long as that.
@@ -330,8 +325,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
         else
           lo = max(0, lo - kItemCost);
         c.bounds[e] = before_units + static_cast<long long>(head) * len + lo;
-        c.spread0[e] = range_of(cost, start + kItemCost, ctas);
-        c.spread1[e] = range_of(cost, start + kItemCost + len - 1, ctas);
+        if (e == 1) c.last_range = range_of(cost, start + kItemCost + len - 1, ctas);
         if (e == 0) {
           c.first_b = b;
           c.first_tile = x - first[b];
@@ -588,51 +582,69 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
     __stcg(slot + kMAt + r, m);
     __stcg(slot + kLAt + r, l);
   }
-  const int c0 = ctl.spread0[lo == 0 ? 1 : 0], c1 = ctl.spread1[lo == 0 ? 1 : 0];
-  __threadfence();
-  tile_sync(x);
-  if (r == 0 && half == 0) {
-    const bool last = atomicAdd(p.arrived + 2 * c0 + x, 1u) == static_cast<uint32_t>(c1 - c0);
-    ctl.last[x] = last ? 1u : 0u;
-    if (last) p.arrived[2 * c0 + x] = 0u;
-  }
-  tile_sync(x);
-  const bool last = ctl.last[x] != 0u;
-  tile_sync(x);  // before the flag is written again
-  if (last && mine) {
-    __threadfence();
-    auto part = [&](int k) { return p.partial + (static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * 2 + x) * kTileFloats; };
-    float top = -INFINITY, sum = 0.f;
+  // the range in which the item begins tells the join about it
+  if (lo == 0 && x == 0 && half == 0 && r == 0)
+    p.split[blockIdx.x] = SplitItem{req.t0, req.n, req.seq, req.rows, base, head, ctl.last_range, 0};
+}
+
+// Items that are spread over several ranges, after the other kernel: block (c, y) the
+// rows 16 y .. 16 y + 15 of the item that begins in range c.  (Joined by the CTA
+// that finished last, an item over 19 ranges, 2.5 MB of partial sums, took 70 us:
+// one SM reads 64 bytes a clock.)
+constexpr int kJoinRows = 16;
+constexpr int kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const SplitItem it = p.split[c];
+  const int row = static_cast<int>(blockIdx.y) * kJoinRows + threadIdx.x % kJoinRows;   // of the item
+  if (it.last < 0 || it.base + row >= it.rows) return;
+  constexpr int kQuads = D / 4 / (kJoinThreads / kJoinRows);   // 4 or 2 groups of four columns a thread
+  const int quad0 = static_cast<int>(threadIdx.x) / kJoinRows * kQuads;
+  const int x = row / kTile, r = row % kTile;
+  constexpr size_t kTileFloats = static_cast<size_t>(kTile) * (D + 2);
+  const float* first = p.partial + (static_cast<size_t>(2 * c + 1) * 2 + x) * kTileFloats;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc[kQuads];
+#pragma unroll
+  for (int e = 0; e < kQuads; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part(k) + kMAt + r));
-    const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int k = c0; k <= c1; ++k) sum += __ldcg(part(k) + kLAt + r) * ex2(__ldcg(part(k) + kMAt + r) - base);
-    const float inv = inverse_sum(sum, sees);
-#pragma unroll 1
-    for (int ch = 0; ch < D / 32; ++ch) {   // 16 columns
-      uint32_t acc[16];
+  for (int k = c; k <= it.last; ++k) {
+    const float* s = k == c ? first : p.partial + (static_cast<size_t>(2 * k) * 2 + x) * kTileFloats;
+    const float m = __ldcg(s + static_cast<size_t>(D) * kTile + r);
+    const float l = __ldcg(s + static_cast<size_t>(D + 1) * kTile + r);
+    float4 v[kQuads];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] = 0u;
-#pragma unroll 1
-      for (int k = c0; k <= c1; ++k) {
-        const float* q = part(k);
-        float4 v[4];
+    for (int e = 0; e < kQuads; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(s) + static_cast<size_t>(quad0 + e) * kTile + r);
+    const float up = fmaxf(top, m);
+    const float base = up == -INFINITY ? 0.f : up;
+    const float fa = ex2(top - base), fb = ex2(m - base);
+    top = up;
+    sum = sum * fa + l * fb;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(q) + static_cast<size_t>(quad0 + 4 * ch + e) * kTile + r);
-        const float f = ex2(__ldcg(q + kMAt + r) - base);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[4 * e] = __float_as_uint(fmaf(v[e].x, f, __uint_as_float(acc[4 * e])));
-          acc[4 * e + 1] = __float_as_uint(fmaf(v[e].y, f, __uint_as_float(acc[4 * e + 1])));
-          acc[4 * e + 2] = __float_as_uint(fmaf(v[e].z, f, __uint_as_float(acc[4 * e + 2])));
-          acc[4 * e + 3] = __float_as_uint(fmaf(v[e].w, f, __uint_as_float(acc[4 * e + 3])));
-        }
-      }
-      store_row(dst + 16 * ch, acc, inv, sees);
+    for (int e = 0; e < kQuads; ++e) {
+      acc[e].x = acc[e].x * fa + v[e].x * fb;
+      acc[e].y = acc[e].y * fa + v[e].y * fb;
+      acc[e].z = acc[e].z * fa + v[e].z * fb;
+      acc[e].w = acc[e].w * fa + v[e].w * fb;
     }
-    if (lse != nullptr) *lse = sees ? kLn2 * base + logf(sum) : -INFINITY;
   }
+  const int rr = it.base + row;
+  const int tok = rr / p.group;
+  const int h = it.head * p.group + (rr - tok * p.group);
+  const bool sees = it.seq - it.n + tok + 1 > 0;
+  const float inv = inverse_sum(sum, sees);
+  __half* dst = p.out + static_cast<size_t>(it.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * quad0;
+#pragma unroll
+  for (int e = 0; e < kQuads; ++e) {
+    const __half2 q0 = __floats2half2_rn(sees ? acc[e].x * inv : 0.f, sees ? acc[e].y * inv : 0.f);
+    const __half2 q1 = __floats2half2_rn(sees ? acc[e].z * inv : 0.f, sees ? acc[e].w * inv : 0.f);
+    *reinterpret_cast<uint2*>(dst + 4 * e) = make_uint2(*reinterpret_cast<const uint32_t*>(&q0), *reinterpret_cast<const uint32_t*>(&q1));
+  }
+  if (p.lse != nullptr && quad0 == 0)
+    p.lse[static_cast<size_t>(it.t0 + tok) * p.q_heads + h] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
 }
 
 template <int D>
@@ -668,6 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) p.split[blockIdx.x].last = -1;   // no item begins here and ends later, so far
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int ctas, count;
   if (!find_range(p, ctl, smem_raw, ctas, count)) return;
   if (warp == kMmaWarp) tc::tmem_alloc(&ctl.tmem_base, kTmemCols);
@@ -981,6 +995,20 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
   prompt_kernel<D><<<ctas, kThreads, kSmem, stream>>>(p, kmap, vmap, qmap);
+  exl3_status st = launch_status();
+  if (st != EXL3_OK) return st;
+  // a table whose rows hold no item that is ever split leaves nothing to join
+  if (p.most <= static_cast<long long>(kWhole) * kKeys) return EXL3_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), kItemRows / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return EXL3_ERR_CUDA;
   return launch_status();
 }
 
