@@ -200,7 +200,7 @@ constexpr int kWhole = 8;
 constexpr int kLeast = 6;   // units that are worth a range of their own
 // Ranges are cut in equal parts of units plus kItemCost for each item: beginning and
 // ending one (Q, the first scores, the output) takes about as long as that.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 3;
 
 // The items of a range: row tiles in order, the heads of a row tile after one
 // another.
