@@ -140,11 +140,16 @@ __device__ __forceinline__ uint32_t half2_sub1152(uint32_t v) {
 __device__ __forceinline__ uint32_t cvt_lo(uint32_t flipped) { return half2_sub1152(__byte_perm(flipped, 0x64646464u, 0x4140)); }
 __device__ __forceinline__ uint32_t cvt_hi(uint32_t flipped) { return half2_sub1152(__byte_perm(flipped, 0x64646464u, 0x4342)); }
 
-// CTA `c` of `ctas` takes the units [c * units / ctas, (c + 1) * units / ctas).
+// CTA `c` of `ctas` takes the units [c * units / ctas, (c + 1) * units / ctas).  (Of
+// 64-bit divisions, each a few hundred clocks, a short call notices four.)
+constexpr long long kFewUnits = 1LL << 22;   // times kMaxCtas: 32 bits
 __device__ __forceinline__ long long range_begin(long long units, int c, int ctas) {
+  if (units < kFewUnits) return static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas);
   return static_cast<long long>(static_cast<unsigned long long>(units) * c / ctas);
 }
 __device__ __forceinline__ int range_of(long long units, long long u, int ctas) {
+  if (units < kFewUnits)
+    return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(ctas) - 1u) / static_cast<uint32_t>(units));
   return static_cast<int>((static_cast<unsigned long long>(u + 1) * ctas - 1) / units);
 }
 

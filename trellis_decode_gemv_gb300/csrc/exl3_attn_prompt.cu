@@ -239,26 +239,45 @@ struct Walker {
 
 // ---- prelude: units of all items, and where this CTA's range begins -----------------
 
-__device__ __forceinline__ long long block_scan(Control& c, long long v, long long& total) {
-  long long* warp_sum = reinterpret_cast<long long*>(c.top);   // not in use yet
+// Exclusive prefixes of N values over the CTA's threads in place of them, and their
+// totals.  `room`: shared memory of its own, N * 24 numbers; one barrier.
+template <int N>
+__device__ __forceinline__ void block_scan(long long* room, long long (&v)[N], long long (&total)[N]) {
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps <= 32, "a lane for each warp");
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  long long inc = v;
+  long long inc[N];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
+  for (int i = 0; i < N; ++i) inc[i] = v[i];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, inc[i], d);
+      if (lane >= d) inc[i] += o;
+    }
+  if (lane == 31) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) room[i * kWarps + warp] = inc[i];
   }
-  if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  long long before = 0;
-  total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    before += w < warp ? warp_sum[w] : 0;
-    total += warp_sum[w];
+  long long sums[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) sums[i] = lane < kWarps ? room[i * kWarps + lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, sums[i], d);
+      if (lane >= d) sums[i] += o;
+    }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    total[i] = __shfl_sync(0xFFFFFFFFu, sums[i], 31);
+    const long long before = __shfl_sync(0xFFFFFFFFu, sums[i], (warp + 31) & 31);
+    v[i] = inc[i] - v[i] + (warp > 0 ? before : 0);
   }
-  __syncthreads();
-  return before + inc - v;
 }
 
 // `room`: 12 bytes for each request (borrowed from the operand images).  False: the
@@ -269,19 +288,21 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   int2* req = reinterpret_cast<int2*>(first + ((p.requests + 1) & ~1));  // its new tokens (0: another launch's) and length
   const int per = (p.requests + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
-  long long mine = 0, tiles;
+  long long* sums = reinterpret_cast<long long*>(c.top);   // not in use yet
+  long long mine[1] = {0}, tiles[1];
   for (int b = b0; b < b1; ++b) {
     const Req r = load_req(p, b);
     req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq);
-    mine += row_tiles(r.rows);
+    mine[0] += row_tiles(r.rows);
   }
-  long long at = block_scan(c, mine, tiles);
+  block_scan(sums, mine, tiles);
+  long long at = mine[0];
   for (int b = b0; b < b1; ++b) {
     first[b] = static_cast<int32_t>(at);
     at += row_tiles(req[b].x * p.group);
   }
   __syncthreads();
-  const int n = static_cast<int>(tiles);
+  const int n = static_cast<int>(tiles[0]);
   const int share = (n + kThreads - 1) / kThreads;
   const int x0 = min(tid * share, n), x1 = min(x0 + share, n);
   int from = 0, to = p.requests;   // the last request that begins at or before x0
@@ -289,19 +310,19 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
     const int mid = (from + to) >> 1;
     if (first[mid] <= x0) from = mid; else to = mid;
   }
-  long long sum = 0, real = 0, ranges = 0;   // cost, units, ranges that this thread's tiles are worth
+  long long part[3] = {0, 0, 0}, all[3];   // cost, units, ranges that this thread's tiles are worth
   for (int x = x0, b = from; x < x1; ++x) {
     while (b + 1 < p.requests && first[b + 1] <= x) ++b;
     const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
-    sum += static_cast<long long>(len + kItemCost) * p.kv_heads;
-    real += static_cast<long long>(len) * p.kv_heads;
-    ranges += static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads;
+    part[0] += static_cast<long long>(len + kItemCost) * p.kv_heads;
+    part[1] += static_cast<long long>(len) * p.kv_heads;
+    part[2] += static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads;
   }
-  long long cost, units, all_ranges;
-  long long before = block_scan(c, sum, cost);
-  long long before_units = block_scan(c, real, units);
-  block_scan(c, ranges, all_ranges);
-  ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all_ranges));
+  const long long own_cost = part[0];
+  block_scan(sums + 32, part, all);
+  const long long cost = all[0], units = all[1];
+  long long before = part[0], before_units = part[1];
+  ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all[2]));
   const int cta = blockIdx.x;
   if (cta >= ctas) return false;
   const long long u[2] = {range_begin(cost, cta, ctas), range_begin(cost, cta + 1, ctas)};
@@ -309,14 +330,14 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
     c.bounds[1] = units;   // the last range's end is in no item
   }
   __syncthreads();
-  if (before < cost && u[1] >= before && u[0] < before + sum) {
+  if (before < cost && u[1] >= before && u[0] < before + own_cost) {
     for (int x = x0, b = from; x < x1; ++x) {
       while (b + 1 < p.requests && first[b + 1] <= x) ++b;
       const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
-      const long long all = static_cast<long long>(len + kItemCost) * p.kv_heads;
+      const long long of_tile = static_cast<long long>(len + kItemCost) * p.kv_heads;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        if (u[e] < before || u[e] >= before + all) continue;
+        if (u[e] < before || u[e] >= before + of_tile) continue;
         const int head = static_cast<int>((u[e] - before) / (len + kItemCost));
         const long long start = before + static_cast<long long>(head) * (len + kItemCost);
         int lo = static_cast<int>(u[e] - start);
@@ -334,7 +355,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
           c.first_req = load_req(p, b);
         }
       }
-      before += all;
+      before += of_tile;
       before_units += static_cast<long long>(len) * p.kv_heads;
     }
   }
