@@ -74,12 +74,14 @@ __device__ __forceinline__ int req_tiles(const Req& r) { return (r.rows + 8 * NT
 template <int D>
 __device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq + unit_keys<D>() - 1) / unit_keys<D>()); }
 
-// Ranges are cut in equal parts of units plus kItemCost for each item (Q, the join of
-// the warps).  An item of at most kWhole units is not split: a boundary that falls
-// into it moves to its nearer end.
-constexpr int kItemCost = 1;
-constexpr int kWhole = 24;
-constexpr int kLeast = 12;   // units that are worth a range of their own
+// Ranges are cut in equal parts of units plus kItemCost for each item (its Q, the
+// join of the warps).  An item of at most kWhole units is not split: a boundary that
+// falls into it moves to its nearer end.  Measured on 1 to 200 requests of 300 to
+// 131 K keys; with an item counted as one unit 200 requests of up to 600 keys took
+// 45 us, with four 35; with kWhole 24 a single request of 517 keys 10.2, with 12 8.7.
+constexpr int kItemCost = 4;
+constexpr int kWhole = 12;
+constexpr int kLeast = 8;    // units that are worth a range of their own
 
 // What a request's items cost together, and the ranges that they are worth.
 template <int D, int NT>

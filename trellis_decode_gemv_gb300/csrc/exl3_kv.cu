@@ -190,12 +190,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // ---- append ----------------------------------------------------------------------
 
 // One CTA per (window of tokens, head): the runs (the tokens of this call that go
-// into one page) that begin in the window, one after the other; four warps take the
-// keys, four the values.  A run's values are read once, 16 bytes a lane, and stay in
-// registers between the maximum and the rounding (at most 16 rows of 8 values a
-// lane); the bound is reading 2 bytes and writing 1 per value.
-constexpr int kAppendThreads = 256;
-constexpr int kSideThreads = kAppendThreads / 2;
+// into one page) that begin in the window, one after the other; half of the threads
+// take the keys, half the values.  A run's values are read once, 16 bytes a lane, and
+// stay in registers between the maximum and the rounding.  The bound is reading 2
+// bytes and writing 1 per value, with issuing the rounding (5 instructions a value)
+// close behind it: a side of a page is at most 64 threads with up to 16 rows each,
+// not more threads with fewer, which spent as much again on addresses and the run.
+template <int SIZE>
+constexpr int append_threads() { return SIZE < 32 ? 64 : 2 * SIZE; }
 
 struct AppendParams {
   exl3_kv_cache c;
@@ -206,44 +208,44 @@ struct AppendParams {
   int window;          // tokens, a power of two, at most a page
 };
 
-// q = the nearest integer to the binary32 quotient x / s, as the byte at the bottom
-// of the result.  The product with 1 / s is within 2^-15 of the quotient (|q| <= 127),
-// so it rounds to the same integer except next to a tie, and only there (`tie`) the
-// quotient itself is needed.
-__device__ __forceinline__ uint32_t quantize(float x, float inv, bool& tie) {
-  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: the sum's last bits are the integer
-  const float y = __fmul_rn(x, inv);
-  const float z = __fadd_rn(y, kMagic);
-  tie |= fabsf(__fsub_rn(y, __fsub_rn(z, kMagic))) > 0.4999f;
-  return __float_as_uint(z);
-}
-
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// Eight values to the nearest integers to their binary32 quotients by s.  The quotient
+// lies between the products with 1 / s a little enlarged and a little reduced (by
+// 2^-21, more than the three roundings together); where both round to the same
+// integer so does it, and only next to a tie the division is needed.
 __device__ __forceinline__ uint2 quantize8(const uint4& v, float s, float inv) {
-  float x[8];
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float more = inv * (1.f + 0x1p-21f), less = inv * (1.f - 0x1p-21f);
+  const uint64_t hi = pair(more, more), lo = pair(less, less);
+  const uint64_t magic = pair(12582912.f, 12582912.f);   // 1.5 * 2^23: a sum's last bits are the integer
+  uint32_t q[8], differ = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    const uint64_t x = pair(f.x, f.y);
+    const uint64_t a = add2(mul2(x, hi), magic), b = add2(mul2(x, lo), magic);
+    q[2 * i] = static_cast<uint32_t>(a);
+    q[2 * i + 1] = static_cast<uint32_t>(a >> 32);
+    differ |= (q[2 * i] ^ static_cast<uint32_t>(b)) | (q[2 * i + 1] ^ static_cast<uint32_t>(b >> 32));
   }
-  bool tie = false;
-  uint32_t q[8];
+  if (differ != 0u) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quantize(x[i], inv, tie);
-  if (tie) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x[i], s)));
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      q[2 * i] = static_cast<uint32_t>(__float2int_rn(__fdiv_rn(f.x, s)));
+      q[2 * i + 1] = static_cast<uint32_t>(__float2int_rn(__fdiv_rn(f.y, s)));
+    }
   }
   return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
 }
 
 template <int D, int SIZE>
-__global__ void __launch_bounds__(kAppendThreads, SIZE <= 32 ? 6 : SIZE == 64 ? 4 : 2) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(append_threads<SIZE>()) append_kernel(const AppendParams p) {
+  constexpr int kAppendThreads = append_threads<SIZE>();
+  constexpr int kSideThreads = kAppendThreads / 2;
   constexpr int kLanes = D / 8;                       // lanes of a row
   constexpr int kRowsAtOnce = kSideThreads / kLanes;  // 8 or 16
   constexpr int kMost = SIZE / kRowsAtOnce;           // rows of a lane
@@ -298,10 +300,14 @@ __global__ void __launch_bounds__(kAppendThreads, SIZE <= 32 ? 6 : SIZE == 64 ? 
     for (int k = 0; k < kMost; ++k)
       v[k] = st / kLanes + k * kRowsAtOnce < n ? __ldg(reinterpret_cast<const uint4*>(row + static_cast<size_t>(k * kRowsAtOnce) * stride))
                                                : make_uint4(0u, 0u, 0u, 0u);
-    uint32_t m = 0;   // |x| as binary16 bits order as numbers do
+    __half2 most = __float2half2_rn(0.f);
 #pragma unroll
-    for (int k = 0; k < kMost; ++k)
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu), __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
+    for (int k = 0; k < kMost; ++k) {
+      const __half2* w = reinterpret_cast<const __half2*>(&v[k]);
+      most = __hmax2_nan(most, __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])), __hmax2_nan(__habs2(w[2]), __habs2(w[3]))));
+    }
+    // |x| as binary16 bits order as numbers do, infinity and NaN above them
+    uint32_t m = *reinterpret_cast<const uint32_t*>(&most) & 0x7FFF7FFFu;
     m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
     if ((tid & 31) == 0) tops[parity][tid >> 5] = m;
     __syncthreads();
@@ -338,10 +344,10 @@ __global__ void __launch_bounds__(kAppendThreads, SIZE <= 32 ? 6 : SIZE == 64 ? 
 template <int D>
 void launch_append(const AppendParams& p, dim3 grid, cudaStream_t cs) {
   switch (p.c.page_size) {
-    case 16: append_kernel<D, 16><<<grid, kAppendThreads, 0, cs>>>(p); break;
-    case 32: append_kernel<D, 32><<<grid, kAppendThreads, 0, cs>>>(p); break;
-    case 64: append_kernel<D, 64><<<grid, kAppendThreads, 0, cs>>>(p); break;
-    default: append_kernel<D, 128><<<grid, kAppendThreads, 0, cs>>>(p); break;
+    case 16: append_kernel<D, 16><<<grid, append_threads<16>(), 0, cs>>>(p); break;
+    case 32: append_kernel<D, 32><<<grid, append_threads<32>(), 0, cs>>>(p); break;
+    case 64: append_kernel<D, 64><<<grid, append_threads<64>(), 0, cs>>>(p); break;
+    default: append_kernel<D, 128><<<grid, append_threads<128>(), 0, cs>>>(p); break;
   }
 }
 
