@@ -167,9 +167,11 @@ constexpr size_t head_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas + sizeo
 
 // Up to kStepRows query rows per key/value head, in tiles of at most kStepTile that
 // each read the cache (the later ones from L2).  Against the other kernel, whose
-// tiles of 128 rows are mostly empty then: 32 rows 62 us to 89 (16 requests of 4000
-// keys) and 39 to 93 (one of 32000), 64 rows 107 to 90 and 60 to 93, 128 rows 199 to 91.
-constexpr int kStepRows = 64;
+// tiles of 128 rows are mostly empty then: 32 rows 62 us to 82 (16 requests of 4000
+// keys) and 39 to 50 (one of 32000), 64 rows 107 to 83 and 60 to 50.  (One tile of 32
+// rows, which widens every byte once, took 60 and 53 us: its registers leave six
+// warps to an SM, and their latencies show.)
+constexpr int kStepRows = 48;
 constexpr int kStepTile = 16;
 constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kStepTile) * (head_dim + 2); }
 
