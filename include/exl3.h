@@ -528,6 +528,8 @@ exl3_status exl3_device_status(const void *status_word, exl3_stream_t stream);
  * names, in order.  Keys and values are int8, symmetric, with one binary32 scale
  * for each page and head: value = q * scale, the largest |value| a page has held
  * over 127 (the quantizer of exl3_quantize_act, its block a page of one head).
+ * Scales are non-negative (exl3_kv_append writes no others) and finite, but for
+ * the NaN of a page that took an infinity or a NaN.
  * One step of a server is exl3_kv_plan once, then for every layer
  * exl3_kv_append and exl3_attention on that layer's cache.  All lengths, tables
  * and maps are device memory: nothing of a step waits for the host, and a step
@@ -610,6 +612,8 @@ exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_half *k, long 
  * request: a status word (first 256 bytes), arrival counters, then the partial
  * results of the work that is split between thread blocks.  It must be
  * zero-filled once after allocation; every call leaves the counters zero again.
+ * A wait inside a kernel that runs out ends the call without its results and sets the
+ * status word (exl3_device_status reads it, as any workspace's).
  * Two calls that may run concurrently must not share one.  0 for invalid
  * heads, head_dim or max_new < 1.
  */
@@ -634,7 +638,8 @@ size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, i
  * The scores, the softmax statistics and the sums are binary32; the int8 keys
  * and values enter the products exactly (as binary16 integers) and the
  * probabilities rounded to binary16, relative to the row's largest p_j * v_scale.
- * The result does not depend on the order in which thread blocks run.
+ * The result does not depend on the order in which thread blocks run.  One to
+ * three launches.
  * Errors: EXL3_ERR_NULL, EXL3_ERR_SHAPE (cache fields, q_heads not a multiple of
  * kv_heads, strides, table_stride < 1), EXL3_ERR_BATCH (requests outside
  * 0..EXL3_MAX_REQUESTS, tokens < 0, max_new < 1), EXL3_ERR_ALIGN,

@@ -12,29 +12,41 @@
 // softmax warps of one tile work, the MMAs of the other run.
 //
 // Warp roles (24 warps):
-//   0-7, 8-15 softmax of tile A and B: two threads share a row (its TMEM lane), one
+//   0         MMA issue (one lane) and TMEM allocation.
+//   1         producer: page numbers and scales (two units ahead), tensor copies of
+//             the int8 tiles.  Pages may be smaller than a unit: one copy per page,
+//             scales per 16 keys.
+//   2, 3      Q of the next item (A, B) into shared memory as soon as the last
+//             scores of the current one are computed.
+//   4-11, 12-19 softmax of tile A and B: two threads share a row (its TMEM lane), one
 //             for each 64 keys of a unit and each half of O's columns; their warps
 //             exchange the row's largest score.  They also take O out.  O is only
 //             rescaled when a score passes the running maximum by 2^8, by these
 //             threads, between the MMAs that add to it.
-//   16-19     widening: int8 tiles in shared memory into binary16 operand images,
+//   20-23     widening: int8 tiles in shared memory into binary16 operand images,
 //             two of K and two of V.  Both are [key][D] rows of 64-element,
 //             128-byte pieces in the 128-byte swizzle: K is read as a K-major
 //             operand, V as an MN-major one, so V needs no transposition.
-//   20        MMA issue (one lane) and TMEM allocation.
-//   21        producer: page numbers and scales (three units ahead), tensor copies
-//             of the int8 tiles.  Pages may be smaller than a unit: one copy per
-//             page, scales per 16 keys.
-//   22, 23    Q of the next item (A, B) into shared memory as soon as the last
-//             scores of the current one are computed.
 //
-// Barriers: int8 K and V tiles full/empty, K and V images full, the MMAs
-// that read them done, scales full
-// (four slots: a slot is rewritten only after the softmax of both tiles has used
-// it), per tile Q full/empty, S full, P full, product done, O done.  Every wait is
-// bounded; on timeout the CTA sets its abort flag and the status word, every role
-// stops waiting, the MMA lane waits (bounded) for its MMAs and the producer for its
-// copies, TMEM is freed.
+// Barriers: int8 K and V tiles full/empty, K and V images full, a unit's MMAs done
+// (its images are free), scales full (four slots: a slot is rewritten only after
+// the softmax of both tiles has used it), per tile Q full/empty, S full, P full (by
+// half of the keys), product done, O done.  Every wait is bounded; on timeout the
+// CTA sets its abort flag and the status word, every role stops waiting, the MMA
+// lane waits (bounded) for its MMAs and the producer for its copies, TMEM is freed.
+//
+// Measured (2070 MHz, 32 heads over 8, D = 128): a prompt of 8192 tokens 478 us, 1150
+// Tflop/s, the tensor pipe active for half of the cycles; four chunks of 512 tokens
+// after 32K 899 us, 1204 Tflop/s.  An MMA of 128 x 128 x 16 takes 64 clocks, so a
+// unit's 32 take 2048 at D = 128, and a unit takes about 4000.  Two chains bound it:
+// a tile's S, softmax, P V one after another, because P lies in place of S and the
+// next S must wait for the product; and shared memory, which feeds two operands of S,
+// one of P V, the widening and its stores (about 2700 clocks a unit).  Small code
+// matters: with the loops rolled (the 24 warps run five different ones) the
+// instruction cache stopped missing, the most of the way from 1542 us to 898 for the
+// prompt of 8192 when it was first measured.  128 scores a thread spill; a second MMA
+// thread (1255 us where one took 911) and scores fetched ahead of their use (spills)
+// were slower.
 #include "exl3_attn.cuh"
 
 namespace exl3 {
@@ -80,7 +92,7 @@ struct Control {
   float4 scale[kScaleSlots][kGroups];
   alignas(8) float top[2][2][kTile];          // per tile and half of the keys: a row's largest score; at an item's end its sum
   long long bounds[2];
-  int last_range;                  // of the item that ends after this range
+  int last_range;                             // of the item that ends after this range
   Req first_req;
   int first_b, first_tile, first_head, first_lo;
   uint32_t tmem_base, abort;

@@ -22,6 +22,14 @@
 // permutes that widen them also pair the keys.  P^T comes from S^T by one 8x8
 // transposition (movmatrix).  The tensor copies swizzle 16-byte pieces, so both
 // reads are free of bank conflicts for D = 128.
+//
+// Measured (64 requests of 4096 keys, 32 heads over 8): D = 128 94 us, 5.7 TB/s of
+// keys and values, read once (543.7 MB of DRAM traffic for 541); D = 64 57 us, 4.7
+// TB/s.  Instructions issue in 42% of the cycles, so it is neither they nor the
+// bytes alone: 9 consumer warps an SM (168 registers, three CTAs) hide their own
+// latencies only in part.  One request of 131K keys takes 59 us where its 268.6 MB
+// need 40: its units are done after 38 us for most CTAs, and the 57 partial results
+// of each head, joined by the last arrival, add about 10.
 #include "exl3_attn.cuh"
 
 namespace exl3 {
