@@ -407,14 +407,20 @@ __device__ __forceinline__ void widen(const unsigned char* tile, uint32_t image,
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Largest of 16 scores.
 __device__ __forceinline__ float max16(const uint32_t* a) {
   float m[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    m[i] = fmaxf(fmaxf(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1])),
-                 fmaxf(__uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3])));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  for (int i = 0; i < 4; ++i) m[i] = max3(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]), __uint_as_float(a[4 * i + 2]));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) m[i] = max3(m[i], m[i + 2], __uint_as_float(a[4 * i + 3]));
+  return fmaxf(max3(m[0], m[1], __uint_as_float(a[11])), __uint_as_float(a[15]));
 }
 
 // Largest x = c ks s + log2 vs (c ks >= 0) of 16 scores of one scale; `left`: how
