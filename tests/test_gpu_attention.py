@@ -298,3 +298,18 @@ def test_in_a_graph_with_lengths_that_change():
         seq.copy_(cuda(z["seq_len"]))
         graph.replay()
         check(z, (out, lse))
+
+
+@pytest.mark.parametrize("heads,dim", [(8, 128), (16, 128), (5, 64), (12, 64)])
+@pytest.mark.parametrize("seq", [[4500], [17000], [68000], [9000, 30, 5200], [3000, 2999, 3, 1, 8000]])
+def test_long_requests_over_many_blocks(heads, dim, seq):
+    """One key/value head: an item's partial results come from up to a few hundred blocks, joined in one step or two.
+    Twice from one workspace with the same bits, the counters left zero."""
+    x = make(np.random.default_rng(len(seq) + seq[0]), heads, 1, dim, 64, seq, [1] * len(seq))
+    ws = B.alloc_attention_workspace(heads, 1, dim, 1, "cuda")
+    first = run(x, workspace=ws)
+    check(x, first)
+    second = run(x, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(first, second))
+    head = ws[:256 + 4 * 3 * 640].view(torch.int32)   # the status word, the arrival counters
+    assert int(head.abs().sum()) == 0

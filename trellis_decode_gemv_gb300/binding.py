@@ -802,7 +802,7 @@ def exl3_kv_plan(ctx_len, new_len, tokens, page_size, free_pages, free_state, bl
                          f"and free_state of {free_state.numel()}")
     def room(name, t, count):
         if t is None:
-            return ctx_len.new_empty(count)
+            return torch.empty(count, dtype=torch.int32, device=dev)   # new_empty takes twice as long
         if t.numel() < count:
             raise ValueError(f"{name} holds {t.numel()} elements, expected {count}")
         return t

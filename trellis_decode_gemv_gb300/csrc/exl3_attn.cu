@@ -94,7 +94,7 @@ extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_hal
   if (p.most > 0x7FFFFF00LL) p.most = 0x7FFFFF00LL;
   p.status = static_cast<uint32_t*>(workspace);
   p.arrived = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + 256);
-  p.split = reinterpret_cast<attn::SplitItem*>(p.arrived + attn::kMaxCtas);
+  p.split = reinterpret_cast<attn::SplitItem*>(p.arrived + attn::kCounters);
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + attn::head_bytes());
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool step = static_cast<long long>(max_new) * p.group <= attn::kStepRows;

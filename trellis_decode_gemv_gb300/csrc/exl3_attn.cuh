@@ -67,7 +67,9 @@ struct AttnParams {
   long long most;          // keys that a table row holds
   int rows_lo, rows_hi;    // requests with rows in [rows_lo, rows_hi] are this launch's
   uint32_t* status;
-  uint32_t* arrived;       // [kMaxCtas], zero between calls: few rows, arrivals at the item that begins in CTA c and ends later
+  // few rows, zero between calls: [kMaxCtas] arrivals at the item that begins in CTA c and ends later, then
+  // [2 * kMaxCtas] at the part of an item that begins with slot 2c, 2c + 1 of `partial`
+  uint32_t* arrived;
   SplitItem* split;        // [kMaxPromptCtas]: many rows, that item
   float* partial;          // [2 * kMaxCtas] slots: 2c the item that began before CTA c's range, 2c + 1 the one that ends after it
 };
@@ -163,7 +165,8 @@ exl3_status query_map(CUtensorMap* map, const AttnParams& p, int head_dim, int t
 
 // The status word, the arrival counters and the split items come first in the workspace.
 constexpr int kMaxPromptCtas = 160;
-constexpr size_t head_bytes() { return 256 + sizeof(uint32_t) * kMaxCtas + sizeof(SplitItem) * kMaxPromptCtas; }
+constexpr int kCounters = 3 * kMaxCtas;
+constexpr size_t head_bytes() { return 256 + sizeof(uint32_t) * kCounters + sizeof(SplitItem) * kMaxPromptCtas; }
 
 // Up to kStepRows query rows per key/value head, in tiles of at most kStepTile that
 // each read the cache (the later ones from L2).  Against the other kernel, whose

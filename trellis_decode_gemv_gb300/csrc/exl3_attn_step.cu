@@ -36,19 +36,21 @@ namespace exl3 {
 namespace attn {
 namespace {
 
-constexpr int kConsumers = 3;
-constexpr int kThreads = 32 * (kConsumers + 1);
 // Keys of a unit: 4 KB of K and of V, whatever the head dimension (32 keys of 64
 // elements are too little for what a unit costs besides: 68 us for 64 requests of
 // 4096 keys and 8 heads, where 64 keys take 57).
 template <int D>
 constexpr int unit_keys() { return 4096 / D; }
 constexpr int kQSlots = 2;
+constexpr int kJoinOnce = 24;   // partial results that are joined in one step
 constexpr int kJoinBarrier = 1;
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
+  static constexpr int kConsumers = 3;
+  static constexpr int kThreads = 32 * (kConsumers + 1);
+  static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
   static constexpr int kStages = 6;
   static_assert(kStages % kConsumers == 0, "each stage belongs to one consumer, so that no parity wait skips a phase");
   static constexpr int kUnit = unit_keys<D>();
@@ -56,9 +58,9 @@ struct Cfg {
   static constexpr int kHalfBytes = kUnit * D;           // K or V of a unit
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kPartStride = D + 4;
-  static constexpr int kCtasPerSm = 3;
 };
 
+template <int kConsumers>
 __device__ __forceinline__ void join_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(kJoinBarrier), "n"(32 * kConsumers) : "memory");
 }
@@ -181,6 +183,7 @@ struct Shared {
   using C = Cfg<D, NT>;
   unsigned char ring[C::kStages][C::kStageBytes];  // first: 1024-byte aligned
   __half q[kQSlots][C::kRows * D];
+  static constexpr int kConsumers = C::kConsumers, kThreads = C::kThreads;
   float part[kConsumers][8][C::kPartStride];
   float pm[kConsumers][8], pl[kConsumers][8];
   float4 scale[C::kStages][C::kGroups];   // per 16 keys: PageScale
@@ -194,6 +197,7 @@ struct Shared {
 // The consumers' sums of a row, 4 columns of it: with the row's maximum and sum.
 template <int D, int NT>
 __device__ __forceinline__ float4 join_warps(const Shared<D, NT>& sh, int row, int q4, float& top, float& sum) {
+  constexpr int kConsumers = Cfg<D, NT>::kConsumers;
   top = -INFINITY;
 #pragma unroll
   for (int k = 0; k < kConsumers; ++k) top = fmaxf(top, sh.pm[k][row]);
@@ -229,12 +233,23 @@ __device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, int
     p.lse[static_cast<size_t>(r.t0 + tok) * p.q_heads + h] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
 }
 
+// 4 columns of a row of a partial result.
+template <int D, int ROWS>
+__device__ __forceinline__ void leave(float* slot, int row, int q4, const float4& acc, float top, float sum) {
+  __stcg(reinterpret_cast<float4*>(slot + row * D) + q4, acc);
+  if (q4 == 0) {
+    __stcg(slot + ROWS * D + row, top);
+    __stcg(slot + ROWS * D + ROWS + row, sum);
+  }
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     step_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, NT>;
   constexpr int kRows = C::kRows;
+  constexpr int kConsumers = C::kConsumers, kThreads = C::kThreads;
   constexpr int kStages = C::kStages;
   constexpr int kUnit = C::kUnit;
   constexpr int kGroups = C::kGroups;
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     float* slot = p.partial + static_cast<size_t>(2 * cta + (w.lo == 0 ? 1 : 0)) * (kRows * (D + 2));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {   // 8 rows at a time
-      join_sync();  // the readers of the rows before are done
+      join_sync<kConsumers>();  // the readers of the rows before are done
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float sum = l[nt][e];
@@ -632,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         for (int k = 0; k < KS; ++k)
           *reinterpret_cast<float2*>(&sh.part[warp][2 * t + e][g * KS * 2 + 2 * k]) = make_float2(o[nt][k][e], o[nt][k][e + 2]);
       }
-      join_sync();
+      join_sync<kConsumers>();
       for (int x = tid; x < (rows - 8 * nt) * kQuads && x < 8 * kQuads; x += 32 * kConsumers) {
         const int row = x / kQuads;
         const int q4 = x - row * kQuads;
@@ -641,92 +656,114 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         if (whole) {
           store_out<D>(p, w.r, w.head, row0 + 8 * nt + row, q4, acc, top, sum);
         } else {
-          __stcg(reinterpret_cast<float4*>(slot + (8 * nt + row) * D) + q4, acc);
-          if (q4 == 0) {
-            __stcg(slot + kRows * D + 8 * nt + row, top);
-            __stcg(slot + kRows * D + kRows + 8 * nt + row, sum);
-          }
+          leave<D, kRows>(slot, 8 * nt + row, q4, acc, top, sum);
         }
       }
     }
     if (whole) continue;
 
     // ---- the item crosses ranges: the last to arrive joins --------------------------
+    // Many ranges in two levels: the last of 8, 16 or 32 neighbours joins theirs into
+    // the first one's slot, the last of those that joined puts the rest together.
     const int c0 = w.lo == 0 ? to.c0 : from.c0, c1 = w.lo == 0 ? to.c1 : from.c1;
-    __threadfence();
-    join_sync();
-    if (tid == 0) {
-      const uint32_t before_me = atomicAdd(p.arrived + c0, 1u);
-      sh.last = before_me == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
-      if (sh.last != 0u) p.arrived[c0] = 0u;
+    const int spread = c1 - c0 + 1;
+    const bool two = spread > kJoinOnce;
+    const int some = spread <= 64 ? 3 : spread <= 256 ? 4 : 5;   // its logarithm
+    int k0 = c0, k1 = c1, step = 1;
+    uint32_t* count = p.arrived + c0;
+    if (two) {
+      k0 += (cta - c0) >> some << some;
+      k1 = min(k0 + (1 << some) - 1, c1);
+      count = p.arrived + kMaxCtas + 2 * k0 + (k0 == c0 ? 1 : 0);
     }
-    join_sync();
-    if (sh.last == 0u) continue;
-    __threadfence();
-    // Every warp adds up its share of the partial results, 8 rows at a time (a lane
-    // holds 4 columns of several rows); then the warps are joined as above.
-    constexpr size_t kSlot = static_cast<size_t>(kRows) * (D + 2);
-    constexpr int kLanes = D / 4;              // lanes of a row
-    constexpr int kAtOnce = 32 / kLanes;       // rows at a time
-    constexpr int kMine = 8 / kAtOnce;         // rows of a lane
-    const int q4 = lane % kLanes;
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      const int row_of = r0 + lane / kLanes;
-      float top[kMine], sum[kMine];
-      float4 acc[kMine];
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        top[i] = -INFINITY;
-        sum[i] = 0.f;
-        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    uint32_t others = static_cast<uint32_t>(k1 - k0);
+    for (;;) {
+      __threadfence();
+      join_sync<kConsumers>();
+      if (tid == 0) {
+        const uint32_t before_me = atomicAdd(count, 1u);
+        sh.last = before_me == others ? 1u : 0u;
+        if (sh.last != 0u) *count = 0u;
       }
-#pragma unroll 2
-      for (int k = c0 + warp; k <= c1; k += kConsumers) {
-        const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
-        float pm[kMine], pl[kMine];
-        float4 v[kMine];
+      join_sync<kConsumers>();
+      if (sh.last == 0u) break;
+      __threadfence();
+      const bool rest = step > 1 || !two;   // nothing is left to join after this
+      // Every warp adds up its share of the partial results, 8 rows at a time (a lane
+      // holds 4 columns of several rows); then the warps are joined as above.
+      constexpr size_t kSlot = static_cast<size_t>(kRows) * (D + 2);
+      constexpr int kLanes = D / 4;              // lanes of a row
+      constexpr int kAtOnce = 32 / kLanes;       // rows at a time
+      constexpr int kMine = 8 / kAtOnce;         // rows of a lane
+      const int q4 = lane % kLanes;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+        const int row_of = r0 + lane / kLanes;
+        float top[kMine], sum[kMine];
+        float4 acc[kMine];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const int row = i * kAtOnce + row_of;
-          pm[i] = -INFINITY;
-          pl[i] = 0.f;
-          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (row < rows) {
-            pm[i] = __ldcg(s + kRows * D + row);
-            pl[i] = __ldcg(s + kRows * D + kRows + row);
-            v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
+          top[i] = -INFINITY;
+          sum[i] = 0.f;
+          acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 2
+        for (int k = k0 + warp * step; k <= k1; k += kConsumers * step) {
+          const float* s = p.partial + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * kSlot;
+          float pm[kMine], pl[kMine];
+          float4 v[kMine];
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int row = i * kAtOnce + row_of;
+            pm[i] = -INFINITY;
+            pl[i] = 0.f;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < rows) {
+              pm[i] = __ldcg(s + kRows * D + row);
+              pl[i] = __ldcg(s + kRows * D + kRows + row);
+              v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * D) + q4);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const float up = fmaxf(top[i], pm[i]);
+            const float base = up == -INFINITY ? 0.f : up;
+            const float fa = ex2(top[i] - base), fb = ex2(pm[i] - base);
+            top[i] = up;
+            sum[i] = sum[i] * fa + pl[i] * fb;
+            acc[i].x = acc[i].x * fa + v[i].x * fb;
+            acc[i].y = acc[i].y * fa + v[i].y * fb;
+            acc[i].z = acc[i].z * fa + v[i].z * fb;
+            acc[i].w = acc[i].w * fa + v[i].w * fb;
           }
         }
+        join_sync<kConsumers>();
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const float up = fmaxf(top[i], pm[i]);
-          const float base = up == -INFINITY ? 0.f : up;
-          const float fa = ex2(top[i] - base), fb = ex2(pm[i] - base);
-          top[i] = up;
-          sum[i] = sum[i] * fa + pl[i] * fb;
-          acc[i].x = acc[i].x * fa + v[i].x * fb;
-          acc[i].y = acc[i].y * fa + v[i].y * fb;
-          acc[i].z = acc[i].z * fa + v[i].z * fb;
-          acc[i].w = acc[i].w * fa + v[i].w * fb;
+          const int row = i * kAtOnce + lane / kLanes;
+          *reinterpret_cast<float4*>(&sh.part[warp][row][4 * q4]) = acc[i];
+          if (q4 == 0) {
+            sh.pm[warp][row] = top[i];
+            sh.pl[warp][row] = sum[i];
+          }
+        }
+        join_sync<kConsumers>();
+        for (int x = tid; x < (rows - r0) * kQuads && x < 8 * kQuads; x += 32 * kConsumers) {
+          float mx, total;
+          const int row = x / kQuads, col = x % kQuads;
+          const float4 v = join_warps(sh, row, col, mx, total);
+          if (rest)
+            store_out<D>(p, w.r, w.head, row0 + r0 + row, col, v, mx, total);
+          else
+            leave<D, kRows>(p.partial + static_cast<size_t>(2 * k0 + (k0 == c0 ? 1 : 0)) * kSlot, r0 + row, col, v, mx, total);
         }
       }
-      join_sync();
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int row = i * kAtOnce + lane / kLanes;
-        *reinterpret_cast<float4*>(&sh.part[warp][row][4 * q4]) = acc[i];
-        if (q4 == 0) {
-          sh.pm[warp][row] = top[i];
-          sh.pl[warp][row] = sum[i];
-        }
-      }
-      join_sync();
-      for (int x = tid; x < (rows - r0) * kQuads && x < 8 * kQuads; x += 32 * kConsumers) {
-        float mx, total;
-        const float4 v = join_warps(sh, x / kQuads, x % kQuads, mx, total);
-        store_out<D>(p, w.r, w.head, row0 + r0 + x / kQuads, x % kQuads, v, mx, total);
-      }
+      if (rest) break;
+      k0 = c0;
+      k1 = c1;
+      step = 1 << some;
+      count = p.arrived + c0;
+      others = static_cast<uint32_t>((spread - 1) >> some);
     }
   }
   if (!ok && lane == 0) {
@@ -743,7 +780,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   if (!allow_smem(step_kernel<D, NT>, smem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count() * C::kCtasPerSm;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  step_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(p, kmap, vmap);
+  step_kernel<D, NT><<<ctas, C::kThreads, smem, stream>>>(p, kmap, vmap);
   return launch_status();
 }
 
