@@ -72,6 +72,7 @@ constexpr int kTmemCols = 512;
 constexpr int kPairBarrier = 1;        // + 4 * tile + quarter: the two warps of 32 rows
 constexpr int kHalf = kKeys / 2;       // keys of a softmax thread
 constexpr int kScaleSlots = 4;
+constexpr float kRoom = 15.f;          // log2 of the largest P: binary16 ends at 2^16
 
 template <int D>
 struct Cfg {
@@ -110,6 +111,20 @@ __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t pa
 }
 
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(kPairBarrier + id), "n"(64) : "memory"); }
+
+// The same, and whether `any` holds for one of the 64 threads.
+__device__ __forceinline__ bool pair_any(int id, bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(kPairBarrier + id), "n"(64), "r"(any ? 1u : 0u)
+      : "memory");
+  return r != 0u;
+}
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -492,17 +507,18 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const
       top = fmaxf(top, fmaxf(max_of<MASK>(a, sc[i], left - 16 * i), max_of<MASK>(a + 16, sc[i + 1], left - 16 * i - 16)));
     }
   }
-  st_shared_f32(mine, ok ? fmaxf(top, -INFINITY) : top);   // scores that are all NaN count as none
-  pair_sync(pair_id);
-  const float its = ld_shared_f32(other);
-  ok = __all_sync(0xFFFFFFFFu, ok && its == its);
-  if (!ok) return;
-  top = fmaxf(top, its);   // not NaN: `its` is not
-  if (first) {
-    m = top;
-  } else {
-    const bool over = top > m + kSlack;
-    if (__any_sync(0xFFFFFFFFu, over)) {   // in both warps of the rows
+  // In most units no score of the rows passes the maximum by 2^kRoom, and one barrier says so.
+  if (pair_any(pair_id, first || !ok || top > m + kRoom)) {
+    st_shared_f32(mine, ok ? fmaxf(top, -INFINITY) : top);   // scores that are all NaN count as none
+    pair_sync(pair_id);
+    const float its = ld_shared_f32(other);
+    ok = __all_sync(0xFFFFFFFFu, ok && its == its);
+    if (!ok) return;
+    top = fmaxf(top, its);   // not NaN: `its` is not
+    if (first) {
+      m = top;
+    } else {
+      const bool over = top > m + kRoom;
       const float keep = over ? ex2(m - top) : 1.f;
       if (over) m = top;
       l *= keep;
@@ -517,8 +533,8 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const
       }
       tc::tmem_st_wait();
       tc_fence_before();
-      pair_sync(pair_id);   // all of O, before either warp lets the next product begin
     }
+    pair_sync(pair_id);   // all of O, before either warp lets the next product begin; the exchange is read
   }
   const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
