@@ -985,9 +985,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++n, ++used) {
-        // the scales are there when the scores are: the second wait only orders their reads
-        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&ctl.s_full[x], used & 1) &&
-                                         poll_wait(&ctl.c_full[n % kScaleSlots], (n / kScaleSlots) & 1));
+        // the scales first: they are there long before the scores
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&ctl.c_full[n % kScaleSlots], (n / kScaleSlots) & 1) &&
+                                         mbar_wait(&ctl.s_full[x], used & 1));
         if (!ok && lane == 0) atomicOr(&ctl.abort, 1u);
         if (busy) {
           if (ok) tc_fence_after();
