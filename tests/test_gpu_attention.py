@@ -313,3 +313,18 @@ def test_long_requests_over_many_blocks(heads, dim, seq):
     assert all(torch.equal(a, b) for a, b in zip(first, second))
     head = ws[:256 + 4 * 3 * 640].view(torch.int32)   # the status word, the arrival counters
     assert int(head.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (14, 2, 64)])
+def test_prompts_beside_single_tokens(heads, kv_heads, dim):
+    """A call that takes both kernels, the second beginning where the first's blocks end: three times from one workspace
+    with the same bits."""
+    seq = [900, 1, 64, 2100, 333, 0, 700, 1500, 80, 128, 3000, 17]
+    new = [1, 1, 30, 1, 120, 0, 1, 65, 1, 3, 1, 17]
+    x = make(np.random.default_rng(dim), heads, kv_heads, dim, 32, seq, new)
+    ws = B.alloc_attention_workspace(heads, kv_heads, dim, max(new), "cuda")
+    first = run(x, workspace=ws)
+    check(x, first)
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(first, run(x, workspace=ws)))
+    assert int(ws[:4].view(torch.int32)) == 0

@@ -45,7 +45,7 @@ extern "C" size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int 
   const size_t step = 2 * attn::kMaxCtas * attn::step_slot_floats(head_dim);
   const size_t prompt = 2 * attn::kMaxPromptCtas * attn::prompt_slot_floats(head_dim);
   const bool few = static_cast<long long>(max_new) * (q_heads / kv_heads) <= attn::kStepRows;
-  return attn::head_bytes() + (few || step > prompt ? step : prompt) * sizeof(float);
+  return attn::head_bytes() + (few ? step : step + prompt) * sizeof(float);
 }
 
 extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_half* q, long long q_stride, int q_heads,
@@ -98,12 +98,15 @@ extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_hal
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + attn::head_bytes());
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool step = static_cast<long long>(max_new) * p.group <= attn::kStepRows;
-  if (step || requests > 1) {
+  const bool both = !step && requests > 1;
+  if (step || both) {
     p.rows_lo = 1;
     p.rows_hi = step ? 0x7FFFFFFF : attn::kStepRows;
+    p.followed = both;
     if ((st = attn::launch_step(p, *cache, (step ? max_new : 1) * p.group > 8, cs)) != EXL3_OK || step) return st;
   }
-  p.rows_lo = requests > 1 ? attn::kStepRows + 1 : 1;
+  p.rows_lo = both ? attn::kStepRows + 1 : 1;
   p.rows_hi = 0x7FFFFFFF;
-  return attn::launch_prompt(p, *cache, cs);
+  p.partial += 2 * attn::kMaxCtas * attn::step_slot_floats(cache->head_dim);
+  return attn::launch_prompt(p, *cache, both, cs);
 }

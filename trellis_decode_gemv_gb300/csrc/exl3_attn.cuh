@@ -62,6 +62,7 @@ struct AttnParams {
   float c;                 // scale * log2(e)
   int q_box;               // prompt kernel: Q comes by tensor copies of whole tokens
   int negate;              // prompt kernel: c is the absolute value, Q changes its sign
+  int followed;            // few rows: the other kernel may begin where this one's blocks end
   int q_heads, kv_heads, group, requests, tokens;
   int table_stride, pages, page_shift;
   long long most;          // keys that a table row holds
@@ -180,7 +181,7 @@ constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kSt
 
 // More: tiles of 256 rows.
 constexpr size_t prompt_slot_floats(int head_dim) { return static_cast<size_t>(256) * (head_dim + 2); }
-exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStream_t stream);
+exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, bool after_step, cudaStream_t stream);
 exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream);
 
 }  // namespace attn

@@ -722,7 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) p.split[blockIdx.x].last = -1;   // no item begins here and ends later, so far
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int ctas, count;
-  if (!find_range(p, ctl, smem_raw, ctas, count)) return;
+  if (!find_range(p, ctl, smem_raw, ctas, count)) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the few-rows kernel is
+    return;
+  }
   if (warp == kMmaWarp) tc::tmem_alloc(&ctl.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -1021,11 +1024,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_dealloc(tmem, kTmemCols);
   }
   if (tid == 0 && aborted(ctl)) atomicOr(p.status, 1u);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the few-rows kernel is
 }
 
 template <int D>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
-                   cudaStream_t stream) {
+                   bool after_step, cudaStream_t stream) {
   constexpr int kSmem = Cfg<D>::kTiles + static_cast<int>(sizeof(Control));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
@@ -1033,7 +1037,20 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   if (!allow_smem(prompt_kernel<D>, kSmem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
-  prompt_kernel<D><<<ctas, kThreads, kSmem, stream>>>(p, kmap, vmap, qmap);
+  // After the few-rows kernel a CTA begins as soon as an SM is free: the two write
+  // nothing in common (one of 100 tokens beside 8 single ones over 300 keys: 38 us, so 31;
+  // 2 of 500 beside 11 over up to 8 K: 135, so 132).
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t own = {};
+  own.gridDim = dim3(static_cast<unsigned>(ctas));
+  own.blockDim = dim3(kThreads);
+  own.dynamicSmemBytes = kSmem;
+  own.stream = stream;
+  own.attrs = attr;
+  own.numAttrs = after_step ? 1 : 0;
+  if (cudaLaunchKernelEx(&own, prompt_kernel<D>, p, kmap, vmap, qmap) != cudaSuccess) return EXL3_ERR_CUDA;
   exl3_status st = launch_status();
   if (st != EXL3_OK) return st;
   // a table whose rows hold no item that is ever split leaves nothing to join
@@ -1042,9 +1059,6 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), kItemRows / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return EXL3_ERR_CUDA;
@@ -1053,7 +1067,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
 
 }  // namespace
 
-exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStream_t stream) {
+exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, bool after_step, cudaStream_t stream) {
   CUtensorMap km, vm;
   exl3_status st;
   if ((st = cache_map(&km, c.k, c, c.page_size)) != EXL3_OK || (st = cache_map(&vm, c.v, c, c.page_size)) != EXL3_OK) return st;
@@ -1065,7 +1079,7 @@ exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, cudaStrea
   q.q_box = kTile % p.group == 0 && !q.negate ? 1 : 0;
   CUtensorMap qm = km;
   if (q.q_box != 0 && (st = query_map(&qm, p, c.head_dim, kTile / p.group)) != EXL3_OK) return st;
-  return c.head_dim == 64 ? launch<64>(q, km, vm, qm, stream) : launch<128>(q, km, vm, qm, stream);
+  return c.head_dim == 64 ? launch<64>(q, km, vm, qm, after_step, stream) : launch<128>(q, km, vm, qm, after_step, stream);
 }
 
 }  // namespace attn

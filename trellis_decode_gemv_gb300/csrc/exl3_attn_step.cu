@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
+  if (p.followed) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // This CTA's range.  Up to 32 requests every warp finds it by itself.
   Edge from, to;
   int ctas, first = 0;
