@@ -3,14 +3,14 @@
 //
 // Mathematics.  With k_j = ks_j * K_j and v_j = vs_j * V_j (K, V int8, one scale
 // per page and head) and c = scale * log2(e), a row's result is
-//   x_j = c ks_j (q . K_j) + log2 vs_j,   m >= max_j x_j - 8,   P_j = 2^(x_j - m),
+//   x_j = c ks_j (q . K_j) + log2 vs_j,   m >= max_j x_j - 8 or 15,   P_j = 2^(x_j - m),
 //   out = (sum_j P_j V_j) / l,   l = sum_j P_j / vs_j,   lse = ln 2 * m + ln l.
 // The value's scale rides in the exponent, so V enters the product as it is
 // stored and P (rounded to binary16 for the tensor cores) keeps its 11 bits
 // whatever the pages' scales are, as it would not if it were multiplied by a
 // small scale first; the sum l takes it out again, in binary32.  m, a running
-// maximum, is only moved when a score passes it by more than 2^8: P stays within
-// binary16's range, and the accumulators are rescaled rarely.
+// maximum, is only moved when a score passes it by more than 2^8 (few rows) or 2^15
+// (many): P stays within binary16's range, and the accumulators are rescaled rarely.
 //
 // Work.  An item is one (request, key/value head, tile of query rows); it has
 // as many units (tiles of keys) as its rows see.  The units of all items, in
@@ -18,8 +18,8 @@
 // lengths are.  An item inside one range is finished there; one that crosses
 // ranges leaves partial results (m, l and the sums, binary32), which the CTA whose
 // arrival completes the item (few rows) or a second kernel (many rows) joins in the
-// order of the keys, so the result does not depend on the order of the CTAs.  Everything is computed from the lengths
-// in device memory.
+// order of the keys, so the result does not depend on the order of the CTAs.
+// Everything is computed from the lengths in device memory.
 #pragma once
 
 #include "exl3_kv.cuh"
@@ -171,10 +171,9 @@ constexpr size_t head_bytes() { return 256 + sizeof(uint32_t) * kCounters + size
 
 // Up to kStepRows query rows per key/value head, in tiles of at most kStepTile that
 // each read the cache (the later ones from L2).  Against the other kernel, whose
-// tiles of 128 rows are mostly empty then: 32 rows 62 us to 82 (16 requests of 4000
-// keys) and 39 to 50 (one of 32000), 64 rows 107 to 83 and 60 to 50.  (One tile of 32
-// rows, which widens every byte once, took 60 and 53 us: its registers leave six
-// warps to an SM, and their latencies show.)
+// tiles of 128 rows are mostly empty then: 32 rows 34 us to 52 (16 requests of up to
+// 4000 keys) and 35 to 44 (one of 32000), 48 rows 46 to 47, 45 to 44 and 16 to 25 (4 of
+// 1000), 64 rows 57 to 48, 54 to 44 and 16 to 25.
 constexpr int kStepRows = 48;
 constexpr int kStepTile = 16;
 constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kStepTile) * (head_dim + 2); }

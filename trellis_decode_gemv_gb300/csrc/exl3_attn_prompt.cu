@@ -20,9 +20,9 @@
 //             scores of the current one are computed.
 //   4-11, 12-19 softmax of tile A and B: two threads share a row (its TMEM lane), one
 //             for each 64 keys of a unit and each half of O's columns; their warps
-//             exchange the row's largest score.  They also take O out.  O is only
-//             rescaled when a score passes the running maximum by 2^8, by these
-//             threads, between the MMAs that add to it.
+//             look by a barrier whether any score passes the running maximum by 2^15,
+//             and only then exchange the rows' largest and rescale O, between the
+//             MMAs that add to it.  They also take O out.
 //   20-23     widening: int8 tiles in shared memory into binary16 operand images,
 //             two of K and two of V.  Both are [key][D] rows of 64-element,
 //             128-byte pieces in the 128-byte swizzle: K is read as a K-major
@@ -35,13 +35,17 @@
 // CTA sets its abort flag and the status word, every role stops waiting, the MMA
 // lane waits (bounded) for its MMAs and the producer for its copies, TMEM is freed.
 //
-// Measured (2070 MHz, 32 heads over 8, D = 128): a prompt of 8192 tokens 478 us, 1150
-// Tflop/s, the tensor pipe active for half of the cycles; four chunks of 512 tokens
-// after 32K 899 us, 1204 Tflop/s.  An MMA of 128 x 128 x 16 takes 64 clocks, so a
-// unit's 32 take 2048 at D = 128, and a unit takes about 4000.  Two chains bound it:
+// Measured (2070 MHz, 32 heads over 8, D = 128): a prompt of 8192 tokens 453 us, 1214
+// Tflop/s, the tensor pipe active for 52% of the cycles; four chunks of 512 tokens
+// after 32K 827 us, 1309 Tflop/s.  An MMA of 128 x 128 x 16 takes 64 clocks, so a
+// unit's 32 take 2048 at D = 128, and a unit takes about 3800.  Two things bound it:
 // a tile's S, softmax, P V one after another, because P lies in place of S and the
 // next S must wait for the product; and shared memory, which feeds two operands of S,
-// one of P V, the widening and its stores (about 2700 clocks a unit).  Small code
+// one of P V, the widening and its stores (about 2700 clocks a unit), and whose queue
+// every wait and exchange stands in: three barriers polled at a time instead of one
+// made the kernel 5% slower, the softmax warps polling S another 5%.  (Units of 64
+// keys with two S a tile, which take the product out of the chain, were 1.5 times as
+// slow: twice the MMAs and waits for the one thread that issues them.)  Small code
 // matters: with the loops rolled (the 24 warps run five different ones) the
 // instruction cache stopped missing, the most of the way from 1542 us to 898 for the
 // prompt of 8192 when it was first measured.  128 scores a thread spill; a second MMA
