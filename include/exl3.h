@@ -613,7 +613,8 @@ exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_half *k, long 
  * results of the work that is split between thread blocks.  It must be
  * zero-filled once after allocation; every call leaves the counters zero again.
  * A wait inside a kernel that runs out ends the call without its results and sets the
- * status word (exl3_device_status reads it, as any workspace's).
+ * status word (exl3_device_status reads it, as any workspace's);
+ * zero-fill the workspace again before it is used further.
  * Two calls that may run concurrently must not share one.  0 for invalid
  * heads, head_dim or max_new < 1.
  */

@@ -328,3 +328,19 @@ def test_prompts_beside_single_tokens(heads, kv_heads, dim):
     for _ in range(2):
         assert all(torch.equal(a, b) for a, b in zip(first, run(x, workspace=ws)))
     assert int(ws[:4].view(torch.int32)) == 0
+
+
+@pytest.mark.parametrize("new", [1, 6, 150])
+@pytest.mark.parametrize("top", [12.0, 40.0, 130.0, -130.0])
+def test_scores_that_climb(new, top):
+    """Scores that rise (or fall) along the keys by up to 16 powers of two in 128 keys: the running maximum lags behind
+    them, is passed within its room, and moves again and again."""
+    heads, kv_heads, dim, page, seq = 4, 1, 128, 32, 1500
+    x = make(np.random.default_rng(new), heads, kv_heads, dim, page, [seq], [new])
+    for i, pg in enumerate(x["block_table"][0, :-(-seq // page)]):
+        at = np.arange(i * page, (i + 1) * page)
+        x["k"][pg] = np.rint(120 * np.minimum(at / seq, 1.0))[None, :, None].astype(np.int8) + (x["k"][pg] // 64)
+        x["k_scale"][pg] = 0.01
+    q = top / (120 * 0.01 * dim * x["scale"])
+    x["q"] = (q * (1 + 0.1 * np.random.default_rng(5).standard_normal(x["q"].shape))).astype(np.float16)
+    check(x, run(x))
