@@ -43,7 +43,8 @@
 // next S must wait for the product; and shared memory, which feeds two operands of S,
 // one of P V, the widening and its stores (about 2700 clocks a unit), and whose queue
 // every wait and exchange stands in: three barriers polled at a time instead of one
-// made the kernel 5% slower, the softmax warps polling S another 5%.  (Units of 64
+// made the kernel 5% slower, the softmax warps polling S another 5%, widening by three
+// warps in place of four, to leave the MMA warp's scheduler alone, 9%.  (Units of 64
 // keys with two S a tile, which take the product out of the chain, were 1.5 times as
 // slow: twice the MMAs and waits for the one thread that issues them.)  Small code
 // matters: with the loops rolled (the 24 warps run five different ones) the
