@@ -995,7 +995,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < steps; ++j, ++n, ++used) {
-        // the scales first: they are there long before the scores
+        // The scales first: they are there long before the scores.  Not at an item's first
+        // unit: after units that this tile skipped, the scales' barrier may be any number of
+        // phases behind, and a parity wait would pass for an old one.  Behind unit n's scores
+        // it is in phase n / kScaleSlots or past it: K of unit n is copied after the scales of
+        // unit n - 1 are announced.
+        if (j == 0) ok = ok && mbar_wait(&ctl.s_full[x], used & 1);
         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&ctl.c_full[n % kScaleSlots], (n / kScaleSlots) & 1) &&
                                          mbar_wait(&ctl.s_full[x], used & 1));
         if (!ok && lane == 0) atomicOr(&ctl.abort, 1u);
