@@ -56,10 +56,11 @@ class Wait:
 
 
 class Kernel:
-    """`scales_late`: the softmax warps wait for the scales behind the scores at an item's first unit."""
+    """`scales_late`: the softmax warps wait for the scales behind the scores at an item's first unit.  `all_meet`: the two
+    warps of 32 rows meet there even where they have no rows."""
 
-    def __init__(self, items, scales_late=True):
-        self.items, self.scales_late = items, scales_late
+    def __init__(self, items, scales_late=True, all_meet=True):
+        self.items, self.scales_late, self.all_meet = items, scales_late, all_meet
         self.units = [(i, j) for i, item in enumerate(items) for j in range(item[0])]
         self.b_full, self.b_empty = [Barrier(2) for _ in "kv"], [Barrier(1) for _ in "kv"]   # a copy is an arrival too
         self.k_full, self.v_full = [Barrier(1) for _ in range(2)], [Barrier(1) for _ in range(2)]
@@ -75,6 +76,8 @@ class Kernel:
         self.scale_readers = [0] * SLOTS
         self.q = [None, None]
         self.s = [None, None]
+        self.o = [None, None]              # item, half products added
+        self.meet = [[Barrier(2) for _ in range(2)] for _ in range(2)]      # the two warps of a pair
 
     def tiles(self, item):
         return [x for x in (0, 1) if self.items[item][1 + x] > 0]
@@ -154,6 +157,11 @@ class Kernel:
     def product(self, x, h, u):
         need(self.image[1][u & 1] == u, "a product with another unit's values")
         need(self.s[x] == u, "a product with another unit's probabilities")
+        item, j = self.units[u]
+        if j == 0 and h == 0:
+            self.o[x] = (item, 0)
+        need(self.o[x] == (item, 2 * j + h), "sums of another item")
+        self.o[x] = (item, 2 * j + h + 1)
 
     def mma(self):
         used, begun = [0, 0], [0, 0]
@@ -193,7 +201,7 @@ class Kernel:
         self.mmas.append(None)
 
     def softmax(self, x, half, pair):
-        n = used = items = 0
+        n = used = items = met = 0
         for item, (steps, *pairs) in enumerate(self.items):
             if pairs[x] == 0:
                 n += steps
@@ -210,11 +218,22 @@ class Kernel:
                     yield
                     need(self.scale[n % SLOTS] == n, "another unit's scales")
                     self.scale_readers[n % SLOTS] -= 1
+                if j == 0 and (busy or self.all_meet):
+                    self.meet[x][pair].arrive()
+                    yield Wait(self.meet[x][pair], met, "the other warp")
+                    met += 1
                 self.p_full[x][half].arrive()
                 yield
                 n, used = n + 1, used + 1
             yield Wait(self.o_done[x], items, "o_done")
             items += 1
+            if busy:
+                self.meet[x][pair].arrive()
+                yield Wait(self.meet[x][pair], met, "the other warp")
+                met += 1
+                for _ in range(2):    # columns of the sums, one after another
+                    need(self.o[x] == (item, 2 * steps), "sums written over before they are read")
+                    yield
 
     def actors(self):
         yield "producer", self.producer()
@@ -282,6 +301,12 @@ def test_scales_waited_for_first_after_skipped_items():
     are copied after the scales of unit n - 1 are announced."""
     assert faults(1000, scales_late=False) == {"a wait on c_full passed for an earlier phase"}
     assert "another unit's scales" in faults(1000, strict=False, scales_late=False)
+
+
+def test_warps_meet_between_an_items_sums_and_the_next_product():
+    """Two warps share 32 rows.  The next item's first product waits for one of them only, so that one has to know that
+    the other has read the sums before, even if the next item leaves both without rows."""
+    assert faults(1000, all_meet=False) == {"sums written over before they are read"}
 
 
 @pytest.mark.parametrize("skipped", [4, 5, 7, 8, 12])

@@ -103,3 +103,15 @@ def test_items_of_one_tile_before_items_of_two(heads, kv_heads, dim, page, small
     seq = [int(keys + rng.integers(0, 128)) for _ in range(requests)]
     new = [int(rng.integers(40, 64)) if i % 3 == 2 else small for i in range(requests)]
     repeat(build(small, heads, kv_heads, dim, page, seq, new))
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 1, 128), (8, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("keys", [260, 100, 900])
+def test_tiles_of_few_rows_behind_full_ones(heads, kv_heads, dim, keys):
+    """Many items a block, full tiles and tiles of 1 to 96 rows in turn: warps that have rows in one item and none in the
+    next."""
+    group = heads // kv_heads
+    rng = np.random.default_rng(keys)
+    rows = [256 if i % 2 == 0 else int(rng.choice([52, 64, 72, 96, 132, 160, 192, 224])) for i in range(400)]
+    new = [max(r // group, 1) for r in rows]
+    repeat(build(keys, heads, kv_heads, dim, 32, [max(keys, n) + i % 5 for i, n in enumerate(new)], new))

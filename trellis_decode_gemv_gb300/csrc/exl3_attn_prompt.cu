@@ -1013,6 +1013,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             softmax_unit<D, true>(s_at, o_at, sc, left, j == 0, m, l, mine_top, other_top, pair_id, ok);
           else
             softmax_unit<D, false>(s_at, o_at, sc, left, j == 0, m, l, mine_top, other_top, pair_id, ok);
+        } else if (j == 0) {
+          // Warps without rows meet as well (the others do in softmax_unit): the first
+          // product, which writes over all of O, waits for this half's warps only, and the
+          // other half's may still be reading the last item's O.
+          pair_sync(pair_id);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_full[x][half]);
