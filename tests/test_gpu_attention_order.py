@@ -115,3 +115,12 @@ def test_tiles_of_few_rows_behind_full_ones(heads, kv_heads, dim, keys):
     rows = [256 if i % 2 == 0 else int(rng.choice([52, 64, 72, 96, 132, 160, 192, 224])) for i in range(400)]
     new = [max(r // group, 1) for r in rows]
     repeat(build(keys, heads, kv_heads, dim, 32, [max(keys, n) + i % 5 for i, n in enumerate(new)], new))
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 1, 64), (8, 2, 128)])
+@pytest.mark.parametrize("requests", [700, 2500])
+def test_first_queries_where_the_prelude_wrote(heads, kv_heads, dim, requests):
+    """The requests' table of the range prelude lies where the first items' queries are copied to."""
+    rng = np.random.default_rng(requests)
+    new = [13 if i % 2 else int(rng.integers(13, 40)) for i in range(requests)]
+    repeat(build(requests, heads, kv_heads, dim, 64, [n + int(rng.integers(0, 90)) for n in new], new))

@@ -732,6 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&ctl.tmem_base, kTmemCols);
+  // The prelude wrote its table where the first Q comes by tensor copies: stores of one
+  // proxy before those of the other.
+  fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
