@@ -638,7 +638,8 @@ size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, i
  *       sizes the workspace; a request with more is computed all the same.
  * The scores, the softmax statistics and the sums are binary32; the int8 keys
  * and values enter the products exactly (as binary16 integers) and the
- * probabilities rounded to binary16, relative to the row's largest p_j * v_scale.
+ * probabilities rounded to binary16: 11 bits for a p_j * v_scale down to 2^-21 of
+ * the row's largest, below that the nearest multiple of 2^-31 of it or finer.
  * The result does not depend on the order in which thread blocks run.  One to
  * three launches.
  * Errors: EXL3_ERR_NULL, EXL3_ERR_SHAPE (cache fields, q_heads not a multiple of

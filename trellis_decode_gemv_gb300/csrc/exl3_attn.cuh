@@ -3,14 +3,19 @@
 //
 // Mathematics.  With k_j = ks_j * K_j and v_j = vs_j * V_j (K, V int8, one scale
 // per page and head) and c = scale * log2(e), a row's result is
-//   x_j = c ks_j (q . K_j) + log2 vs_j,   m >= max_j x_j - 8 or 15,   P_j = 2^(x_j - m),
+//   x_j = c ks_j (q . K_j) + log2 vs_j,   max_j x_j - 15.9 <= m <= max_j x_j - 7,   P_j = 2^(x_j - m),
 //   out = (sum_j P_j V_j) / l,   l = sum_j P_j / vs_j,   lse = ln 2 * m + ln l.
 // The value's scale rides in the exponent, so V enters the product as it is
 // stored and P (rounded to binary16 for the tensor cores) keeps its 11 bits
 // whatever the pages' scales are, as it would not if it were multiplied by a
-// small scale first; the sum l takes it out again, in binary32.  m, a running
-// maximum, is only moved when a score passes it by more than 2^8 (few rows) or 2^15
-// (many): P stays within binary16's range, and the accumulators are rescaled rarely.
+// small scale first; the sum l takes it out again, in binary32.  m follows the running
+// maximum from 2^7 below it and is only moved when a score passes it by more than
+// 2^15.9, so the accumulators are rescaled rarely.  The row's largest P is then between
+// 2^7 and 2^15.9: a P keeps its 11 bits down to 2^-21 of it and is cut at 2^-32 of it, where one
+// key outweighs the others by that much (with a largest P of 1 many keys next to one of
+// 2^25 times their weight added nothing to the numerator and all of theirs to l).  More
+// moves than from a largest P of 1: a prompt of 8192 tokens 478 us in place of 470 (481
+// with moves at 2^15), steps the same.
 //
 // Work.  An item is one (request, key/value head, tile of query rows); it has
 // as many units (tiles of keys) as its rows see.  The units of all items, in
@@ -37,7 +42,8 @@ using tc::smem_u32;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;     // log2 of the largest P
+constexpr float kRoom = 15.9f;    // log2 of the largest P: binary16 ends at 2^16
+constexpr float kBelow = 7.f;     // m's distance to the maximum when it is set; kRoom - kBelow powers of two to the next move
 constexpr float kTinyScale = -90.f;  // log2 that stands for a value scale of 0: its V add nothing, its P still count in l
 constexpr int kMaxCtas = 160 * 4; // ranges that the workspace has counters for
 

@@ -20,8 +20,8 @@
 //             scores of the current one are computed.
 //   4-11, 12-19 softmax of tile A and B: two threads share a row (its TMEM lane), one
 //             for each 64 keys of a unit and each half of O's columns; their warps
-//             look by a barrier whether any score passes the running maximum by 2^15,
-//             and only then exchange the rows' largest and rescale O, between the
+//             look by a barrier whether any score passes m by 2^15.9, and
+//             only then exchange the rows' largest and rescale O, between the
 //             MMAs that add to it.  They also take O out.
 //   20-23     widening: int8 tiles in shared memory into binary16 operand images,
 //             two of K and two of V.  Both are [key][D] rows of 64-element,
@@ -77,7 +77,6 @@ constexpr int kTmemCols = 512;
 constexpr int kPairBarrier = 1;        // + 4 * tile + quarter: the two warps of 32 rows
 constexpr int kHalf = kKeys / 2;       // keys of a softmax thread
 constexpr int kScaleSlots = 4;
-constexpr float kRoom = 15.f;          // log2 of the largest P: binary16 ends at 2^16
 
 template <int D>
 struct Cfg {
@@ -523,11 +522,12 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const
     if (!ok) return;
     top = fmaxf(top, its);   // not NaN: `its` is not
     if (first) {
-      m = top;
+      m = top - kBelow;
     } else {
       const bool over = top > m + kRoom;
-      const float keep = over ? ex2(m - top) : 1.f;
-      if (over) m = top;
+      const float next = top - kBelow;
+      const float keep = over ? ex2(m - next) : 1.f;
+      if (over) m = next;
       l *= keep;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
