@@ -15,6 +15,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import test_gpu_attention as A
 from trellis_decode_gemv_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +71,14 @@ def test_one_key_far_above_many(heads, dim, keys, requests, where):
     assert (off <= allowed).all(), f"{(off / allowed).max():.2f} times what is allowed, gap {GAPS[(off / allowed).max((0, 2)).argmax() % 8]}"
     off = np.abs(got_lse.double().cpu().numpy() - lse[None])
     assert (off <= lse_allowed).all(), f"lse: {(off / lse_allowed).max():.2f} times what is allowed"
+
+
+@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("tiny", [0.0, 1e-45, 1e-40, 2.0 ** -126, 1e-33, 2.0 ** -100, 2.0 ** -90, 2.0 ** -89, 1e-20])
+def test_value_scales_next_to_zero(new, tiny):
+    """Pages whose value scale is next to nothing, subnormal ones among them, beside others and alone: their values add
+    nothing, their probabilities count."""
+    x = A.make(np.random.default_rng(new), 4, 1, 128, 16, [700, new + 3, 40], [new, new, 1])
+    x["v_scale"][x["block_table"][0, :43:3]] = tiny
+    x["v_scale"][x["block_table"][1, :-(-(new + 3) // 16)]] = tiny
+    A.check(x, A.run(x))

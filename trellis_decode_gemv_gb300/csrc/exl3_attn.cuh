@@ -44,7 +44,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRoom = 15.9f;    // log2 of the largest P: binary16 ends at 2^16
 constexpr float kBelow = 7.f;     // m's distance to the maximum when it is set; kRoom - kBelow powers of two to the next move
-constexpr float kTinyScale = -90.f;  // log2 that stands for a value scale of 0: its V add nothing, its P still count in l
+// log2 that stands for a value scale of 0 and all below 2^-90: V of less than 2^-83 add
+// nothing to a binary16 output, but their P have to count in l, within binary32's range
+// (the logarithm of 2^-130, say, left 1 / scale infinite).
+constexpr float kTinyScale = -90.f;
 constexpr int kMaxCtas = 160 * 4; // ranges that the workspace has counters for
 
 // An item of the many-rows kernel that begins in a range and ends in a later one.
@@ -120,7 +123,7 @@ struct PageScale {
 __device__ __forceinline__ PageScale page_scale(const AttnParams& p, float ks, float vs) {
   PageScale s;
   s.c = ks * p.c;
-  s.lv = vs == 0.f ? kTinyScale : log2f(vs);
+  s.lv = vs >= 0.f && vs <= 0x1p-90f ? kTinyScale : log2f(vs);   // NaN stays NaN
   // of the rounded logarithm, so that l and the sums agree; finite, so that it spoils no row whose P is 0
   s.iv = vs != vs ? 1.f : exp2f(-s.lv);
   return s;
