@@ -499,7 +499,8 @@ exl3_status exl3_set_path(int path);
  * Failure-detection test hook (no counterpart in the pages).  While `on` is
  * non-zero, the operand producers of the tensor-core kernel (operand B) and
  * of the dense prefill kernel (both operands) post nothing, so the bounded
- * device-side waits for the operands run out: every role of the kernel
+ * device-side waits for the operands run out (those of the attention kernels
+ * post the first keys of each block's range and nothing after): every role of the kernel
  * stops, waits (bounded) for its copies in flight, frees its tensor memory,
  * and the kernel ORs 1 into the workspace status word (see
  * exl3_workspace_bytes) before it exits.  The call's outputs are then not
@@ -612,9 +613,9 @@ exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_half *k, long 
  * request: a status word (first 256 bytes), arrival counters, then the partial
  * results of the work that is split between thread blocks.  It must be
  * zero-filled once after allocation; every call leaves the counters zero again.
- * A wait inside a kernel that runs out ends the call without its results and sets the
- * status word (exl3_device_status reads it, as any workspace's);
- * zero-fill the workspace again before it is used further.
+ * A wait inside a kernel that runs out sets the status word (exl3_device_status
+ * reads it, as any workspace's); the rows that could not be finished are NaN, in
+ * out and lse. Zero-fill the workspace again before it is used further.
  * Two calls that may run concurrently must not share one.  0 for invalid
  * heads, head_dim or max_new < 1.
  */

@@ -312,6 +312,8 @@ extern "C" exl3_status exl3_device_status(const void* status_word, exl3_stream_t
   return word == 0u ? EXL3_OK : EXL3_ERR_DEVICE_CHECK;
 }
 
+int exl3::debug_stall() { return g_debug_stall.load(std::memory_order_relaxed); }
+
 extern "C" exl3_status exl3_debug_stall_tensor_wait(int on) {
   g_debug_stall.store(on != 0 ? 1 : 0, std::memory_order_relaxed);
   return EXL3_OK;

@@ -92,6 +92,7 @@ extern "C" exl3_status exl3_attention(const exl3_kv_cache* cache, const exl3_hal
   // keys are numbered in 31 bits
   p.most = static_cast<long long>(table_stride) << p.page_shift;
   if (p.most > 0x7FFFFF00LL) p.most = 0x7FFFFF00LL;
+  p.stall = debug_stall();
   p.status = static_cast<uint32_t*>(workspace);
   p.arrived = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + 256);
   p.split = reinterpret_cast<attn::SplitItem*>(p.arrived + attn::kCounters);

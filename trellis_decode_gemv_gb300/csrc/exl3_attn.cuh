@@ -71,6 +71,7 @@ struct AttnParams {
   float c;                 // scale * log2(e)
   int q_box;               // prompt kernel: Q comes by tensor copies of whole tokens
   int negate;              // prompt kernel: c is the absolute value, Q changes its sign
+  int stall;               // test hook: the producers post the first unit of a range only
   int followed;            // few rows: the other kernel may begin where this one's blocks end
   int q_heads, kv_heads, group, requests, tokens;
   int table_stride, pages, page_shift;
@@ -110,6 +111,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// In place of a row's sum l where a wait ran out before all of its keys were read: it
+// stays through the joins and makes the row's output NaN.
+__device__ __forceinline__ float unfinished() { return __int_as_float(0x7FC00000); }
 
 // The row's result from its sums: `sees` whether it sees a key at all.
 __device__ __forceinline__ float inverse_sum(float l, bool sees) { return sees ? __fdividef(1.f, l) : 0.f; }

@@ -582,6 +582,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   const int sw = (threadIdx.x >> 5) - kSoftmaxWarp0;
   const int x = sw >> 3, half = (sw >> 2) & 1, pair_id = 4 * x + (sw & 3);
   const uint32_t mine_top = smem_u32(&ctl.top[x][half][r]), other_top = smem_u32(&ctl.top[x][half ^ 1][r]);
+  if (!ok) l = unfinished();
   if (busy) {
     st_shared_f32(mine_top, l);
     pair_sync(pair_id);
@@ -599,13 +600,18 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   constexpr size_t kMAt = static_cast<size_t>(D) * kTile, kLAt = static_cast<size_t>(D + 1) * kTile;
   float* slot = p.partial + (static_cast<size_t>(2 * blockIdx.x + (lo == 0 ? 1 : 0)) * 2 + x) * kTileFloats;
   const int quad0 = half * (D / 8);   // this half's first four columns
-  if (ok && busy) {
+  if (busy) {
     const float inv = inverse_sum(l, sees);
 #pragma unroll 1
     for (int ch = 0; ch < D / 64; ++ch) {
       uint32_t a[32];
-      tmem_ld32(o_at + 32 * ch, a);
-      tmem_ld_wait();
+      if (ok) {
+        tmem_ld32(o_at + 32 * ch, a);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a[e] = 0u;
+      }
       if (whole) {
         if (mine) store_row(dst + 32 * ch, a, inv, sees);
       } else {
@@ -619,7 +625,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   }
   float* lse = p.lse != nullptr && half == 0 ? p.lse + static_cast<size_t>(req.t0 + tok) * p.q_heads + h : nullptr;
   if (whole) {
-    if (ok && mine && lse != nullptr) *lse = sees ? kLn2 * (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
+    if (mine && lse != nullptr) *lse = sees ? kLn2 * (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
     return;
   }
   if (half == 0) {
@@ -863,8 +869,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t copy_bytes = static_cast<uint32_t>(per_page * D);
     Look l0 = look_up(), l1 = look_up();
     Scales s0 = scales_of(l0);
+    const uint32_t posts = p.stall != 0 ? 1u : static_cast<uint32_t>(count);
     uint32_t n = 0;
-    for (; n < static_cast<uint32_t>(count); ++n) {
+    for (; n < posts; ++n) {
       const Look l2 = look_up();
       const Scales s1 = scales_of(l1);
       // one copy per page that holds keys of the request; what is not copied is

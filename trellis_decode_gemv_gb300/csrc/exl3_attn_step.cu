@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
           ks[gr] = in ? __ldg(p.k_scale + at) : 0.f;
           vs[gr] = in ? __ldg(p.v_scale + at) : 1.f;
         }
-        const int n = min(32, w.hi - g0);
+        const int n = p.stall == 0 ? min(32, w.hi - g0) : i == 0 ? 1 : 0;
         for (int j = 0; j < n; ++j, ++i) {
           const uint32_t st = i % kStages;
           const uint32_t use = i / kStages;
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         if (g == 0) {
           sh.pm[warp][2 * t + e] = m[nt][e];
-          sh.pl[warp][2 * t + e] = sum;
+          sh.pl[warp][2 * t + e] = ok ? sum : unfinished();
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k)

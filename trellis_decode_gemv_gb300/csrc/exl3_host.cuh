@@ -48,6 +48,9 @@ inline exl3_status launch_status() {
 // Number of SMs of the current device (queried once per device).
 int device_sm_count();
 
+// Whether exl3_debug_stall_tensor_wait is on.
+int debug_stall();
+
 // Allows `kernel` its dynamic shared memory on the current device, once for each
 // device (`done` a static of the caller, one bit a device).
 template <typename F>
