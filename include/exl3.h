@@ -601,7 +601,7 @@ exl3_status exl3_kv_plan(const int32_t *ctx_len, const int32_t *new_len, int req
  *   k, v [tokens][kv_heads][head_dim] halves, token t at k + t * k_stride halves
  *   (strides multiples of 8, at least kv_heads * head_dim).
  * Slots outside the cache are skipped.  One launch.  Errors: EXL3_ERR_NULL,
- * EXL3_ERR_SHAPE (cache fields, strides), EXL3_ERR_BATCH (tokens < 0),
+ * EXL3_ERR_SHAPE (cache fields, kv_heads above 65535, strides), EXL3_ERR_BATCH (tokens < 0),
  * EXL3_ERR_ALIGN.
  */
 exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_half *k, long long k_stride,
@@ -644,7 +644,7 @@ size_t exl3_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, i
  * The result does not depend on the order in which thread blocks run.  One to
  * three launches.
  * Errors: EXL3_ERR_NULL, EXL3_ERR_SHAPE (cache fields, q_heads not a multiple of
- * kv_heads, strides, table_stride < 1), EXL3_ERR_BATCH (requests outside
+ * kv_heads or above 65535, strides, table_stride < 1), EXL3_ERR_BATCH (requests outside
  * 0..EXL3_MAX_REQUESTS, tokens < 0, max_new < 1), EXL3_ERR_ALIGN,
  * EXL3_ERR_WORKSPACE.
  */

@@ -872,7 +872,8 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
     """Attention of each request's newest tokens over `cache` (see the header):
     q [tokens, q_heads, head_dim] halves, q_start [requests + 1] and seq_len
     [requests] int32, block_table [requests, width] int32.  max_new: the most new
-    tokens of any request (default: all tokens).  scale: default head_dim**-0.5.
+    tokens of any request (default: all tokens of the call, which sizes the workspace and
+    picks the kernels as for one prompt; a step of single tokens says 1).  scale: default head_dim**-0.5.
     Returns out (like q), or (out, lse) with lse a float32 tensor [tokens,
     q_heads] to write or True for a new one."""
     dev = cache.device

@@ -24,10 +24,10 @@
 // reads are free of bank conflicts for D = 128.
 //
 // Measured (64 requests of 4096 keys, 32 heads over 8): D = 128 94 us, 5.7 TB/s of
-// keys and values, read once (543.7 MB of DRAM traffic for 541); D = 64 57 us, 4.7
+// keys and values, read once (543.7 MB of DRAM traffic for 541); D = 64 58 us, 4.6
 // TB/s.  Instructions issue in 42% of the cycles, so it is neither they nor the
 // bytes alone: 9 consumer warps an SM (168 registers, three CTAs) hide their own
-// latencies only in part.  One request of 131K keys takes 55 us where its 268.6 MB
+// latencies only in part.  One request of 131K keys takes 56 us where its 268.6 MB
 // need 40; the 57 partial results of each head added 10 us when the last arrival joined
 // them all, and add about 5 in two steps.  Tiles of 16 rows want more registers than
 // three CTAs an SM leave: with two (242 registers, six consumer warps in place of

@@ -193,12 +193,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // One CTA per (window of tokens, head): the runs (the tokens of this call that go
 // into one page) that begin in the window, one after the other; half of the threads
 // take the keys, half the values.  A run's values are read once, 16 bytes a lane, and
-// stay in registers between the maximum and the rounding.  The bound is reading 2
-// bytes and writing 1 per value, with issuing the rounding (5 instructions a value)
-// close behind it: a side of a page is at most 64 threads with up to 16 rows each,
-// not more threads with fewer, which spent as much again on addresses and the run.
-// Prompts of 25 K tokens, 8 heads of 128: 34 us, 154 MB at 4.5 TB/s (50 MB of it
-// written), 16.0 M instructions in 46% of the issue cycles.
+// stay in registers between the maximum and the rounding: a side of a page is at most
+// 64 threads with up to 16 rows each, not more threads with fewer, which spent as much
+// again on addresses and the run.  Prompts of 25 K tokens, 8 heads of 128: 34 us, 154 MB
+// at 4.5 TB/s (50 MB of it written), 16.0 M instructions in 46% of the issue cycles.
+// Neither the bytes (23 us) nor the instructions bind it alone: each block is one chain
+// of slots, values and stores, and 128 registers a thread leave 16 warps an SM to hide it.
 template <int SIZE>
 constexpr int append_threads() { return SIZE < 32 ? 64 : 2 * SIZE; }
 
