@@ -82,3 +82,32 @@ def test_value_scales_next_to_zero(new, tiny):
     x["v_scale"][x["block_table"][0, :43:3]] = tiny
     x["v_scale"][x["block_table"][1, :-(-(new + 3) // 16)]] = tiny
     A.check(x, A.run(x))
+
+
+@pytest.mark.parametrize("heads,dim,new", [(8, 128, 1), (16, 64, 1), (4, 128, 100), (4, 64, 30)])
+@pytest.mark.parametrize("size", [8, 16, 19, 20, 21, 22, 23, 24, 25, 26, 27, 28, 29, 31, 34])
+@pytest.mark.parametrize("spread", [12.0, 64.0])
+def test_scores_as_large_as_the_types_allow(heads, dim, new, size, spread):
+    """Scores around 2^size that differ by up to `spread` powers of two, or as far as binary32 tells them apart, in random
+    order: whatever the weights are, equal values make an output of that value, to its own rounding (2^-11) and what the
+    probabilities' rounding to binary16 (2^-11) and sums over n keys leave."""
+    page, keys = 32, 3000
+    g = torch.Generator(device="cuda").manual_seed(size)
+    pages = -(-keys // page)
+    k = torch.zeros((pages, 1, page, dim), dtype=torch.int8, device="cuda")
+    k[..., 0] = 127
+    k[..., 1] = torch.randint(0, 128, (pages, 1, page), generator=g, device="cuda").to(torch.int8)
+    big = 2.0 ** min(size - 7, 15)
+    unit = 2.0 ** size / (127 * big)                           # powers of two for a product of one
+    small = spread / (127 * unit)
+    q = torch.zeros((new, heads, dim), dtype=torch.float16, device="cuda")
+    q[:, :, 0] = big
+    q[:, :, 1] = small * (0.5 + torch.rand((new, heads), generator=g, device="cuda"))
+    cache = B.Exl3KvCache.from_tensors(k, torch.full_like(k, 100), torch.full((pages, 1), unit, device="cuda"),
+                                       torch.full((pages, 1), 1 / 64, device="cuda"))
+    out, lse = B.exl3_attention(cache, q, torch.tensor([0, new], dtype=torch.int32, device="cuda"),
+                                torch.tensor([keys], dtype=torch.int32, device="cuda"),
+                                torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1), max_new=new, scale=float(np.log(2)), lse=True)
+    off = float((out.double() - 100 / 64).abs().max())
+    assert off <= 100 / 64 * (2.0 ** -10 + (keys + 64) * 2.0 ** -23), off
+    assert bool(torch.isfinite(lse).all())

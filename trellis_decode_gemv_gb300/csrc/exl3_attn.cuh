@@ -119,6 +119,11 @@ __device__ __forceinline__ float unfinished() { return __int_as_float(0x7FC00000
 // The row's result from its sums: `sees` whether it sees a key at all.
 __device__ __forceinline__ float inverse_sum(float l, bool sees) { return sees ? __fdividef(1.f, l) : 0.f; }
 
+// What a score x has to pass before m moves.  Rounded down, so that x - m (exact for an x of
+// m's size) is at most kRoom for an x that does not pass, however large both are: rounded to
+// nearest, P left binary16's range at scores from 2^24 or so on.
+__device__ __forceinline__ float room_above(float m) { return __fadd_rd(m, kRoom); }
+
 struct PageScale {
   float c;  // c ks
   float lv; // log2 vs

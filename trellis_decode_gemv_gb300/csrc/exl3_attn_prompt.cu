@@ -77,6 +77,7 @@ constexpr int kTmemCols = 512;
 constexpr int kPairBarrier = 1;        // + 4 * tile + quarter: the two warps of 32 rows
 constexpr int kHalf = kKeys / 2;       // keys of a softmax thread
 constexpr int kScaleSlots = 4;
+constexpr float kFar = 65536.f;        // x - m is taken exactly for an m past this (binary32 steps of 2^-7 and more)
 
 template <int D>
 struct Cfg {
@@ -156,6 +157,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  float v[16];
+  tc::tmem_ld16(taddr, v);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e]);
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -458,18 +465,24 @@ __device__ __forceinline__ float max_of(const uint32_t* v, const float4& f, int 
   }
 }
 
-// P of 16 scores of one scale to tensor memory, their sum / vs onto l.
-template <bool MASK>
+// P of 16 scores of one scale to tensor memory, their sum / vs onto l.  EXACT: x as the
+// maximum took it, then its distance to m, and only the first `left` scores.  Otherwise c ks
+// s + (log2 vs - m), one instruction for two scores less, whose rounding by m's size a large
+// m does not allow: P could pass binary16's range or vanish.  (Prompt of 8192: 485 us, 478
+// without any regard to large m, 497 with all units EXACT.)
+template <bool EXACT>
 __device__ __forceinline__ void exp_of(const uint32_t* v, const float4& f, int left, float base, float& l, uint32_t p_at) {
   uint32_t pk[8];
-  const float lv = f.y - base;
-  const uint64_t ff = pair(f.x, f.x), lvlv = pair(lv, lv);
+  const float y = EXACT ? f.y : f.y - base;
+  const uint64_t ff = pair(f.x, f.x), yy = pair(y, y), mm = pair(-base, -base);
   uint64_t sum = 0;   // two zeros
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
+    uint64_t x = fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ff, yy);
+    if constexpr (EXACT) x = add2(x, mm);
     float p0, p1;
-    unpair(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ff, lvlv), p0, p1);
-    if constexpr (MASK) {
+    unpair(x, p0, p1);
+    if constexpr (EXACT) {
       p0 = e < left ? p0 : -INFINITY;
       p1 = e + 1 < left ? p1 : -INFINITY;
     }
@@ -491,40 +504,51 @@ __device__ __forceinline__ void exp_of(const uint32_t* v, const float4& f, int l
 // scores that are in registers by then.
 __device__ __forceinline__ constexpr uint32_t p_column(int i) { return static_cast<uint32_t>((i >> 1) * 32 + (i & 1) * 8); }
 
+// Whether a row's m is so large that x - m has to be taken exactly.  (m is the same in
+// both warps of the rows.)
+__device__ __forceinline__ bool is_far(float m) { return __any_sync(0xFFFFFFFFu, fabsf(m) > kFar && m != -INFINITY); }
+
 // 64 of a row's scores (the row's other 64 are another warp's): the running maximum
 // m (O and l rescaled when it moves), P in place of the scores, l.  `left`: the
-// keys of these 64 that the row sees, looked at only where the unit needs a mask.
+// keys of these 64 that the row sees, looked at only if EXACT, as a unit that needs a
+// mask has to be.  True: m has become large, and the unit has to be taken again, EXACT.
 // `s_at` the scores, `o_at` this thread's half of O; `mine` the row's place in the
 // exchange of the two warps, `other` the other warp's.  A warp whose wait ran out
 // takes part in the exchange with NaN, and both give up.  S is read twice, 32 scores
 // at a time, in loops that are not unrolled: the code of all roles has to stay in the
 // instruction cache (unrolled, the kernel took 1.6 times as long).
-template <int D, bool MASK>
-__device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const float4* sc, int left, bool first, float& m,
+template <int D, bool EXACT>
+__device__ __forceinline__ bool softmax_unit(uint32_t s_at, uint32_t o_at, const float4* sc, int left, bool first, float& m,
                                              float& l, uint32_t mine, uint32_t other, int pair_id, bool& ok) {
-  uint32_t a[32];
+  constexpr int kOnce = EXACT ? 1 : 2;   // groups at a time: few units are EXACT, and their code is to be small
+  uint32_t a[16 * kOnce];
   float top = __int_as_float(0x7FC00000);
   if (ok) {
     top = -INFINITY;
 #pragma unroll 1
-    for (int i = 0; i < 4; i += 2) {
-      tmem_ld32(s_at + 16 * i, a);
-      tmem_ld_wait();
-      top = fmaxf(top, fmaxf(max_of<MASK>(a, sc[i], left - 16 * i), max_of<MASK>(a + 16, sc[i + 1], left - 16 * i - 16)));
+    for (int i = 0; i < 4; i += kOnce) {
+      if constexpr (EXACT) {
+        tmem_ld16(s_at + 16 * i, a);
+        top = fmaxf(top, max_of<true>(a, sc[i], left - 16 * i));
+      } else {
+        tmem_ld32(s_at + 16 * i, a);
+        tmem_ld_wait();
+        top = fmaxf(top, fmaxf(max_of<false>(a, sc[i], left), max_of<false>(a + 16, sc[i + 1], left)));
+      }
     }
   }
   // In most units no score of the rows passes the maximum by 2^kRoom, and one barrier says so.
-  if (pair_any(pair_id, first || !ok || top > m + kRoom)) {
+  if (pair_any(pair_id, first || !ok || top - m > kRoom)) {
     st_shared_f32(mine, ok ? fmaxf(top, -INFINITY) : top);   // scores that are all NaN count as none
     pair_sync(pair_id);
     const float its = ld_shared_f32(other);
     ok = __all_sync(0xFFFFFFFFu, ok && its == its);
-    if (!ok) return;
+    if (!ok) return false;
     top = fmaxf(top, its);   // not NaN: `its` is not
     if (first) {
       m = top - kBelow;
     } else {
-      const bool over = top > m + kRoom;
+      const bool over = top - m > kRoom;
       const float next = top - kBelow;
       const float keep = over ? ex2(m - next) : 1.f;
       if (over) m = next;
@@ -542,17 +566,24 @@ __device__ __forceinline__ void softmax_unit(uint32_t s_at, uint32_t o_at, const
       tc_fence_before();
     }
     pair_sync(pair_id);   // all of O, before either warp lets the next product begin; the exchange is read
+    if (!EXACT && is_far(m)) return true;   // both warps have the same rows and the same m
   }
   const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-  for (int i = 0; i < 4; i += 2) {
-    tmem_ld32(s_at + 16 * i, a);
-    tmem_ld_wait();
-    exp_of<MASK>(a, sc[i], left - 16 * i, base, l, s_at + p_column(i));
-    exp_of<MASK>(a + 16, sc[i + 1], left - 16 * i - 16, base, l, s_at + p_column(i + 1));
+  for (int i = 0; i < 4; i += kOnce) {
+    if constexpr (EXACT) {
+      tmem_ld16(s_at + 16 * i, a);
+      exp_of<true>(a, sc[i], left - 16 * i, base, l, s_at + p_column(i));
+    } else {
+      tmem_ld32(s_at + 16 * i, a);
+      tmem_ld_wait();
+      exp_of<false>(a, sc[i], left, base, l, s_at + p_column(i));
+      exp_of<false>(a + 16, sc[i + 1], left, base, l, s_at + p_column(i + 1));
+    }
   }
   tc::tmem_st_wait();
   tc_fence_before();
+  return false;
 }
 
 // Columns of a row of the output.
@@ -1004,6 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
       float m = -INFINITY, l = 0.f;
+      bool exact = false;
       for (int j = 0; j < steps; ++j, ++n, ++used) {
         // The scales first: they are there long before the scores.  Not at an item's first
         // unit: after units that this tile skipped, the scales' barrier may be any number of
@@ -1019,10 +1051,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4* sc = &ctl.scale[n % kScaleSlots][half * (kGroups / 2)];
           const int key0 = (w.lo + j) * kKeys;
           const int left = lim - key0 - half * kHalf;     // of this half of the unit
-          if (key0 + kKeys > lim_min)
-            softmax_unit<D, true>(s_at, o_at, sc, left, j == 0, m, l, mine_top, other_top, pair_id, ok);
-          else
-            softmax_unit<D, false>(s_at, o_at, sc, left, j == 0, m, l, mine_top, other_top, pair_id, ok);
+          // from its first masked unit on an item is masked
+          exact = exact || key0 + kKeys > lim_min;
+          bool first = j == 0;
+          if (__builtin_expect(!exact, 1)) {
+            exact = softmax_unit<D, false>(s_at, o_at, sc, left, first, m, l, mine_top, other_top, pair_id, ok);
+            first = false;
+          }
+          if (__builtin_expect(exact, 0)) softmax_unit<D, true>(s_at, o_at, sc, left, first, m, l, mine_top, other_top, pair_id, ok);
         } else if (j == 0) {
           // Warps without rows meet as well (the others do in softmax_unit): the first
           // product, which writes over all of O, waits for this half's warps only, and the

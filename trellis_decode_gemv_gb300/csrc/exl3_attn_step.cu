@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
             float x = fmaf(s[hf][nt][e], sc[hf].x, sc[hf].y);
             if (mask && key0 + hf * 16 + g + (e >> 1) * 8 >= lim[nt][e & 1]) x = -INFINITY;
             s[hf][nt][e] = x;
-            over |= x > m[nt][e & 1] + kRoom;
+            over |= x > room_above(m[nt][e & 1]);
           }
       if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
             // a row moves its own maximum only: what the other rows of the tile hold (nothing
             // of any request, past the item's rows) does not change its bits
-            const bool moves = top > m[nt][e] + kRoom;
+            const bool moves = top > room_above(m[nt][e]);
             const float next = top - kBelow;
             const float keep = moves ? ex2(m[nt][e] - next) : 1.f;   // 0 from a maximum of -inf
             if (moves) m[nt][e] = next;
