@@ -35,9 +35,9 @@
 // CTA sets its abort flag and the status word, every role stops waiting, the MMA
 // lane waits (bounded) for its MMAs and the producer for its copies, TMEM is freed.
 //
-// Measured (2070 MHz, 32 heads over 8, D = 128; one launch): a prompt of 8192 tokens 465
-// us, 1183 Tflop/s, the tensor pipe active for 52% of the cycles; four chunks of 512
-// tokens after 32K 818 us, 1323 Tflop/s, 56%.  An MMA of 128 x 128 x 16 takes 64 clocks, so a
+// Measured (2070 MHz, 32 heads over 8, D = 128; one launch): a prompt of 8192 tokens 464
+// us, 1185 Tflop/s, the tensor pipe active for 51% of the cycles; four chunks of 512
+// tokens after 32K 826 us, 1310 Tflop/s, 55%.  An MMA of 128 x 128 x 16 takes 64 clocks, so a
 // unit's 32 take 2048 at D = 128, and a unit takes about 3800.  Two things bound it:
 // a tile's S, softmax, P V one after another, because P lies in place of S and the
 // next S must wait for the product; and shared memory, which feeds two operands of S,
