@@ -521,6 +521,73 @@ exl3_status exl3_debug_stall_tensor_wait(int on);
  */
 exl3_status exl3_device_status(const void *status_word, exl3_stream_t stream);
 
+/* ---- norms, rotary positions -------------------------------------------------- */
+
+/** Longest row of a norm; most projections that one exl3_rms_norm_i8 serves. */
+#define EXL3_MAX_NORM 32768
+#define EXL3_MAX_NORM_OUTS 4
+
+/**
+ * The residual's addition and the root-mean-square norm, row by row:
+ *   h = x + residual (x without one),   y = h / sqrt(mean(h^2) + eps) * weight,
+ * in binary32, each output rounded once to binary16 (y from the h that is not
+ * rounded).
+ *   x, residual [rows][n] halves, row r at x + r * x_stride halves (strides
+ *   multiples of 8, at least n); residual may be NULL.  weight [n].
+ *   y [rows][n]; h [rows][n] or NULL, written only with a residual.
+ * y and h may be x or residual themselves (of stride n), but not one another.
+ * n a multiple of 8 up to EXL3_MAX_NORM.  One launch.
+ * Errors: EXL3_ERR_BATCH (rows < 0), EXL3_ERR_SHAPE (n, strides, eps negative or
+ * not finite), EXL3_ERR_NULL, EXL3_ERR_ALIGN.
+ */
+exl3_status exl3_rms_norm(const exl3_half *x, long long x_stride, const exl3_half *residual,
+                          long long residual_stride, const exl3_half *weight, float eps, int rows,
+                          int n, exl3_half *y, exl3_half *h, exl3_stream_t stream);
+
+/**
+ * The same for the int8 projections (exl3_gemm_i8) that read y: for each of
+ * `outs` (1 to EXL3_MAX_NORM_OUTS) the signs of its input side, the blockwise
+ * transform and the quantizer of exl3_quantize_act, all on binary32 values:
+ *   z = Hb(signs[o] (.) y)  (z = y where signs[o] is NULL),
+ *   qscale = max|z| / 127 over a block of 128,  q = nearest integer to z / qscale.
+ * A block of zeros has scale 0 and q 0, one that holds an infinity or a NaN scale
+ * NaN and q 0.
+ *   signs   host array of `outs` device pointers (length n each, or NULL)
+ *   q       [outs][rows][n] int8;  qscale [outs][rows][n / 128]
+ * n a multiple of 128 up to EXL3_MAX_NORM; the rest as exl3_rms_norm.  One launch.
+ * Errors: as exl3_rms_norm, and EXL3_ERR_BATCH (outs).
+ */
+exl3_status exl3_rms_norm_i8(const exl3_half *x, long long x_stride, const exl3_half *residual,
+                             long long residual_stride, const exl3_half *weight, float eps, int rows,
+                             int n, const exl3_half *const *signs, int outs, int8_t *q, float *qscale,
+                             exl3_half *h, exl3_stream_t stream);
+
+/**
+ * Rotary positions on queries and keys: of every head's first `rotary_dim`
+ * elements, pair i < rotary_dim / 2 is turned by position[t] * f_i and scaled,
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin),
+ * (a, b) the elements i and i + rotary_dim / 2, or 2i and 2i + 1 (`interleaved`);
+ * the other elements are copied.
+ *   freqs [rotary_dim / 2]: f_i as a fraction of a turn, f_i / (2 pi) * 2^64
+ *         rounded to an integer.  position * freqs modulo 2^64 is then the angle
+ *         with its whole turns gone, exact to 2^-34 of a turn at any position.
+ *   q [tokens][q_heads][head_dim] halves, token t at q + t * q_stride (strides
+ *         multiples of 8, at least heads * head_dim), k the same with its own
+ *         stride; k_heads 0: no keys (k, k_out may be NULL).  q_out and k_out may
+ *         be q and k (with the same strides).
+ *   position [tokens]: a token of a negative position belongs to no request
+ *         (exl3_kv_plan); it is copied as it is.
+ * Angles, cosines, sines and products are binary32, the results rounded once.
+ * head_dim and rotary_dim <= head_dim multiples of 16, head_dim up to 512.  One launch.
+ * Errors: EXL3_ERR_BATCH (tokens < 0), EXL3_ERR_SHAPE (heads, dims, strides, factor
+ * not finite), EXL3_ERR_NULL, EXL3_ERR_ALIGN.
+ */
+exl3_status exl3_rotary(const exl3_half *q, long long q_stride, exl3_half *q_out,
+                        long long q_out_stride, int q_heads, const exl3_half *k, long long k_stride,
+                        exl3_half *k_out, long long k_out_stride, int k_heads, int head_dim,
+                        int rotary_dim, int interleaved, const int32_t *position,
+                        const uint64_t *freqs, float factor, int tokens, exl3_stream_t stream);
+
 /* ---- attention over a paged key/value cache held in 8 bits -------------------
  *
  * What a decoder needs between the q/k/v projections and the output projection
@@ -653,6 +720,60 @@ exl3_status exl3_attention(const exl3_kv_cache *cache, const exl3_half *q, long 
                            int tokens, int max_new, const int32_t *block_table, int table_stride,
                            float scale, exl3_half *out, long long out_stride, float *lse,
                            void *workspace, size_t workspace_bytes, exl3_stream_t stream);
+
+/**
+ * Forks of requests: row i of a new block table continues request parent[i]
+ * (beams, samples of one prompt, a batch put together anew); a request that no
+ * row continues is finished.  parent[i] outside 0..requests-1: an empty row.
+ *   - Full pages are shared by all rows of a parent.  A partly filled page stays
+ *     with the parent's first row; each further row takes a page from the ring's
+ *     head, rows in order, and a copy (exl3_kv_copy).  A row for which the ring
+ *     holds no page any more becomes empty.
+ *   - Pages that a request held before and no row holds after go to the ring's
+ *     end, in ascending order (beyond the ring's capacity they are dropped).
+ * Outputs:
+ *   ctx_out     [rows]               the parent's ctx_len (cut to what the table
+ *                                    row holds); 0 of an empty row
+ *   table_out   [rows][table_stride] the row's pages, then -1
+ *   copy_from, copy_to, copy_tokens [rows]  page, page and filled tokens of the
+ *                                    row's copy; -1, -1, 0: none
+ *   free_pages                       the ring: returned pages are entered
+ *   free_state_out [3]               {head, count} after the call, and the rows
+ *                                    that got no page
+ * No output overlaps an input but the ring.  Page numbers outside 0..pages-1 are
+ * copied with the table and never returned.
+ * workspace: exl3_kv_fork_workspace_bytes(pages) bytes (0 for pages < 1),
+ * zero-filled once after allocation; every call leaves it zero again.  Calls that
+ * may run concurrently must not share one.  One launch.
+ * Errors: EXL3_ERR_BATCH (rows or requests outside 0..EXL3_MAX_REQUESTS),
+ * EXL3_ERR_SHAPE (page_size, pages < 1, table_stride < 1, free_capacity < 0),
+ * EXL3_ERR_NULL, EXL3_ERR_ALIGN, EXL3_ERR_WORKSPACE.
+ */
+size_t exl3_kv_fork_workspace_bytes(int pages);
+exl3_status exl3_kv_fork(const int32_t *parent, int rows, const int32_t *ctx_len, int requests,
+                         int page_size, int pages, int32_t *free_pages, int free_capacity,
+                         const int32_t *free_state, int32_t *free_state_out,
+                         const int32_t *block_table, int table_stride, int32_t *ctx_out,
+                         int32_t *table_out, int32_t *copy_from, int32_t *copy_to,
+                         int32_t *copy_tokens, void *workspace, size_t workspace_bytes,
+                         exl3_stream_t stream);
+
+/** Most layers of one exl3_kv_copy. */
+#define EXL3_MAX_LAYERS 512
+
+/**
+ * The pages that forks have to copy, in the caches of all layers at once: for
+ * every pair i the first tokens[i] tokens (cut to 0..page_size) of page from[i]
+ * into page to[i], keys, values and scales of all heads.  Pairs with a page
+ * outside the pool (-1) are skipped.  No page is the target of two pairs, nor
+ * the source of one and the target of another.
+ *   caches  host array of `layers` caches (at most EXL3_MAX_LAYERS) of equal
+ *           pages, kv_heads, page_size and head_dim
+ * One launch.  Errors: EXL3_ERR_BATCH (layers, pairs < 0), EXL3_ERR_NULL, EXL3_ERR_SHAPE
+ * (cache fields, caches that differ), EXL3_ERR_ALIGN.
+ */
+exl3_status exl3_kv_copy(const exl3_kv_cache *caches, int layers, const int32_t *from,
+                         const int32_t *to, const int32_t *tokens, int pairs, exl3_stream_t stream);
 
 /** Size of the fixed device array that exl3_gemv_noalloc uses as scratch. */
 #define EXL3_NOALLOC_SCRATCH_BYTES (4u << 20)

@@ -9,6 +9,7 @@ and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -101,6 +102,12 @@ _SIGNATURES = {
     "exl3_attention_workspace_bytes": ([_I, _I, _I, _I], _SZ),
     "exl3_attention": ([ctypes.POINTER(Exl3KvCacheStruct), _P, _LL, _I, _P, _P, _I, _I, _I, _P, _I, ctypes.c_float,
                         _P, _LL, _P, _P, _SZ, _P], _I),
+    "exl3_rms_norm": ([_P, _LL, _P, _LL, _P, ctypes.c_float, _I, _I, _P, _P, _P], _I),
+    "exl3_rms_norm_i8": ([_P, _LL, _P, _LL, _P, ctypes.c_float, _I, _I, ctypes.POINTER(_P), _I, _P, _P, _P, _P], _I),
+    "exl3_rotary": ([_P, _LL, _P, _LL, _I, _P, _LL, _P, _LL, _I, _I, _I, _I, _P, _P, ctypes.c_float, _I, _P], _I),
+    "exl3_kv_fork_workspace_bytes": ([_I], _SZ),
+    "exl3_kv_fork": ([_P, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "exl3_kv_copy": ([ctypes.POINTER(Exl3KvCacheStruct), _I, _P, _P, _P, _I, _P], _I),
     "exl3_set_path": ([_I], _I),
     "exl3_set_prefill": ([_I], _I),
     "exl3_debug_stall_tensor_wait": ([_I], _I),
@@ -908,3 +915,257 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
         _ptr(lse, "lse", _F32, dev), _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(),
         _stream(dev)))
     return out if lse is None else (out, lse)
+
+
+# ---- norms, rotary positions ---------------------------------------------------------
+
+MAX_NORM = 32768
+MAX_NORM_OUTS = 4
+
+
+def _matrix(t, name, n, dev, rows=None):
+    """Pointer and row stride of halves [rows, n] whose rows may be apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or t.shape[1] != n or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, {n}]")
+    if t.device.type != "cuda" or t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {'a GPU' if dev.type != 'cuda' else dev}")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float16")
+    stride = t.stride()
+    if stride[1] != 1 and n > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), stride[0] if t.shape[0] > 1 else n
+
+
+def _norm_inputs(x, weight, residual):
+    if x.dim() not in (1, 2):
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows, n] or [n]")
+    x2 = x if x.dim() == 2 else x.view(1, -1)
+    rows, n = x2.shape
+    dev = x.device
+    xp, xs = _matrix(x2, "x", n, dev)
+    rp, rs = (None, n) if residual is None else _matrix(residual.view(x2.shape) if x.dim() == 1 else residual, "residual", n, dev, rows)
+    if weight.numel() != n:
+        raise ValueError(f"weight holds {weight.numel()} elements, expected {n}")
+    return rows, n, dev, xp, xs, rp, rs, _ptr(weight, "weight", _HALF, dev)
+
+
+def _norm_out(t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def exl3_rms_norm(x, weight, eps, residual=None, out=None, h=None):
+    """Residual addition and root-mean-square norm of binary16 rows x [rows, n] (or [n]; rows
+    may be apart): returns (y, h), h = x + residual rounded to binary16, y its norm
+    (taken before that rounding) times weight [n].  Without a residual h is x.  out and h
+    may be x or residual themselves."""
+    rows, n, dev, xp, xs, rp, rs, wp = _norm_inputs(x, weight, residual)
+    out = _norm_out(out, "out", x.shape, torch.float16, dev)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is an output of the addition: there is no residual")
+        h = x
+    else:
+        h = _norm_out(h, "h", x.shape, torch.float16, dev)
+    _check(load_library().exl3_rms_norm(xp, xs, rp, rs, wp, eps, rows, n, _ptr(out, "out", _HALF, dev),
+                                        None if residual is None else _ptr(h, "h", _HALF, dev), _stream(dev)))
+    return out, h
+
+
+def exl3_rms_norm_i8(x, weight, eps, signs, residual=None, q=None, qscale=None, h=None):
+    """The same with the outputs that int8 projections read (exl3_gemm_i8): for each of
+    `signs` (1 to 4 tensors s_in [n], or None for a projection without input rotation) the
+    rotation and the int8 quantization with a scale for each 128 values.  Returns (q int8
+    [outs, rows, n], qscale float32 [outs, rows, n / 128], h); x [n]: without the rows."""
+    rows, n, dev, xp, xs, rp, rs, wp = _norm_inputs(x, weight, residual)
+    outs = len(signs)
+    ptrs = (_P * max(outs, 1))(*[_ptr(s, f"signs[{i}]", _HALF, dev) for i, s in enumerate(signs)])
+    for i, s in enumerate(signs):
+        if s is not None and s.numel() != n:
+            raise ValueError(f"signs[{i}] holds {s.numel()} elements, expected {n}")
+    lead = (outs,) + tuple(x.shape[:-1])
+    q = _norm_out(q, "q", lead + (n,), torch.int8, dev)
+    qscale = _norm_out(qscale, "qscale", lead + (n // 128,), torch.float32, dev)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is an output of the addition: there is no residual")
+        h = x
+    else:
+        h = _norm_out(h, "h", x.shape, torch.float16, dev)
+    _check(load_library().exl3_rms_norm_i8(xp, xs, rp, rs, wp, eps, rows, n, ptrs, outs, _ptr(q, "q", _I8, dev),
+                                           _ptr(qscale, "qscale", _F32, dev),
+                                           None if residual is None else _ptr(h, "h", _HALF, dev), _stream(dev)))
+    return q, qscale, h
+
+
+class Exl3RotaryFreqs:
+    """What exl3_rotary takes of a model's rotary positions: freqs int64 [rotary_dim / 2],
+    each pair's angle a position as a 64-bit fraction of a turn, and the factor on
+    cosines and sines."""
+
+    def __init__(self, radians, factor=1.0, device="cuda"):
+        """radians: the angle of each pair at position 1 (floats)."""
+        turns = [int(round(float(r) / (2 * math.pi) * 2.0 ** 64)) & (2 ** 64 - 1) for r in radians]
+        signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+        self.rotary_dim = 2 * len(signed)
+        self.factor = float(factor)
+        self.freqs = torch.tensor(signed, dtype=torch.int64).to(device)
+
+
+def exl3_rotary_freqs(rotary_dim, base=10000.0, scaling="none", scale=1.0, original=8192, device="cuda", low=1.0, high=4.0,
+                      fast=32.0, slow=1.0, factor=None):
+    """Rotary frequencies base**(-2i / rotary_dim), scaled for contexts `scale` times longer than
+    the `original` one:
+      none, linear (all over scale), ntk (a larger base);
+      llama3: pairs that turn less than `low` times within the original context over
+        scale, more than `high` times as they are, between them a mixture;
+      yarn: the same between `slow` and `fast` turns, linear in the pair's number, and a
+        factor of 0.1 ln(scale) + 1 on cosine and sine.
+    factor: another factor on cosine and sine than the scaling's own."""
+    if rotary_dim < 2 or rotary_dim % 2 or base <= 1.0 or scale < 1.0:
+        raise ValueError(f"rotary_dim {rotary_dim}, base {base}, scale {scale}: expected an even number, more than 1, at least 1")
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * scale ** (rotary_dim / (rotary_dim - 2))
+    radians = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    own_factor = 1.0
+    if scaling == "linear":
+        radians = [r / scale for r in radians]
+    elif scaling == "llama3":
+        if high <= low:
+            raise ValueError(f"low {low} and high {high}: expected low < high")
+        mix = [min(max((original * r / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for r in radians]
+        radians = [r / scale * (1 - k) + r * k for r, k in zip(radians, mix)]
+    elif scaling == "yarn":
+        def pair(turns):
+            return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        first, last = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary_dim - 1)
+        drop = [min(max((i - first) / max(last - first, 0.001), 0.0), 1.0) for i in range(len(radians))]
+        radians = [r / scale * k + r * (1 - k) for r, k in zip(radians, drop)]
+        own_factor = 0.1 * math.log(scale) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling {scaling!r}: expected none, linear, ntk, llama3 or yarn")
+    return Exl3RotaryFreqs(radians, own_factor if factor is None else factor, device)
+
+
+def exl3_rotary(q, k, position, freqs, interleaved=False, q_out=None, k_out=None):
+    """Rotary positions on q [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim] halves
+    (slices of a fused projection's output, say; k may be None), position int32
+    [tokens], freqs an Exl3RotaryFreqs.  Returns (q_out, k_out), new tensors unless
+    given; they may be q and k.  Tokens of negative position are copied as they are."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
+    tokens, heads, dim = q.shape
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    qp, qs = _rows(q, "q", dim, dev)
+    kp, ks, kv_heads = None, 0, 0
+    if k is not None:
+        kp, ks = _rows(k, "k", dim, dev)
+        kv_heads = k.shape[1]
+        if k.shape[0] != tokens:
+            raise ValueError(f"k has {k.shape[0]} tokens, q {tokens}")
+    if position.numel() != tokens:
+        raise ValueError(f"position holds {position.numel()} elements for {tokens} tokens")
+
+    def room(name, t, like):
+        if t is None:
+            t = torch.empty(like.shape, dtype=torch.float16, device=dev)
+            return t, t.data_ptr(), like.shape[1] * dim
+        if t.shape != like.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+        return (t,) + _rows(t, name, dim, dev)
+
+    q_out, qo, qos = room("q_out", q_out, q)
+    ko, kos = None, 0
+    if k is not None:
+        k_out, ko, kos = room("k_out", k_out, k)
+    _check(load_library().exl3_rotary(
+        qp, qs, qo, qos, heads, kp, ks, ko, kos, kv_heads, dim, freqs.rotary_dim, 1 if interleaved else 0,
+        _ptr(position, "position", _I32, dev), _ptr(freqs.freqs, "freqs", _I64, dev), freqs.factor, tokens, _stream(dev)))
+    return q_out, k_out
+
+
+# ---- forks of requests ---------------------------------------------------------------
+
+MAX_LAYERS = 512
+
+
+class Exl3KvFork:
+    """What exl3_kv_fork returns: ctx_len [rows], block_table [rows, width], copy_from, copy_to,
+    copy_tokens [rows], free_state [3], all int32."""
+
+    def __init__(self, rows, width, dev):
+        room = torch.empty(4 * rows + 3, dtype=torch.int32, device=dev)
+        self.ctx_len, self.copy_from, self.copy_to, self.copy_tokens, self.free_state = room.split([rows, rows, rows, rows, 3])
+        self.block_table = torch.empty((rows, width), dtype=torch.int32, device=dev)
+
+
+def exl3_kv_fork_workspace_bytes(pages: int) -> int:
+    return int(load_library().exl3_kv_fork_workspace_bytes(pages))
+
+
+def alloc_kv_fork_workspace(pages: int, device) -> torch.Tensor:
+    """A zero-filled workspace for exl3_kv_fork."""
+    nbytes = exl3_kv_fork_workspace_bytes(pages)
+    if nbytes == 0:
+        raise Exl3Error(2, "invalid number of pages for a workspace")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def exl3_kv_fork(parent, ctx_len, page_size, pages, free_pages, free_state, block_table, workspace=None, out=None):
+    """A block table whose row i continues request parent[i] (int32 [rows], -1: an empty row): see
+    the header.  ctx_len [requests], block_table [requests, width], the ring free_pages
+    and its free_state as exl3_kv_plan's.  Returns an Exl3KvFork (`out`, if given, of
+    the same rows and width); its copy_from, copy_to and copy_tokens go to
+    exl3_kv_copy before the rows are used."""
+    dev = ctx_len.device
+    rows, n = parent.numel(), ctx_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] < n or free_state.numel() < 2:
+        raise ValueError(f"{n} requests with block_table of {tuple(block_table.shape)} and free_state of {free_state.numel()}")
+    width = block_table.shape[1]
+    if out is None:
+        out = Exl3KvFork(rows, width, dev)
+    elif out.block_table.shape != (rows, width) or out.block_table.device != dev:
+        raise ValueError(f"out holds a table of {tuple(out.block_table.shape)} on {out.block_table.device}, "
+                         f"expected {(rows, width)} on {dev}")
+    if workspace is None:
+        workspace = alloc_kv_fork_workspace(pages, dev)
+    _check(load_library().exl3_kv_fork(
+        _ptr(parent, "parent", _I32, dev), rows, _ptr(ctx_len, "ctx_len", _I32, dev), n, page_size, pages,
+        _ptr(free_pages, "free_pages", _I32, dev), free_pages.numel(), _ptr(free_state, "free_state", _I32, dev),
+        out.free_state.data_ptr(), _ptr(block_table, "block_table", _I32, dev), width, out.ctx_len.data_ptr(),
+        out.block_table.data_ptr(), out.copy_from.data_ptr(), out.copy_to.data_ptr(), out.copy_tokens.data_ptr(),
+        _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(), _stream(dev)))
+    return out
+
+
+class Exl3KvCacheGroup:
+    """The caches of a model's layers, marshalled once for exl3_kv_copy."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches or len(self.caches) > MAX_LAYERS:
+            raise ValueError(f"{len(self.caches)} caches: expected 1 to {MAX_LAYERS}")
+        self.device = self.caches[0].device
+        if any(c.device != self.device for c in self.caches):
+            raise ValueError("the caches of a group must be on one device")
+        self.structs = (Exl3KvCacheStruct * len(self.caches))(*[c.struct for c in self.caches])
+
+
+def exl3_kv_copy(caches, copy_from, copy_to, copy_tokens):
+    """Copy the first copy_tokens[i] tokens of page copy_from[i] into page copy_to[i] in all
+    layers of `caches` (an Exl3KvCacheGroup), with the pages' scales; -1: no copy."""
+    dev = caches.device
+    pairs = copy_from.numel()
+    if copy_to.numel() != pairs or copy_tokens.numel() != pairs:
+        raise ValueError(f"{pairs} pages to copy from, {copy_to.numel()} to copy to, {copy_tokens.numel()} token counts")
+    _check(load_library().exl3_kv_copy(
+        caches.structs, len(caches.caches), _ptr(copy_from, "copy_from", _I32, dev), _ptr(copy_to, "copy_to", _I32, dev),
+        _ptr(copy_tokens, "copy_tokens", _I32, dev), pairs, _stream(dev)))
