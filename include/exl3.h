@@ -722,6 +722,39 @@ exl3_status exl3_attention(const exl3_kv_cache *cache, const exl3_half *q, long 
                            void *workspace, size_t workspace_bytes, exl3_stream_t stream);
 
 /**
+ * exl3_attention for requests that share their leading tokens (what exl3_kv_fork
+ * makes of one prompt, or requests behind one system prompt): the keys that a group
+ * shares are read once for all of its rows.
+ *   group_start [groups + 1]: group g is the requests group_start[g] ..
+ *       group_start[g + 1] - 1 (nondecreasing; a request outside all groups shares
+ *       nothing)
+ *   prefix_len [groups]: the leading tokens that the requests of a group have in
+ *       common, 0 allowed.  Of these as many are read once as are a multiple of 32
+ *       (head_dim 128), 64 (head_dim 64) or 128 (max_new * q_heads / kv_heads above 48),
+ *       from the pages of the group's first request that holds them all; where the
+ *       pages of the others hold something else, the result is that of neither.
+ *       A request that holds fewer cached tokens than that, and one that is alone
+ *       in its group, is computed from its own pages throughout.
+ *   max_group: the most new tokens that the requests of a group bring together; like
+ *       max_new it picks the kernels and sizes the workspace.
+ *   workspace: exl3_attention_shared_workspace_bytes of at least these sizes, under
+ *       exl3_attention's rules; 0 for sizes that a call would refuse.
+ * All else, the precision and the errors as exl3_attention; EXL3_ERR_BATCH also for
+ * groups < 0, requests + groups above EXL3_MAX_REQUESTS and max_group < 1.  Two to four
+ * launches.
+ */
+size_t exl3_attention_shared_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_new,
+                                             int max_group, int tokens);
+exl3_status exl3_attention_shared(const exl3_kv_cache *cache, const exl3_half *q,
+                                  long long q_stride, int q_heads, const int32_t *q_start,
+                                  const int32_t *seq_len, int requests, int tokens, int max_new,
+                                  const int32_t *block_table, int table_stride,
+                                  const int32_t *group_start, const int32_t *prefix_len, int groups,
+                                  int max_group, float scale, exl3_half *out, long long out_stride,
+                                  float *lse, void *workspace, size_t workspace_bytes,
+                                  exl3_stream_t stream);
+
+/**
  * Forks of requests: row i of a new block table continues request parent[i]
  * (beams, samples of one prompt, a batch put together anew); a request that no
  * row continues is finished.  parent[i] outside 0..requests-1: an empty row.

@@ -108,6 +108,32 @@ def test_copy_refusals(lib, kw, status):
     assert _copy(lib, **kw) == status
 
 
+def _shared(lib, **kw):
+    a = dict(cache=ctypes.byref(_struct()), q=A, qs=256, heads=4, start=A, seq=A, requests=2, tokens=3, max_new=2, table=A, stride=4, gs=A,
+             pl=A, groups=1, max_group=2, scale=0.125, out=A, os=256, lse=A, ws=A, wsb=1 << 30) | kw
+    return lib.exl3_attention_shared(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(cache=None), 1), (dict(heads=3), 2), (dict(stride=0), 2), (dict(qs=248), 2), (dict(os=260), 2), (dict(requests=-1), 5),
+    (dict(requests=B.MAX_REQUESTS), 5), (dict(groups=-1), 5), (dict(groups=B.MAX_REQUESTS), 5), (dict(tokens=-1), 5), (dict(max_new=0), 5),
+    (dict(max_group=0), 5), (dict(q=None), 1), (dict(start=None), 1), (dict(gs=None), 1), (dict(pl=None), 1), (dict(out=None), 1),
+    (dict(q=A + 2), 6), (dict(gs=A + 2), 6), (dict(pl=A + 1), 6), (dict(lse=A + 2), 6), (dict(ws=A + 4), 6), (dict(ws=None), 7),
+    (dict(wsb=64), 7), (dict(requests=0), 0), (dict(tokens=0), 0)])
+def test_attention_shared_refusals(lib, kw, status):
+    assert _shared(lib, **kw) == status
+
+
+def test_attention_shared_workspace_bytes(lib):
+    size = lib.exl3_attention_shared_workspace_bytes
+    few, more, many = size(32, 8, 128, 1, 8, 8), size(32, 8, 128, 1, 8, 9), size(32, 8, 128, 1, 64, 64)
+    assert lib.exl3_attention_workspace_bytes(32, 8, 128, 1) < few < more < many
+    assert more - few == 2 * 32 * (128 + 2) * 4        # the two parts of a token's rows
+    for bad in ((0, 8, 128, 1, 1, 1), (33, 8, 128, 1, 1, 1), (32, 8, 96, 1, 1, 1), (32, 8, 128, 0, 1, 1), (32, 8, 128, 1, 0, 1),
+                (32, 8, 128, 1, 1, 0)):
+        assert size(*bad) == 0
+
+
 def test_binding_refuses_cpu_tensors_and_shapes():
     x, w = torch.zeros((2, 256), dtype=torch.float16), torch.ones(256, dtype=torch.float16)
     pos, f = torch.zeros(2, dtype=torch.int32), B.exl3_rotary_freqs(64, device="cpu")

@@ -15,6 +15,7 @@ _BINDING_NAMES = (
     "CB_3INST", "CB_1MAD",
     "Exl3KvCache", "exl3_kv_plan", "exl3_kv_append", "exl3_attention", "exl3_attention_workspace_bytes",
     "alloc_attention_workspace",
+    "exl3_attention_shared", "exl3_attention_shared_workspace_bytes", "alloc_attention_shared_workspace",
     "exl3_rms_norm", "exl3_rms_norm_i8", "exl3_rotary", "exl3_rotary_freqs", "Exl3RotaryFreqs",
     "Exl3KvFork", "exl3_kv_fork", "exl3_kv_fork_workspace_bytes", "alloc_kv_fork_workspace", "Exl3KvCacheGroup", "exl3_kv_copy",
 )

@@ -108,6 +108,9 @@ _SIGNATURES = {
     "exl3_kv_fork_workspace_bytes": ([_I], _SZ),
     "exl3_kv_fork": ([_P, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
     "exl3_kv_copy": ([ctypes.POINTER(Exl3KvCacheStruct), _I, _P, _P, _P, _I, _P], _I),
+    "exl3_attention_shared_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _SZ),
+    "exl3_attention_shared": ([ctypes.POINTER(Exl3KvCacheStruct), _P, _LL, _I, _P, _P, _I, _I, _I, _P, _I, _P, _P, _I, _I,
+                               ctypes.c_float, _P, _LL, _P, _P, _SZ, _P], _I),
     "exl3_set_path": ([_I], _I),
     "exl3_set_prefill": ([_I], _I),
     "exl3_debug_stall_tensor_wait": ([_I], _I),
@@ -884,6 +887,22 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
     Returns out (like q), or (out, lse) with lse a float32 tensor [tokens,
     q_heads] to write or True for a new one."""
     dev = cache.device
+    dim, heads, tokens, n, qp, qs, scale, out, op, os_, lse = _attention_arguments(cache, q, q_start, seq_len, block_table, scale, out, lse)
+    if max_new is None:
+        max_new = max(tokens, 1)
+    if workspace is None:
+        workspace = alloc_attention_workspace(heads, cache.kv_heads, dim, max_new, dev)
+    _check(load_library().exl3_attention(
+        cache._ref, qp, qs, heads, _ptr(q_start, "q_start", _I32, dev), _ptr(seq_len, "seq_len", _I32, dev), n, tokens,
+        max_new, _ptr(block_table, "block_table", _I32, dev), block_table.shape[1], scale, op, os_,
+        _ptr(lse, "lse", _F32, dev), _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(),
+        _stream(dev)))
+    return out if lse is None else (out, lse)
+
+
+def _attention_arguments(cache, q, q_start, seq_len, block_table, scale, out, lse):
+    """What the attention calls have in common: their checks, and the outputs that are not given."""
+    dev = cache.device
     dim = cache.head_dim
     qp, qs = _rows(q, "q", dim, dev)
     tokens, heads, _ = q.shape
@@ -892,8 +911,6 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
         raise ValueError(f"{n} requests with q_start of {q_start.numel()} and block_table of {tuple(block_table.shape)}")
     if heads % cache.kv_heads:
         raise ValueError(f"q has {heads} heads for a cache of {cache.kv_heads}")
-    if max_new is None:
-        max_new = max(tokens, 1)
     if scale is None:
         scale = dim ** -0.5
     if out is None:
@@ -907,13 +924,44 @@ def exl3_attention(cache, q, q_start, seq_len, block_table, max_new=None, scale=
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
     elif lse is not None and lse.shape != (tokens, heads):
         raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(tokens, heads)}")
+    return dim, heads, tokens, n, qp, qs, scale, out, op, os_, lse
+
+
+def exl3_attention_shared_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, max_new: int, max_group: int, tokens: int) -> int:
+    return int(load_library().exl3_attention_shared_workspace_bytes(q_heads, kv_heads, head_dim, max_new, max_group, tokens))
+
+
+def alloc_attention_shared_workspace(q_heads: int, kv_heads: int, head_dim: int, max_new: int, max_group: int, tokens: int,
+                                     device) -> torch.Tensor:
+    """A zero-filled workspace for exl3_attention_shared calls of up to these sizes."""
+    nbytes = exl3_attention_shared_workspace_bytes(q_heads, kv_heads, head_dim, max_new, max_group, tokens)
+    if nbytes == 0:
+        raise Exl3Error(2, "invalid heads, head_dim, max_new, max_group or tokens for a workspace")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def exl3_attention_shared(cache, q, q_start, seq_len, block_table, group_start, prefix_len, max_new=None, max_group=None,
+                          scale=None, out=None, lse=None, workspace=None):
+    """exl3_attention for groups of consecutive requests that share their leading tokens, whose
+    keys are read once for a whole group (see the header): group_start [groups + 1] and
+    prefix_len [groups] int32.  max_group: the most new tokens of a group (default: all
+    tokens of the call).  The rest as exl3_attention."""
+    dev = cache.device
+    dim, heads, tokens, n, qp, qs, scale, out, op, os_, lse = _attention_arguments(cache, q, q_start, seq_len, block_table, scale, out, lse)
+    groups = prefix_len.numel()
+    if group_start.numel() != groups + 1:
+        raise ValueError(f"group_start of {group_start.numel()} for {groups} prefixes")
+    if max_new is None:
+        max_new = max(tokens, 1)
+    if max_group is None:
+        max_group = max(tokens, 1)
     if workspace is None:
-        workspace = alloc_attention_workspace(heads, cache.kv_heads, dim, max_new, dev)
-    _check(load_library().exl3_attention(
+        workspace = alloc_attention_shared_workspace(heads, cache.kv_heads, dim, max_new, max_group, max(tokens, 1), dev)
+    _check(load_library().exl3_attention_shared(
         cache._ref, qp, qs, heads, _ptr(q_start, "q_start", _I32, dev), _ptr(seq_len, "seq_len", _I32, dev), n, tokens,
-        max_new, _ptr(block_table, "block_table", _I32, dev), block_table.shape[1], scale, op, os_,
-        _ptr(lse, "lse", _F32, dev), _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(),
-        _stream(dev)))
+        max_new, _ptr(block_table, "block_table", _I32, dev), block_table.shape[1], _ptr(group_start, "group_start", _I32, dev),
+        _ptr(prefix_len, "prefix_len", _I32, dev), groups, max_group, scale, op, os_, _ptr(lse, "lse", _F32, dev),
+        _ptr(workspace, "workspace", (torch.uint8,), dev), workspace.numel(), _stream(dev)))
     return out if lse is None else (out, lse)
 
 

@@ -55,7 +55,7 @@ struct SplitItem {
   int t0, n, seq, rows;   // its request
   int base, head;         // its first row, its key/value head
   int last;               // the range in which it ends, -1: no such item
-  int unused;
+  int own;                // calls with prefixes: of a request's own keys
 };
 
 struct AttnParams {
@@ -83,28 +83,102 @@ struct AttnParams {
   uint32_t* arrived;
   SplitItem* split;        // [kMaxPromptCtas]: many rows, that item
   float* partial;          // [2 * kMaxCtas] slots: 2c the item that began before CTA c's range, 2c + 1 the one that ends after it
+  // calls with prefixes only
+  const int32_t* group_start;
+  const int32_t* prefix_len;
+  int groups, align;       // prefixes count up to a multiple of `align` keys, whole units of the kernel that goes on
+  int prefix_lo, prefix_hi;  // prefixes with rows in [prefix_lo, prefix_hi] are this launch's
+  float* part;             // sums of every row over the prefix, then over its own keys: [2][tokens][q_heads][head_dim]
+  float2* part_ml;         // their m and l: [2][tokens][q_heads]
 };
 
 // A request as the kernels see it; lengths are cut to what the table and the
-// arrays hold.
+// arrays hold.  In a call with prefixes (SHARED) `groups` of these come before the
+// requests: the prefix of group g with the rows of all its requests.
 struct Req {
   int t0, n, rows;  // first token, new tokens, rows (new * group), 0 if another launch's
-  int seq;          // cached tokens, the new ones included
+  int seq;          // cached tokens, the new ones included; a prefix's length
+  int late;         // token i of it sees the keys before min(seq, late + i + 1)
+  int k0;           // its first key: those before are its group's prefix
+  int row;          // of the block table
 };
 
-__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
-  Req r{0, 0, 0, 0};
-  if (b < p.requests) {
-    const int a = min(max(p.q_start[b], 0), p.tokens);
-    const int e = min(max(p.q_start[b + 1], 0), p.tokens);
-    r.t0 = a;
-    r.n = max(e - a, 0);
-    const long long rows = static_cast<long long>(r.n) * p.group;
-    r.rows = rows >= p.rows_lo && rows <= p.rows_hi ? static_cast<int>(rows) : 0;
-    r.seq = static_cast<int>(min(static_cast<long long>(max(p.seq_len[b], 0)), p.most));
+template <bool SHARED>
+__device__ __forceinline__ int req_count(const AttnParams& p) { return SHARED ? p.groups + p.requests : p.requests; }
+
+__device__ __forceinline__ int first_token(const AttnParams& p, int b) { return min(max(p.q_start[b], 0), p.tokens); }
+__device__ __forceinline__ int cached_tokens(const AttnParams& p, int b) {
+  return static_cast<int>(min(static_cast<long long>(max(p.seq_len[b], 0)), p.most));
+}
+__device__ __forceinline__ void set_rows(const AttnParams& p, Req& r, int lo, int hi) {
+  const long long rows = static_cast<long long>(r.n) * p.group;
+  r.rows = rows >= lo && rows <= hi ? static_cast<int>(rows) : 0;
+}
+
+struct Group {
+  int a, e, prefix;  // requests a .. e - 1; the shared keys, 0 where one request alone would share them
+};
+__device__ __forceinline__ Group load_group(const AttnParams& p, int g) {
+  Group x;
+  x.a = min(max(p.group_start[g], 0), p.requests);
+  x.e = min(max(p.group_start[g + 1], x.a), p.requests);
+  const long long len = min(static_cast<long long>(max(p.prefix_len[g], 0)), p.most);
+  x.prefix = x.e - x.a > 1 ? static_cast<int>(len) & ~(p.align - 1) : 0;
+  return x;
+}
+
+// A prefix: its pages are those of the first request that holds all of it.
+__device__ __forceinline__ Req load_prefix(const AttnParams& p, int g) {
+  Req r{0, 0, 0, 0, 0, 0, 0};
+  const Group x = load_group(p, g);
+  if (x.prefix == 0) return r;
+  for (int b = x.a; b < x.e; ++b) {
+    const int n = max(first_token(p, b + 1) - first_token(p, b), 0);
+    if (cached_tokens(p, b) - n < x.prefix) continue;
+    r.t0 = first_token(p, x.a);
+    r.n = max(first_token(p, x.e) - r.t0, 0);
+    r.seq = r.late = x.prefix;
+    r.row = b;
+    set_rows(p, r, p.prefix_lo, p.prefix_hi);
+    break;
   }
   return r;
 }
+
+template <bool SHARED>
+__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
+  Req r{0, 0, 0, 0, 0, 0, 0};
+  if constexpr (SHARED) {
+    if (b < p.groups) return load_prefix(p, b);
+    b -= p.groups;
+  }
+  if (b < p.requests) {
+    const int a = first_token(p, b);
+    const int e = first_token(p, b + 1);
+    r.t0 = a;
+    r.n = max(e - a, 0);
+    set_rows(p, r, p.rows_lo, p.rows_hi);
+    r.seq = cached_tokens(p, b);
+    r.late = r.seq - r.n;
+    r.row = b;
+    if constexpr (SHARED) {
+      int g = -1, hi = p.groups;   // the last group that begins at b or before
+      while (hi - g > 1) {
+        const int mid = (g + hi) >> 1;
+        if (p.group_start[mid] <= b) g = mid; else hi = mid;
+      }
+      if (g >= 0) {
+        const Group x = load_group(p, g);
+        if (b < x.e && r.late >= x.prefix) r.k0 = x.prefix;
+      }
+    }
+  }
+  return r;
+}
+
+// The first key that token `tok` of a request does not see.
+template <bool SHARED>
+__device__ __forceinline__ int sees_before(const Req& r, int tok) { return SHARED ? min(r.seq, r.late + tok + 1) : r.late + tok + 1; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -199,6 +273,9 @@ constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kSt
 
 // More: tiles of 256 rows.
 constexpr size_t prompt_slot_floats(int head_dim) { return static_cast<size_t>(256) * (head_dim + 2); }
+// Keys of a unit of the few-rows kernel (`step`) and of the other.
+constexpr int step_unit(int head_dim) { return 4096 / head_dim; }
+constexpr int kPromptUnit = 128;
 exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, bool after_step, cudaStream_t stream);
 exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream);
 

@@ -64,7 +64,7 @@ using tc::tc_fence_before;
 
 constexpr int kTile = 128;             // rows of an MMA tile
 constexpr int kItemRows = 2 * kTile;
-constexpr int kKeys = 128;             // keys of a unit
+constexpr int kKeys = kPromptUnit;     // keys of a unit
 constexpr int kGroups = kKeys / 16;    // scale groups of a unit
 constexpr int kMmaWarp = 0;
 constexpr int kLoadWarp = 1;
@@ -226,9 +226,15 @@ constexpr uint32_t idesc(int n, bool transposed) {
 
 __device__ __forceinline__ int row_tiles(int rows) { return (rows + kItemRows - 1) / kItemRows; }
 // Units of row tile `rt`: up to the last key that its last row sees, at least one.
-__device__ __forceinline__ int tile_units(const AttnParams& p, int n, int seq, int rt) {
+// `seq` and `late` count from the first of the request's keys.
+template <bool SHARED>
+__device__ __forceinline__ int tile_units(const AttnParams& p, int n, int late, int seq, int rt) {
   const int last = (min((rt + 1) * kItemRows, n * p.group) - 1) / p.group;
-  return max(1, (seq - n + last + kKeys) / kKeys);
+  return max(1, ((SHARED ? min(seq, late + last + 1) : late + last + 1) + kKeys - 1) / kKeys);
+}
+template <bool SHARED>
+__device__ __forceinline__ int tile_units(const AttnParams& p, const Req& r, int rt) {
+  return tile_units<SHARED>(p, r.n, r.late - r.k0, r.seq - r.k0, rt);
 }
 
 // An item of at most kWhole units is not split: leaving and joining partial results
@@ -244,6 +250,7 @@ constexpr int kItemCost = 3;
 
 // The items of a range: row tiles in order, the heads of a row tile after one
 // another.
+template <bool SHARED>
 struct Walker {
   const AttnParams& p;
   int left;   // units of the range from the current item's first on
@@ -251,7 +258,7 @@ struct Walker {
   Req r;
   __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, int count)
       : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
-    units = tile_units(p, r.n, r.seq, rt);
+    units = tile_units<SHARED>(p, r, rt);
     if (lo == units) advance();
     hi = min(units, lo + left);
   }
@@ -262,10 +269,10 @@ struct Walker {
       if (++rt == row_tiles(r.rows)) {
         rt = 0;
         do {
-          r = load_req(p, ++b);
-        } while (r.rows == 0 && b < p.requests);
+          r = load_req<SHARED>(p, ++b);
+        } while (r.rows == 0 && b < req_count<SHARED>(p));
       }
-      units = tile_units(p, r.n, r.seq, rt);
+      units = tile_units<SHARED>(p, r, rt);
     }
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
@@ -322,17 +329,19 @@ __device__ __forceinline__ void block_scan(long long* room, long long (&v)[N], l
 
 // `room`: 12 bytes for each request (borrowed from the operand images).  False: the
 // CTA has nothing to do.
+template <bool SHARED>
 __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void* room, int& ctas, int& count) {
   const int tid = threadIdx.x;
+  const int requests = req_count<SHARED>(p);
   int32_t* first = static_cast<int32_t*>(room);    // row tiles before each request
-  int2* req = reinterpret_cast<int2*>(first + ((p.requests + 1) & ~1));  // its new tokens (0: another launch's) and length
-  const int per = (p.requests + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
+  int2* req = reinterpret_cast<int2*>(first + ((requests + 1) & ~1));  // its new tokens (0: another launch's) and keys
+  const int per = (requests + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, requests), b1 = min(b0 + per, requests);
   long long* sums = reinterpret_cast<long long*>(c.top);   // not in use yet
   long long mine[1] = {0}, tiles[1];
   for (int b = b0; b < b1; ++b) {
-    const Req r = load_req(p, b);
-    req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq);
+    const Req r = load_req<SHARED>(p, b);
+    req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq - r.k0);
     mine[0] += row_tiles(r.rows);
   }
   block_scan(sums, mine, tiles);
@@ -345,15 +354,15 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   const int n = static_cast<int>(tiles[0]);
   const int share = (n + kThreads - 1) / kThreads;
   const int x0 = min(tid * share, n), x1 = min(x0 + share, n);
-  int from = 0, to = p.requests;   // the last request that begins at or before x0
+  int from = 0, to = requests;   // the last request that begins at or before x0
   while (to - from > 1) {
     const int mid = (from + to) >> 1;
     if (first[mid] <= x0) from = mid; else to = mid;
   }
   long long part[3] = {0, 0, 0}, all[3];   // cost, units, ranges that this thread's tiles are worth
   for (int x = x0, b = from; x < x1; ++x) {
-    while (b + 1 < p.requests && first[b + 1] <= x) ++b;
-    const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
+    while (b + 1 < requests && first[b + 1] <= x) ++b;
+    const int len = tile_units<SHARED>(p, req[b].x, SHARED && b < p.groups ? req[b].y : req[b].y - req[b].x, req[b].y, x - first[b]);
     part[0] += static_cast<long long>(len + kItemCost) * p.kv_heads;
     part[1] += static_cast<long long>(len) * p.kv_heads;
     part[2] += static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads;
@@ -372,8 +381,8 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   __syncthreads();
   if (before < cost && u[1] >= before && u[0] < before + own_cost) {
     for (int x = x0, b = from; x < x1; ++x) {
-      while (b + 1 < p.requests && first[b + 1] <= x) ++b;
-      const int len = tile_units(p, req[b].x, req[b].y, x - first[b]);
+      while (b + 1 < requests && first[b + 1] <= x) ++b;
+      const int len = tile_units<SHARED>(p, req[b].x, SHARED && b < p.groups ? req[b].y : req[b].y - req[b].x, req[b].y, x - first[b]);
       const long long of_tile = static_cast<long long>(len + kItemCost) * p.kv_heads;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -392,7 +401,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
           c.first_tile = x - first[b];
           c.first_head = head;
           c.first_lo = lo;
-          c.first_req = load_req(p, b);
+          c.first_req = load_req<SHARED>(p, b);
         }
       }
       before += of_tile;
@@ -505,8 +514,9 @@ __device__ __forceinline__ void exp_of(const uint32_t* v, const float4& f, int l
 __device__ __forceinline__ constexpr uint32_t p_column(int i) { return static_cast<uint32_t>((i >> 1) * 32 + (i & 1) * 8); }
 
 // Whether a row's m is so large that x - m has to be taken exactly.  (m is the same in
-// both warps of the rows.)
-__device__ __forceinline__ bool is_far(float m) { return __any_sync(0xFFFFFFFFu, fabsf(m) > kFar && m != -INFINITY); }
+// both warps of the rows.)  Not for an infinite one: its row is NaN or sees nothing either
+// way, and the rows beside it keep their bits.
+__device__ __forceinline__ bool is_far(float m) { return __any_sync(0xFFFFFFFFu, fabsf(m) > kFar && fabsf(m) < INFINITY); }
 
 // 64 of a row's scores (the row's other 64 are another warp's): the running maximum
 // m (O and l rescaled when it moves), P in place of the scores, l.  `left`: the
@@ -603,11 +613,18 @@ __device__ __forceinline__ void store_row(__half* dst, const uint32_t (&a)[N], f
   }
 }
 
+// Columns of a row's sums.
+template <int N>
+__device__ __forceinline__ void store_sums(float* dst, const uint32_t (&a)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4) *reinterpret_cast<uint4*>(dst + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+}
+
 // The end of an item: its row sums taken out of tensor memory and finished, or left
 // for the range whose arrival completes the item.  Not inlined: its registers are
 // not the unit loop's.
-template <int D>
-__device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req req, int head, int base, int lo, bool whole,
+template <int D, bool SHARED>
+__device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req req, bool own, int head, int base, int lo, bool whole,
                                          bool busy, bool ok, uint32_t o_at, float m, float l) {
   const int r = threadIdx.x & (kTile - 1);
   const int sw = (threadIdx.x >> 5) - kSoftmaxWarp0;
@@ -623,9 +640,9 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   const bool mine = base + r < req.rows;
   const int rr = base + r;
   const int tok = rr / p.group;
-  const int lim = req.seq - req.n + tok + 1;
-  const bool sees = lim > 0;
+  const bool sees = req.late + tok + 1 > 0;
   const int h = head * p.group + (rr - tok * p.group);
+  const size_t part_at = SHARED ? (static_cast<size_t>(own ? p.tokens : 0) + req.t0 + tok) * p.q_heads + h : 0;
   __half* dst = p.out + static_cast<size_t>(req.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + half * (D / 2);
   constexpr size_t kTileFloats = static_cast<size_t>(kTile) * (D + 2);
   constexpr size_t kMAt = static_cast<size_t>(D) * kTile, kLAt = static_cast<size_t>(D + 1) * kTile;
@@ -644,7 +661,11 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
         for (int e = 0; e < 32; ++e) a[e] = 0u;
       }
       if (whole) {
-        if (mine) store_row(dst + 32 * ch, a, inv, sees);
+        if constexpr (SHARED) {
+          if (mine) store_sums(p.part + part_at * D + half * (D / 2) + 32 * ch, a);
+        } else {
+          if (mine) store_row(dst + 32 * ch, a, inv, sees);
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
@@ -656,6 +677,10 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   }
   float* lse = p.lse != nullptr && half == 0 ? p.lse + static_cast<size_t>(req.t0 + tok) * p.q_heads + h : nullptr;
   if (whole) {
+    if constexpr (SHARED) {
+      if (mine && half == 0) p.part_ml[part_at] = make_float2(m, l);
+      return;
+    }
     if (mine && lse != nullptr) *lse = sees ? kLn2 * (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
     return;
   }
@@ -665,7 +690,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   }
   // the range in which the item begins tells the join about it
   if (lo == 0 && x == 0 && half == 0 && r == 0)
-    p.split[blockIdx.x] = SplitItem{req.t0, req.n, req.seq, req.rows, base, head, ctl.last_range, 0};
+    p.split[blockIdx.x] = SplitItem{req.t0, req.n, req.seq, req.rows, base, head, ctl.last_range, own ? 1 : 0};
 }
 
 // Items that are spread over several ranges, after the other kernel: block (c, y) the
@@ -675,8 +700,9 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
 constexpr int kJoinRows = 16;
 constexpr int kJoinThreads = 128;
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  if constexpr (SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const SplitItem it = p.split[c];
@@ -715,6 +741,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int rr = it.base + row;
   const int tok = rr / p.group;
   const int h = it.head * p.group + (rr - tok * p.group);
+  if constexpr (SHARED) {
+    const size_t at = (static_cast<size_t>(it.own ? p.tokens : 0) + it.t0 + tok) * p.q_heads + h;
+#pragma unroll
+    for (int e = 0; e < kQuads; ++e) reinterpret_cast<float4*>(p.part + at * D)[quad0 + e] = acc[e];
+    if (quad0 == 0) p.part_ml[at] = make_float2(top, sum);
+    return;
+  }
   const bool sees = it.seq - it.n + tok + 1 > 0;
   const float inv = inverse_sum(sum, sees);
   __half* dst = p.out + static_cast<size_t>(it.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * quad0;
@@ -728,7 +761,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     p.lse[static_cast<size_t>(it.t0 + tok) * p.q_heads + h] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
 }
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap qmap) {
@@ -764,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) p.split[blockIdx.x].last = -1;   // no item begins here and ends later, so far
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int ctas, count;
-  if (!find_range(p, ctl, smem_raw, ctas, count)) {
+  if (!find_range<SHARED>(p, ctl, smem_raw, ctas, count)) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the few-rows kernel is
     return;
   }
@@ -776,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  Walker w(p, ctl, count);
+  Walker<SHARED> w(p, ctl, count);
 
   if (warp == kMmaWarp) {
     // ---- MMA issue: one lane runs the whole loop -----------------------------------------
@@ -870,10 +903,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto look_up = [&]() -> Look {
       Look k{-1, 0, 0};
       if (live) {
-        const int key = blk * kKeys + key16;
+        const int key = w.r.k0 + blk * kKeys + key16;
         k.head = w.head;
-        k.keys = w.r.seq - blk * kKeys;
-        if (key < w.r.seq) k.page = __ldg(p.table + static_cast<size_t>(w.b) * p.table_stride + (key >> p.page_shift));
+        k.keys = w.r.seq - w.r.k0 - blk * kKeys;
+        if (key < w.r.seq) k.page = __ldg(p.table + static_cast<size_t>(w.r.row) * p.table_stride + (key >> p.page_shift));
         if (++blk == w.hi) {
           w.next();
           live = w.more();
@@ -1031,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         n += static_cast<uint32_t>(steps);
         continue;
       }
-      const int lim = w.r.seq - w.r.n + (w.rt * kItemRows + x * kTile + r) / p.group + 1;   // keys that this row sees
+      const int lim = sees_before<SHARED>(w.r, (w.rt * kItemRows + x * kTile + r) / p.group);   // keys that this row sees
       const int lim_min = __shfl_sync(0xFFFFFFFFu, lim, 0);
       const bool busy = (warp & 3) * 32 < rows;             // the warp has rows at all
       float m = -INFINITY, l = 0.f;
@@ -1049,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (busy) {
           if (ok) tc_fence_after();
           const float4* sc = &ctl.scale[n % kScaleSlots][half * (kGroups / 2)];
-          const int key0 = (w.lo + j) * kKeys;
+          const int key0 = w.r.k0 + (w.lo + j) * kKeys;
           const int left = lim - key0 - half * kHalf;     // of this half of the unit
           // from its first masked unit on an item is masked
           exact = exact || key0 + kKeys > lim_min;
@@ -1073,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       if (ok) tc_fence_after();
       const int base = w.rt * kItemRows + x * kTile;
-      finish_item<D>(p, ctl, w.r, w.head, base, w.lo, w.lo == 0 && w.hi == w.units, busy, ok, o_at, m, l);
+      finish_item<D, SHARED>(p, ctl, w.r, SHARED && w.b >= p.groups, w.head, base, w.lo, w.lo == 0 && w.hi == w.units, busy, ok, o_at, m, l);
       __syncwarp();
     }
   }
@@ -1088,14 +1121,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the few-rows kernel is
 }
 
-template <int D>
+template <int D, bool SHARED>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                    bool after_step, cudaStream_t stream) {
   constexpr int kSmem = Cfg<D>::kTiles + static_cast<int>(sizeof(Control));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
   static std::atomic<unsigned long long> allowed{0};
-  if (!allow_smem(prompt_kernel<D>, kSmem, allowed)) return EXL3_ERR_CUDA;
+  if (!allow_smem(prompt_kernel<D, SHARED>, kSmem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count();
   if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
   // After the few-rows kernel a CTA begins as soon as an SM is free: the two write
@@ -1111,7 +1144,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   own.stream = stream;
   own.attrs = attr;
   own.numAttrs = after_step ? 1 : 0;
-  if (cudaLaunchKernelEx(&own, prompt_kernel<D>, p, kmap, vmap, qmap) != cudaSuccess) return EXL3_ERR_CUDA;
+  if (cudaLaunchKernelEx(&own, prompt_kernel<D, SHARED>, p, kmap, vmap, qmap) != cudaSuccess) return EXL3_ERR_CUDA;
   exl3_status st = launch_status();
   if (st != EXL3_OK) return st;
   // a table whose rows hold no item that is ever split leaves nothing to join
@@ -1122,7 +1155,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return EXL3_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<D, SHARED>, p) != cudaSuccess) return EXL3_ERR_CUDA;
   return launch_status();
 }
 
@@ -1140,7 +1173,9 @@ exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, bool afte
   q.q_box = kTile % p.group == 0 && !q.negate ? 1 : 0;
   CUtensorMap qm = km;
   if (q.q_box != 0 && (st = query_map(&qm, p, c.head_dim, kTile / p.group)) != EXL3_OK) return st;
-  return c.head_dim == 64 ? launch<64>(q, km, vm, qm, after_step, stream) : launch<128>(q, km, vm, qm, after_step, stream);
+  if (p.group_start != nullptr)
+    return c.head_dim == 64 ? launch<64, true>(q, km, vm, qm, after_step, stream) : launch<128, true>(q, km, vm, qm, after_step, stream);
+  return c.head_dim == 64 ? launch<64, false>(q, km, vm, qm, after_step, stream) : launch<128, false>(q, km, vm, qm, after_step, stream);
 }
 
 }  // namespace attn

@@ -43,7 +43,7 @@ namespace {
 // elements are too little for what a unit costs besides: 68 us for 64 requests of
 // 4096 keys and 8 heads, where 64 keys take 57).
 template <int D>
-constexpr int unit_keys() { return 4096 / D; }
+constexpr int unit_keys() { return step_unit(D); }
 constexpr int kQSlots = 2;
 constexpr int kJoinOnce = 24;   // partial results that are joined in one step
 constexpr int kJoinBarrier = 1;
@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 template <int NT>
 __device__ __forceinline__ int req_tiles(const Req& r) { return (r.rows + 8 * NT - 1) / (8 * NT); }
 template <int D>
-__device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq + unit_keys<D>() - 1) / unit_keys<D>()); }
+__device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq - r.k0 + unit_keys<D>() - 1) / unit_keys<D>()); }
 
 // Ranges are cut in equal parts of units plus kItemCost for each item (its Q, the
 // join of the warps).  An item of at most kWhole units is not split: a boundary that
@@ -132,7 +132,7 @@ __device__ __forceinline__ Edge edge_at(const Req& r, int b, long long u, long l
 
 // The items of a range, one after the other.  Each lane of a warp holds one
 // request; every warp walks by itself.
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 struct Walker {
   const AttnParams& p;
   int base, b;        // request of lane 0, current request
@@ -156,6 +156,15 @@ struct Walker {
     r.n = __shfl_sync(0xFFFFFFFFu, mine.n, src);
     r.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, src);
     r.seq = __shfl_sync(0xFFFFFFFFu, mine.seq, src);
+    if constexpr (SHARED) {
+      r.late = __shfl_sync(0xFFFFFFFFu, mine.late, src);
+      r.k0 = __shfl_sync(0xFFFFFFFFu, mine.k0, src);
+      r.row = __shfl_sync(0xFFFFFFFFu, mine.row, src);
+    } else {
+      r.late = r.seq - r.n;
+      r.k0 = 0;
+      r.row = b;
+    }
     blocks = req_blocks<D>(r);
     tiles = req_tiles<NT>(r);
   }
@@ -171,10 +180,10 @@ struct Walker {
       do {
         if (++b - base == 32) {
           base = b;
-          mine = load_req(p, base + (threadIdx.x & 31));
+          mine = load_req<SHARED>(p, base + (threadIdx.x & 31));
         }
         fetch();
-      } while (r.rows == 0 && b < p.requests);
+      } while (r.rows == 0 && b < req_count<SHARED>(p));
     }
   }
   __device__ __forceinline__ bool more() const { return hi > lo; }
@@ -223,13 +232,20 @@ __device__ __forceinline__ float4 join_warps(const Shared<D, NT>& sh, int row, i
   return acc;
 }
 
-// 4 columns of row `rr` of a request's item, finished.
-template <int D>
-__device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, int head, int rr, int q4, const float4& acc, float top,
-                                          float sum) {
+// 4 columns of row `rr` of a request's item, finished; with prefixes, its sums over the
+// prefix or (`own`) its own keys.
+template <int D, bool SHARED>
+__device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, bool own, int head, int rr, int q4, const float4& acc,
+                                          float top, float sum) {
   const int tok = rr / p.group;
   const int h = head * p.group + (rr - tok * p.group);
-  const bool sees = r.seq - r.n + tok + 1 > 0;
+  if constexpr (SHARED) {
+    const size_t at = (static_cast<size_t>(own ? p.tokens : 0) + r.t0 + tok) * p.q_heads + h;
+    *reinterpret_cast<float4*>(p.part + at * D + 4 * q4) = acc;
+    if (q4 == 0) p.part_ml[at] = make_float2(top, sum);
+    return;
+  }
+  const bool sees = r.late + tok + 1 > 0;
   const float inv = inverse_sum(sum, sees);
   const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
   const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
@@ -249,7 +265,7 @@ __device__ __forceinline__ void leave(float* slot, int row, int q4, const float4
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     step_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
@@ -285,8 +301,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
   Edge from, to;
   int ctas, first = 0;
   Req lanes;
-  if (p.requests <= 32) {
-    const Req r = load_req(p, lane);
+  const int count = req_count<SHARED>(p);
+  if (count <= 32) {
+    const Req r = load_req<SHARED>(p, lane);
     lanes = r;
     long long cost = 0, ranges = 0;
     req_cost<D, NT>(p, r, cost, ranges);
@@ -305,21 +322,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     for (int e = 0; e < 2; ++e) {
       const long long u = range_begin(total, cta + e, ctas);
       const int b = __popc(__ballot_sync(0xFFFFFFFFu, inc <= u));   // the request that holds u
-      Req q;
-      q.t0 = 0;
-      q.n = 0;
-      q.rows = 1;
-      q.seq = __shfl_sync(0xFFFFFFFFu, r.seq, b & 31);
+      Req q{0, 0, 1, 0, 0, 0, 0};
+      q.seq = __shfl_sync(0xFFFFFFFFu, r.seq - r.k0, b & 31);
       const long long before = __shfl_sync(0xFFFFFFFFu, inc - cost, b & 31);
-      Edge x{p.requests, 0, 0, 0, 0};
+      Edge x{count, 0, 0, 0, 0};
       if (b < 32) x = edge_at<D>(q, b, u, before, total, ctas);
       if (e == 0) from = x; else to = x;
     }
   } else {
-    const int per = (p.requests + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, p.requests), b1 = min(b0 + per, p.requests);
+    const int per = (count + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, count), b1 = min(b0 + per, count);
     long long mine = 0, ranges = 0;
-    for (int b = b0; b < b1; ++b) req_cost<D, NT>(p, load_req(p, b), mine, ranges);
+    for (int b = b0; b < b1; ++b) req_cost<D, NT>(p, load_req<SHARED>(p, b), mine, ranges);
     long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -331,7 +345,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       sh.warp_sum[warp] = inc;
       sh.warp_ranges[warp] = ranges;
     }
-    if (tid == 0) sh.edge[1] = Edge{p.requests, 0, 0, 0, 0};   // the last range's end is in no item
+    if (tid == 0) sh.edge[1] = Edge{count, 0, 0, 0, 0};   // the last range's end is in no item
     __syncthreads();
     long long total = 0, before = inc - mine, all_ranges = 0;
 #pragma unroll
@@ -345,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const long long u[2] = {range_begin(total, cta, ctas), range_begin(total, cta + 1, ctas)};
     if (u[1] >= before && u[0] < before + mine) {
       for (int b = b0; b < b1; ++b) {
-        const Req r = load_req(p, b);
+        const Req r = load_req<SHARED>(p, b);
         long long n = 0, unused = 0;
         req_cost<D, NT>(p, r, n, unused);
 #pragma unroll
@@ -358,9 +372,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     from = sh.edge[0];
     to = sh.edge[1];
     first = from.b;
-    lanes = load_req(p, first + lane);
+    lanes = load_req<SHARED>(p, first + lane);
   }
-  Walker<D, NT> w(p, from, to, first, lanes);
+  Walker<D, NT, SHARED> w(p, from, to, first, lanes);
 
   if (warp == kConsumers) {
     // ---- producer ------------------------------------------------------------------
@@ -387,9 +401,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
                  p.q + static_cast<size_t>(w.r.t0 + tok) * p.q_stride + static_cast<size_t>(w.head * p.group + (ra - tok * p.group)) * D,
                  static_cast<uint32_t>(rb - ra) * D * 2, &sh.q_full[qs]);
       // units, 32 at a time: lane l looks up unit g0 + l
-      const int32_t* row = p.table + static_cast<size_t>(w.b) * p.table_stride;
+      const int32_t* row = p.table + static_cast<size_t>(w.r.row) * p.table_stride;
       for (int g0 = w.lo; g0 < w.hi && ok; g0 += 32) {
-        const int mykey = (g0 + lane) * kUnit;
+        const int mykey = w.r.k0 + (g0 + lane) * kUnit;
         int block[kGroups];                            // of the tensor map, per 16 keys
         float ks[kGroups], vs[kGroups];
         PageScale scale[kGroups];
@@ -471,13 +485,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_empty[qs]);
     // keys that this lane's rows (8 nt + 2t, + 1) see; the least of the tile
-    const int seen0 = w.r.seq - w.r.n;
     int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) lim[nt][e] = seen0 + (row0 + nt * 8 + 2 * t + e) / p.group + 1;
-    const int lim_min = seen0 + row0 / p.group + 1;
+      for (int e = 0; e < 2; ++e) lim[nt][e] = sees_before<SHARED>(w.r, (row0 + nt * 8 + 2 * t + e) / p.group);
+    const int lim_min = sees_before<SHARED>(w.r, row0 / p.group);
 
     float o[NT][KS][4];
     float m[NT][2], l[NT][2];
@@ -537,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       float4 sc[kGroups];
 #pragma unroll
       for (int hf = 0; hf < kGroups; ++hf) sc[hf] = sh.scale[st][hf];
-      const int key0 = blk * kUnit;
+      const int key0 = w.r.k0 + blk * kUnit;
       const bool mask = key0 + kUnit > lim_min;
       bool over = false;
 #pragma unroll
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
         float top, sum;
         const float4 acc = join_warps(sh, row, q4, top, sum);
         if (whole) {
-          store_out<D>(p, w.r, w.head, row0 + 8 * nt + row, q4, acc, top, sum);
+          store_out<D, SHARED>(p, w.r, SHARED && w.b >= p.groups, w.head, row0 + 8 * nt + row, q4, acc, top, sum);
         } else {
           leave<D, kRows>(slot, 8 * nt + row, q4, acc, top, sum);
         }
@@ -761,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
           const int row = x / kQuads, col = x % kQuads;
           const float4 v = join_warps(sh, row, col, mx, total);
           if (rest)
-            store_out<D>(p, w.r, w.head, row0 + r0 + row, col, v, mx, total);
+            store_out<D, SHARED>(p, w.r, SHARED && w.b >= p.groups, w.head, row0 + r0 + row, col, v, mx, total);
           else
             leave<D, kRows>(p.partial + static_cast<size_t>(2 * k0 + (k0 == c0 ? 1 : 0)) * kSlot, r0 + row, col, v, mx, total);
         }
@@ -780,16 +793,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   const size_t smem = sizeof(Shared<D, NT>);
   static std::atomic<unsigned long long> allowed{0};
-  if (!allow_smem(step_kernel<D, NT>, smem, allowed)) return EXL3_ERR_CUDA;
+  if (!allow_smem(step_kernel<D, NT, SHARED>, smem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count() * C::kCtasPerSm;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  step_kernel<D, NT><<<ctas, C::kThreads, smem, stream>>>(p, kmap, vmap);
+  step_kernel<D, NT, SHARED><<<ctas, C::kThreads, smem, stream>>>(p, kmap, vmap);
   return launch_status();
+}
+
+template <bool SHARED>
+exl3_status launch_any(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int head_dim, bool wide, cudaStream_t stream) {
+  if (head_dim == 64) return wide ? launch<64, 2, SHARED>(p, kmap, vmap, stream) : launch<64, 1, SHARED>(p, kmap, vmap, stream);
+  return wide ? launch<128, 2, SHARED>(p, kmap, vmap, stream) : launch<128, 1, SHARED>(p, kmap, vmap, stream);
 }
 
 }  // namespace
@@ -800,8 +819,7 @@ exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, 
   const int unit = c.head_dim == 64 ? unit_keys<64>() : unit_keys<128>();
   const int rows = c.page_size < unit ? c.page_size : unit;
   if ((st = cache_map(&km, c.k, c, rows)) != EXL3_OK || (st = cache_map(&vm, c.v, c, rows)) != EXL3_OK) return st;
-  if (c.head_dim == 64) return wide ? launch<64, 2>(p, km, vm, stream) : launch<64, 1>(p, km, vm, stream);
-  return wide ? launch<128, 2>(p, km, vm, stream) : launch<128, 1>(p, km, vm, stream);
+  return p.group_start != nullptr ? launch_any<true>(p, km, vm, c.head_dim, wide, stream) : launch_any<false>(p, km, vm, c.head_dim, wide, stream);
 }
 
 }  // namespace attn
