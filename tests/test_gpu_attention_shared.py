@@ -50,15 +50,24 @@ def make(rng, heads, kv_heads, dim, page, groups, extra=0, sharp=1.0):
     return x, np.array(start, np.int32), np.array(prefix, np.int32)
 
 
-def run(x, start, prefix, max_new=None, max_group=None, workspace=None, out=None):
+def widened(x):
+    """The table with columns that no request reaches: what it could hold is worth sharing, so that the kernels for that run."""
+    n, width = x["block_table"].shape
+    page_bytes = 2 * x["k"][0].size
+    wide = np.full((n, max(width, -(-70_000_000 // (n * page_bytes)))), 2 ** 30, np.int32)
+    wide[:, :width] = x["block_table"]
+    return wide
+
+
+def run(x, start, prefix, max_new=None, max_group=None, workspace=None, out=None, wide=True):
     cache = B.Exl3KvCache.from_tensors(cuda(x["k"]), cuda(x["v"]), cuda(x["k_scale"]), cuda(x["v_scale"]))
     if max_new is None:
         max_new = max(int(np.diff(x["q_start"]).max()), 1)
     if max_group is None:
         max_group = max([int(x["q_start"][e] - x["q_start"][a]) for a, e in zip(start[:-1], start[1:])] + [1])
     q = x["q"] if isinstance(x["q"], torch.Tensor) else cuda(x["q"])
-    return B.exl3_attention_shared(cache, q, cuda(x["q_start"]), cuda(x["seq_len"]), cuda(x["block_table"]), cuda(start), cuda(prefix),
-                                   max_new=max_new, max_group=max_group, scale=x["scale"], out=out, lse=True, workspace=workspace)
+    return B.exl3_attention_shared(cache, q, cuda(x["q_start"]), cuda(x["seq_len"]), cuda(widened(x) if wide else x["block_table"]),
+                                   cuda(start), cuda(prefix), max_new=max_new, max_group=max_group, scale=x["scale"], out=out, lse=True, workspace=workspace)
 
 
 HEADS = [(8, 8, 64), (4, 1, 128), (14, 2, 64), (16, 2, 128), (5, 1, 64)]
@@ -182,6 +191,15 @@ def test_strides_rows_of_nobody_and_requests_outside_all_groups(requests):
     assert (room[:, 0] == 7).all() and (room[:, 7:] == 7).all() and (room[n:] == 7).all()
 
 
+@pytest.mark.parametrize("requests,new", [(7, 1), (3, 40)])
+def test_little_to_read(requests, new):
+    """Tables that hold too little for a look at what is shared: the bits of the call without prefixes."""
+    x, start, prefix = make(np.random.default_rng(new), 8, 2, 64, 32, [(200, [(50 + new, new)] * requests)])
+    got = run(x, start, prefix, wide=False)
+    check(x, got)
+    assert all(torch.equal(a, b) for a, b in zip(got, A.run(x)))
+
+
 def test_no_groups_at_all():
     x, _, _ = make(np.random.default_rng(3), 4, 2, 64, 16, [(0, [(90, 1), (33, 2), (None, 1)])])
     check(x, run(x, np.zeros(1, np.int32), np.zeros(0, np.int32)))
@@ -192,7 +210,7 @@ def test_in_a_graph_with_lengths_that_change():
     x, start, prefix = make(np.random.default_rng(21), 8, 2, 64, 32, [(333, [(70, 1), (40, 1), (9, 1)]), (64, [(200, 1)] * 20)])
     y = dict(x, seq_len=np.where(np.arange(23) % 3 == 1, 0, x["seq_len"] - 5).astype(np.int32), q=np.roll(x["q"], 1, 0))
     cache = B.Exl3KvCache.from_tensors(cuda(x["k"]), cuda(x["v"]), cuda(x["k_scale"]), cuda(x["v_scale"]))
-    q, starts, seq, table, gs, pl = (cuda(a) for a in (x["q"], x["q_start"], x["seq_len"], x["block_table"], start, prefix))
+    q, starts, seq, table, gs, pl = (cuda(a) for a in (x["q"], x["q_start"], x["seq_len"], widened(x), start, prefix))
     out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
     ws = B.alloc_attention_shared_workspace(8, 2, 64, 1, 20, 23, "cuda")
 
@@ -221,7 +239,7 @@ def test_default_sizes_and_refusals():
     cache = B.Exl3KvCache.from_tensors(cuda(x["k"]), cuda(x["v"]), cuda(x["k_scale"]), cuda(x["v_scale"]))
     args = [cuda(x[n]) for n in ("q", "q_start", "seq_len", "block_table")]
     out = B.exl3_attention_shared(cache, *args, cuda(start), cuda(prefix))
-    assert torch.equal(out, run(x, start, prefix, max_new=3, max_group=3)[0])
+    assert torch.equal(out, run(x, start, prefix, max_new=3, max_group=3, wide=False)[0])
     small = B.alloc_attention_shared_workspace(4, 2, 64, 3, 3, 2, "cuda")
     with pytest.raises(B.Exl3Error):
         B.exl3_attention_shared(cache, *args, cuda(start), cuda(prefix), max_new=3, max_group=3, workspace=small)

@@ -971,41 +971,57 @@ MAX_NORM = 32768
 MAX_NORM_OUTS = 4
 
 
-def _matrix(t, name, n, dev, rows=None):
+def _matrix(t, name, shape, dev):
     """Pointer and row stride of halves [rows, n] whose rows may be apart."""
+    if t.__class__ is torch.Tensor and t.dtype is torch.float16 and t.shape == shape and t.is_contiguous() and t.device == dev:
+        return t.data_ptr(), shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2 or t.shape[1] != n or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, {n}]")
-    if t.device.type != "cuda" or t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {'a GPU' if dev.type != 'cuda' else dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype != torch.float16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float16")
     stride = t.stride()
-    if stride[1] != 1 and n > 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), stride[0] if t.shape[0] > 1 else n
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
 def _norm_inputs(x, weight, residual):
-    if x.dim() not in (1, 2):
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows, n] or [n]")
-    x2 = x if x.dim() == 2 else x.view(1, -1)
-    rows, n = x2.shape
-    dev = x.device
-    xp, xs = _matrix(x2, "x", n, dev)
-    rp, rs = (None, n) if residual is None else _matrix(residual.view(x2.shape) if x.dim() == 1 else residual, "residual", n, dev, rows)
-    if weight.numel() != n:
-        raise ValueError(f"weight holds {weight.numel()} elements, expected {n}")
-    return rows, n, dev, xp, xs, rp, rs, _ptr(weight, "weight", _HALF, dev)
+    """Shape and device of x [rows, n], pointers and strides of x, residual and weight."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    shape, dev = x.shape, x.device
+    xp, xs = _matrix(x, "x", shape, dev)
+    rp, rs = (None, shape[1]) if residual is None else _matrix(residual, "residual", shape, dev)
+    if weight.numel() != shape[1]:
+        raise ValueError(f"weight holds {weight.numel()} elements, expected {shape[1]}")
+    return shape, dev, xp, xs, rp, rs, _ptr(weight, "weight", _HALF, dev)
 
 
-def _norm_out(t, name, shape, dtype, dev):
+def _norm_out(t, name, shape, dtypes, dev):
+    """An output and its pointer: a new tensor unless it is given."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(shape, dtype=dtypes[0], device=dev)
+        return t, t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
+    return t, _ptr(t, name, dtypes, dev)
+
+
+def _norm_sum(x, residual, h, shape, dev):
+    """h, the sum that goes on, and its pointer."""
+    if residual is not None:
+        return _norm_out(h, "h", shape, _HALF, dev)
+    if h is not None:
+        raise ValueError("h is an output of the addition: there is no residual")
+    return x, None
+
+
+def _as_rows(t):
+    return t if t is None else t.view(1, -1)
 
 
 def exl3_rms_norm(x, weight, eps, residual=None, out=None, h=None):
@@ -1013,16 +1029,17 @@ def exl3_rms_norm(x, weight, eps, residual=None, out=None, h=None):
     may be apart): returns (y, h), h = x + residual rounded to binary16, y its norm
     (taken before that rounding) times weight [n].  Without a residual h is x.  out and h
     may be x or residual themselves."""
-    rows, n, dev, xp, xs, rp, rs, wp = _norm_inputs(x, weight, residual)
-    out = _norm_out(out, "out", x.shape, torch.float16, dev)
-    if residual is None:
-        if h is not None:
-            raise ValueError("h is an output of the addition: there is no residual")
-        h = x
-    else:
-        h = _norm_out(h, "h", x.shape, torch.float16, dev)
-    _check(load_library().exl3_rms_norm(xp, xs, rp, rs, wp, eps, rows, n, _ptr(out, "out", _HALF, dev),
-                                        None if residual is None else _ptr(h, "h", _HALF, dev), _stream(dev)))
+    if x.dim() != 2:
+        if x.dim() != 1:
+            raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows, n] or [n]")
+        y, s = exl3_rms_norm(_as_rows(x), weight, eps, _as_rows(residual), _as_rows(out), _as_rows(h))
+        return (y.view(-1) if out is None else out), x if residual is None else s.view(-1) if h is None else h
+    shape, dev, xp, xs, rp, rs, wp = _norm_inputs(x, weight, residual)
+    out, op = _norm_out(out, "out", shape, _HALF, dev)
+    h, hp = _norm_sum(x, residual, h, shape, dev)
+    status = load_library().exl3_rms_norm(xp, xs, rp, rs, wp, eps, shape[0], shape[1], op, hp, _stream(dev))
+    if status:
+        _check(status)
     return out, h
 
 
@@ -1031,24 +1048,28 @@ def exl3_rms_norm_i8(x, weight, eps, signs, residual=None, q=None, qscale=None, 
     `signs` (1 to 4 tensors s_in [n], or None for a projection without input rotation) the
     rotation and the int8 quantization with a scale for each 128 values.  Returns (q int8
     [outs, rows, n], qscale float32 [outs, rows, n / 128], h); x [n]: without the rows."""
-    rows, n, dev, xp, xs, rp, rs, wp = _norm_inputs(x, weight, residual)
+    if x.dim() != 2:
+        if x.dim() != 1:
+            raise ValueError(f"x has shape {tuple(x.shape)}, expected [rows, n] or [n]")
+        a, b, s = exl3_rms_norm_i8(_as_rows(x), weight, eps, signs, _as_rows(residual), None if q is None else q.unsqueeze(1),
+                                   None if qscale is None else qscale.unsqueeze(1), _as_rows(h))
+        return (a.squeeze(1) if q is None else q, b.squeeze(1) if qscale is None else qscale,
+                x if residual is None else s.view(-1) if h is None else h)
+    shape, dev, xp, xs, rp, rs, wp = _norm_inputs(x, weight, residual)
+    rows, n = shape
     outs = len(signs)
-    ptrs = (_P * max(outs, 1))(*[_ptr(s, f"signs[{i}]", _HALF, dev) for i, s in enumerate(signs)])
+    ptrs = (_P * max(outs, 1))()
     for i, s in enumerate(signs):
-        if s is not None and s.numel() != n:
-            raise ValueError(f"signs[{i}] holds {s.numel()} elements, expected {n}")
-    lead = (outs,) + tuple(x.shape[:-1])
-    q = _norm_out(q, "q", lead + (n,), torch.int8, dev)
-    qscale = _norm_out(qscale, "qscale", lead + (n // 128,), torch.float32, dev)
-    if residual is None:
-        if h is not None:
-            raise ValueError("h is an output of the addition: there is no residual")
-        h = x
-    else:
-        h = _norm_out(h, "h", x.shape, torch.float16, dev)
-    _check(load_library().exl3_rms_norm_i8(xp, xs, rp, rs, wp, eps, rows, n, ptrs, outs, _ptr(q, "q", _I8, dev),
-                                           _ptr(qscale, "qscale", _F32, dev),
-                                           None if residual is None else _ptr(h, "h", _HALF, dev), _stream(dev)))
+        if s is not None:
+            ptrs[i] = _ptr(s, "signs", _HALF, dev)
+            if s.numel() != n:
+                raise ValueError(f"signs[{i}] holds {s.numel()} elements, expected {n}")
+    q, qp = _norm_out(q, "q", (outs, rows, n), _I8, dev)
+    qscale, sp = _norm_out(qscale, "qscale", (outs, rows, n // 128), _F32, dev)
+    h, hp = _norm_sum(x, residual, h, shape, dev)
+    status = load_library().exl3_rms_norm_i8(xp, xs, rp, rs, wp, eps, rows, n, ptrs, outs, qp, sp, hp, _stream(dev))
+    if status:
+        _check(status)
     return q, qscale, h
 
 
@@ -1108,35 +1129,40 @@ def exl3_rotary(q, k, position, freqs, interleaved=False, q_out=None, k_out=None
     given; they may be q and k.  Tokens of negative position are copied as they are."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [tokens, q_heads, head_dim]")
-    tokens, heads, dim = q.shape
-    dev = q.device
-    if dev.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
+    shape, dev = q.shape, q.device
+    tokens, heads, dim = shape
     qp, qs = _rows(q, "q", dim, dev)
-    kp, ks, kv_heads = None, 0, 0
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=torch.float16, device=dev)
+        qo, qos = q_out.data_ptr(), heads * dim
+    elif q_out.shape != shape:
+        raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(shape)}")
+    else:
+        qo, qos = _rows(q_out, "q_out", dim, dev)
+    kp = ko = None
+    ks = kos = kv_heads = 0
     if k is not None:
         kp, ks = _rows(k, "k", dim, dev)
-        kv_heads = k.shape[1]
-        if k.shape[0] != tokens:
-            raise ValueError(f"k has {k.shape[0]} tokens, q {tokens}")
+        shape = k.shape
+        kv_heads = shape[1]
+        if shape[0] != tokens:
+            raise ValueError(f"k has {shape[0]} tokens, q {tokens}")
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.float16, device=dev)
+            ko, kos = k_out.data_ptr(), kv_heads * dim
+        elif k_out.shape != shape:
+            raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {tuple(shape)}")
+        else:
+            ko, kos = _rows(k_out, "k_out", dim, dev)
     if position.numel() != tokens:
         raise ValueError(f"position holds {position.numel()} elements for {tokens} tokens")
-
-    def room(name, t, like):
-        if t is None:
-            t = torch.empty(like.shape, dtype=torch.float16, device=dev)
-            return t, t.data_ptr(), like.shape[1] * dim
-        if t.shape != like.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
-        return (t,) + _rows(t, name, dim, dev)
-
-    q_out, qo, qos = room("q_out", q_out, q)
-    ko, kos = None, 0
-    if k is not None:
-        k_out, ko, kos = room("k_out", k_out, k)
-    _check(load_library().exl3_rotary(
+    status = load_library().exl3_rotary(
         qp, qs, qo, qos, heads, kp, ks, ko, kos, kv_heads, dim, freqs.rotary_dim, 1 if interleaved else 0,
-        _ptr(position, "position", _I32, dev), _ptr(freqs.freqs, "freqs", _I64, dev), freqs.factor, tokens, _stream(dev)))
+        _ptr(position, "position", _I32, dev), _ptr(freqs.freqs, "freqs", _I64, dev), freqs.factor, tokens, _stream(dev))
+    if status:
+        _check(status)
     return q_out, k_out
 
 
@@ -1150,9 +1176,11 @@ class Exl3KvFork:
     copy_tokens [rows], free_state [3], all int32."""
 
     def __init__(self, rows, width, dev):
-        room = torch.empty(4 * rows + 3, dtype=torch.int32, device=dev)
-        self.ctx_len, self.copy_from, self.copy_to, self.copy_tokens, self.free_state = room.split([rows, rows, rows, rows, 3])
-        self.block_table = torch.empty((rows, width), dtype=torch.int32, device=dev)
+        def room(shape):
+            return torch.empty(shape, dtype=torch.int32, device=dev)   # a view of one tensor takes as long as a tensor
+        self.ctx_len, self.copy_from, self.copy_to, self.copy_tokens = room(rows), room(rows), room(rows), room(rows)
+        self.free_state = room(3)
+        self.block_table = room((rows, width))
 
 
 def exl3_kv_fork_workspace_bytes(pages: int) -> int:

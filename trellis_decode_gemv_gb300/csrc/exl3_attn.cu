@@ -111,85 +111,189 @@ exl3_status prepare(AttnParams& p, const exl3_kv_cache* cache, const exl3_half* 
   return EXL3_OK;
 }
 
+// Bytes of keys and values below which a call does not look for shared ones.
+constexpr double kWorthSharing = 64e6;
+
 bool few_rows(int tokens, int group) { return static_cast<long long>(tokens) * group <= kStepRows; }
 
-// Where the sums of a call with prefixes lie in its workspace, and its bytes.
+// Where what a call with prefixes needs besides lies in its workspace, and its bytes.
 struct SharedLayout {
-  size_t part, ml, end;
+  size_t split, flag, where, part, ml, end;
 };
 SharedLayout shared_layout(int q_heads, int kv_heads, int head_dim, int max_new, int max_group, int tokens) {
   const int group = q_heads / kv_heads;
   const size_t step = 2 * kMaxCtas * step_slot_floats(head_dim), prompt = 2 * kMaxPromptCtas * prompt_slot_floats(head_dim);
   const bool few = few_rows(max_new, group) && few_rows(max_group, group);
-  const size_t rows = 2 * static_cast<size_t>(tokens) * q_heads;
+  const size_t rows = static_cast<size_t>(tokens) * q_heads;
   SharedLayout x;
-  x.part = align256(head_bytes() + (few ? step : step + prompt) * sizeof(float));
-  x.ml = x.part + rows * head_dim * sizeof(float);
-  x.end = x.ml + rows * sizeof(float2);
+  x.split = align256(head_bytes() + (few ? step : step + prompt) * sizeof(float));
+  x.flag = align256(x.split + (kMaxCtas + kMaxPromptCtas) * sizeof(SharedSplit));
+  x.where = align256(x.flag + rows * sizeof(uint32_t));
+  x.part = align256(x.where + rows * sizeof(uint32_t));
+  x.ml = x.part + 2 * rows * head_dim * sizeof(float);
+  x.end = x.ml + 2 * rows * sizeof(float2);
   return x;
 }
 
-// A row's result from its sums over the prefix and over its own keys, 8 columns a
-// thread.  Rows of no request are left alone.
-constexpr int kMergeThreads = 128;
+// A row's result from its sums over the prefix and over its own keys, either of which may lie
+// in parts, one for each range that the item was spread over.  A block takes 16 rows (of
+// the tokens' heads of one key/value head), a thread four columns of one: 16
+// neighbouring rows of a part of the many-rows kernel are 256 contiguous bytes.  The
+// parts come in the order of the keys, their factors, 32 parts at a time, while the first
+// sums are on their way.  All that a row needs the other kernels have left beside its sums: finding
+// its request anew took each block 1.5 us.  Rows of no request are left alone.
+constexpr int kMergeRows = 16;
+constexpr int kMergeParts = 32;
+constexpr int kAhead = 8;   // parts of which a thread's columns are on their way
+
+// A row's sums over its prefix or its own keys: of part i the columns lie at x + slot *
+// max(2 i - 1, 0), four of them every `step` floats, the row's m and l in the same way.
+struct Parts {
+  const float *x, *m;
+  int count, slot, step, to_l;
+};
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ AttnParams p) {
-  const int t = blockIdx.x;
-  int b = -1, hi = p.requests + 1;   // the last request that begins at t or before
-  while (hi - b > 1) {
-    const int mid = (b + hi) >> 1;
-    if (p.q_start[mid] <= t) b = mid; else hi = mid;
-  }
-  const bool live = b >= 0 && b < p.requests;
-  Req r{0, 0, 0, 0, 0, 0, 0};
-  if (live) r = load_req<true>(p, p.groups + b);
-  const int h = static_cast<int>(blockIdx.y) * (8 * kMergeThreads / D) + static_cast<int>(threadIdx.x) / (D / 8);
-  const int c = static_cast<int>(threadIdx.x) % (D / 8);
+__global__ void __launch_bounds__(kMergeRows* D / 4, 1024 / (kMergeRows * D / 4)) merge_kernel(const __grid_constant__ AttnParams p) {
+  __shared__ Parts parts_of[2][kMergeRows];
+  __shared__ bool live_of[kMergeRows], sees_of[kMergeRows];
+  __shared__ float factor[kMergeRows][kMergeParts + 1], keep[kMergeRows];
+  __shared__ float top_of[kMergeRows], sum_of[kMergeRows];
+  const int tid = threadIdx.x;
+  const int row = tid % kMergeRows, quad = tid / kMergeRows;
+  const long long at_row = static_cast<long long>(blockIdx.x) * kMergeRows + row;   // token * group + head of the group
+  const long long t = at_row / p.group;
+  const size_t at = static_cast<size_t>(t) * p.q_heads + static_cast<size_t>(blockIdx.y) * p.group + (at_row - t * p.group);
+  // the requests' tokens: all between the first one's and the last one's
+  const Lists lists(p);
+  const int begin = first_token(p, lists, 0), end = first_token(p, lists, p.requests);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live || h >= p.q_heads || t < r.t0 || t - r.t0 >= r.n) return;
-  const bool sees = r.late + (t - r.t0) + 1 > 0;
-  const size_t at = static_cast<size_t>(t) * p.q_heads + h;
-  const size_t own = static_cast<size_t>(p.tokens) * p.q_heads + at;
-  const float2 mo = __ldcg(p.part_ml + own);
-  const float2 mp = r.k0 > 0 ? __ldcg(p.part_ml + at) : make_float2(-INFINITY, 0.f);
-  const float4* po = reinterpret_cast<const float4*>(p.part + own * D) + 2 * c;
-  const float4* pp = reinterpret_cast<const float4*>(p.part + at * D) + 2 * c;
-  float4 x[2], y[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    x[e] = __ldcg(po + e);
-    y[e] = r.k0 > 0 ? __ldcg(pp + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  const float top = fmaxf(mo.x, mp.x);
-  const float base = top == -INFINITY ? 0.f : top;
-  const float fo = ex2(mo.x - base), fp = ex2(mp.x - base);
-  const float sum = mo.y * fo + mp.y * fp;
-  const float inv = inverse_sum(sum, sees);
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float v[4] = {x[e].x * fo + y[e].x * fp, x[e].y * fo + y[e].y * fp, x[e].z * fo + y[e].z * fp, x[e].w * fo + y[e].w * fp};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const __half2 q = __floats2half2_rn(sees ? v[2 * i] * inv : 0.f, sees ? v[2 * i + 1] * inv : 0.f);
-      w[2 * e + i] = *reinterpret_cast<const uint32_t*>(&q);
+  if (tid < 2 * kMergeRows) {
+    const int own = tid / kMergeRows;
+    const bool live = t >= begin && t < end;
+    const uint32_t flag = live ? __ldcg(p.flag + at) : 0u;
+    const uint32_t where = live ? __ldcg(p.where + at) : 0u;
+    const int c = static_cast<int>(min(own ? flag >> 2 : where, static_cast<uint32_t>(kMaxCtas + kMaxPromptCtas))) - 1;
+    Parts x;
+    x.count = live && (own || (flag & kHasPrefix) != 0u) ? 1 : 0;
+    x.slot = 0;
+    x.step = 4;
+    x.to_l = 1;
+    if (c < 0) {
+      const size_t part = (own ? static_cast<size_t>(p.tokens) * p.q_heads : 0) + at;
+      x.x = p.part + part * D;
+      x.m = &p.part_ml[part].x;
+    } else {   // bounded, whatever the lists were
+      const SharedSplit s = p.shared_split[c];
+      const bool step = c < kMaxCtas;
+      const int range = step ? c : c - kMaxCtas, rows = step ? p.step_tile : 256;
+      if (x.count != 0) x.count = max(1, min(s.last, (step ? kMaxCtas : kMaxPromptCtas) - 1) - range + 1);
+      const int in = static_cast<int>(max(0LL, min(at_row - s.first, static_cast<long long>(rows - 1))));
+      x.slot = rows * (D + 2);
+      const float* slot = p.partial + (step ? 0 : 2 * kMaxCtas * step_slot_floats(D)) + static_cast<size_t>(2 * range + 1) * x.slot;
+      if (step) {
+        x.x = slot + in * D;
+        x.m = slot + rows * D + in;
+        x.to_l = rows;
+      } else {
+        slot += (in >> 7) * (prompt_slot_floats(D) / 2);
+        x.x = slot + (in & 127) * 4;
+        x.m = slot + D * 128 + (in & 127);
+        x.step = 4 * 128;
+        x.to_l = 128;
+      }
+    }
+    parts_of[own][row] = x;
+    if (own) {
+      live_of[row] = live;
+      sees_of[row] = (flag & kSees) != 0u;
+      top_of[row] = -INFINITY;
+      sum_of[row] = 0.f;
     }
   }
-  *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(t) * p.out_stride + static_cast<size_t>(h) * D + 8 * c) =
-      make_uint4(w[0], w[1], w[2], w[3]);
-  if (p.lse != nullptr && c == 0) p.lse[at] = sees ? kLn2 * base + logf(sum) : -INFINITY;
+  __syncthreads();
+  const int before = parts_of[0][row].count;
+  const float* at_prefix = parts_of[0][row].x + quad * parts_of[0][row].step;
+  const float* at_own = parts_of[1][row].x + quad * parts_of[1][row].step;
+  const int slot_prefix = parts_of[0][row].slot, slot_own = parts_of[1][row].slot;
+  const int parts = before + parts_of[1][row].count;
+  int most = parts;
+#pragma unroll
+  for (int d = 1; d < kMergeRows; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < most; i0 += kMergeParts) {
+    float4 v[kAhead];
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int n = i0 + j + i;
+        if (n < parts)
+          v[i] = __ldcg(reinterpret_cast<const float4*>(n < before ? at_prefix + static_cast<size_t>(slot_prefix) * max(2 * n - 1, 0)
+                                                                   : at_own + static_cast<size_t>(slot_own) * max(2 * (n - before) - 1, 0)));
+      }
+    };
+    fetch(0);
+    for (int r = tid >> 5; r < kMergeRows; r += kMergeRows * D / 4 / 32) {   // a warp for a row: a part a lane
+      const int i = i0 + (tid & 31);
+      float m = -INFINITY, l = 0.f;
+      const int n = parts_of[0][r].count;
+      if (i < n + parts_of[1][r].count) {
+        const Parts& x = parts_of[i < n ? 0 : 1][r];
+        const float* from = x.m + static_cast<size_t>(x.slot) * max(2 * (i < n ? i : i - n) - 1, 0);
+        m = __ldcg(from);
+        l = __ldcg(from + x.to_l);
+      }
+      const float was = top_of[r];
+      float top = fmaxf(was, m);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      const float base = top == -INFINITY ? 0.f : top;
+      const float f = ex2(m - base), k = ex2(was - base);
+      float sum = l * f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      factor[r][tid & 31] = f;
+      __syncwarp();
+      if ((tid & 31) == 0) {
+        keep[r] = k;
+        sum_of[r] = sum_of[r] * k + sum;
+        top_of[r] = top;
+      }
+    }
+    __syncthreads();
+    const float k = keep[row];
+    acc = make_float4(acc.x * k, acc.y * k, acc.z * k, acc.w * k);
+#pragma unroll 1
+    for (int j = 0; j < kMergeParts && i0 + j < most; j += kAhead) {
+      if (j > 0) fetch(j);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float f = i0 + j + i < parts ? factor[row][j + i] : 0.f;
+        acc = make_float4(fmaf(v[i].x, f, acc.x), fmaf(v[i].y, f, acc.y), fmaf(v[i].z, f, acc.z), fmaf(v[i].w, f, acc.w));
+      }
+    }
+    __syncthreads();
+  }
+  if (!live_of[row]) return;
+  const bool sees = sees_of[row];
+  const float sum = sum_of[row], top = top_of[row], inv = inverse_sum(sum, sees);
+  const __half2 a = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
+  const __half2 b = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
+  *reinterpret_cast<uint2*>(p.out + t * p.out_stride + (at - t * p.q_heads) * D + 4 * quad) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (p.lse != nullptr && quad == 0) p.lse[at] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
 }
 
 template <int D>
 exl3_status launch_merge(const AttnParams& p, cudaStream_t cs) {
-  constexpr int kHeads = 8 * kMergeThreads / D;
+  const long long rows = static_cast<long long>(p.tokens) * p.group;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tokens), static_cast<unsigned>((p.q_heads + kHeads - 1) / kHeads));
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows), static_cast<unsigned>(p.kv_heads));
+  cfg.blockDim = dim3(kMergeRows * D / 4);
   cfg.stream = cs;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -255,28 +359,37 @@ extern "C" exl3_status exl3_attention_shared(const exl3_kv_cache* cache, const e
   p.group_start = group_start;
   p.prefix_len = prefix_len;
   p.groups = groups;
-  p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + at.part);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + at.ml);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.shared_split = reinterpret_cast<attn::SharedSplit*>(ws + at.split);
+  p.flag = reinterpret_cast<uint32_t*>(ws + at.flag);
+  p.where = reinterpret_cast<uint32_t*>(ws + at.where);
+  p.part = reinterpret_cast<float*>(ws + at.part);
+  p.part_ml = reinterpret_cast<float2*>(ws + at.ml);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  // Where all that the tables can hold is soon read, it is not worth the second kernel: 8
+  // requests behind 2011 tokens (38 MB) 14 us, so 18; two behind 4000 (17 MB) 14 and 18; 8
+  // behind 16000 (267 MB) 43 us, so 35.
+  if (static_cast<double>(requests) * static_cast<double>(p.most) * cache->kv_heads * cache->head_dim * 2 <= attn::kWorthSharing)
+    return exl3_attention(cache, q, q_stride, q_heads, q_start, seq_len, requests, tokens, max_new, block_table, table_stride, scale,
+                          out, out_stride, lse, workspace, workspace_bytes, stream);
   // The few-rows kernel takes the requests if they all have few rows, and the prefixes that
-  // have few; the other kernel the rest.
+  // have few; the other kernel the rest, first, so that its blocks begin on SMs of their own.
   const bool own_few = attn::few_rows(max_new, p.group), prefix_few = attn::few_rows(max_group, p.group);
-  const bool both = !own_few || !prefix_few;
+  p.both = !own_few || !prefix_few;
   p.align = own_few ? attn::step_unit(cache->head_dim) : attn::kPromptUnit;
-  p.rows_lo = p.prefix_lo = 1;
   p.rows_hi = own_few ? 0x7FFFFFFF : attn::kStepRows;
   p.prefix_hi = prefix_few ? 0x7FFFFFFF : attn::kStepRows;
   p.followed = 1;
-  const int most = std::max(own_few ? max_new : 1, prefix_few ? max_group : 1);
-  if ((st = attn::launch_step(p, *cache, most * p.group > 8, cs)) != EXL3_OK) return st;
-  attn::AttnParams m = p;
-  if (both) {
-    m.rows_lo = own_few ? 0x7FFFFFFF : attn::kStepRows + 1;
-    m.prefix_lo = prefix_few ? 0x7FFFFFFF : attn::kStepRows + 1;
-    m.rows_hi = own_few ? 0 : 0x7FFFFFFF;
-    m.prefix_hi = prefix_few ? 0 : 0x7FFFFFFF;
-    m.partial += 2 * attn::kMaxCtas * attn::step_slot_floats(cache->head_dim);
-    if ((st = attn::launch_prompt(m, *cache, true, cs)) != EXL3_OK) return st;
+  p.sms = device_sm_count();
+  const bool wide = std::max(own_few ? max_new : 1, prefix_few ? max_group : 1) * p.group > 8;
+  p.step_shift = wide ? 4 : 3;
+  p.step_tile = 1 << p.step_shift;
+  if (p.both) {
+    attn::AttnParams many = p;
+    many.many = 1;
+    many.partial += 2 * attn::kMaxCtas * attn::step_slot_floats(cache->head_dim);
+    if ((st = attn::launch_prompt(many, *cache, false, cs)) != EXL3_OK) return st;
   }
+  if ((st = attn::launch_step(p, *cache, wide, cs)) != EXL3_OK) return st;
   return cache->head_dim == 64 ? attn::launch_merge<64>(p, cs) : attn::launch_merge<128>(p, cs);
 }

@@ -55,7 +55,13 @@ struct SplitItem {
   int t0, n, seq, rows;   // its request
   int base, head;         // its first row, its key/value head
   int last;               // the range in which it ends, -1: no such item
-  int own;                // calls with prefixes: of a request's own keys
+  int unused;
+};
+
+// The same for the parts of a row in calls with prefixes, in either kernel.
+struct SharedSplit {
+  long long first;        // number of the item's first row: token * group + head of the group
+  int last, unused;
 };
 
 struct AttnParams {
@@ -87,7 +93,13 @@ struct AttnParams {
   const int32_t* group_start;
   const int32_t* prefix_len;
   int groups, align;       // prefixes count up to a multiple of `align` keys, whole units of the kernel that goes on
-  int prefix_lo, prefix_hi;  // prefixes with rows in [prefix_lo, prefix_hi] are this launch's
+  int prefix_hi;           // the few-rows kernel takes requests of up to rows_hi rows and prefixes of up to prefix_hi
+  int many;                // this launch is the other kernel
+  int both, sms;           // both kernels run, side by side on the SMs
+  int step_tile, step_shift;  // rows of the few-rows kernel's tiles, their logarithm
+  SharedSplit* shared_split;  // [kMaxCtas] ranges of the few-rows kernel, then [kMaxPromptCtas] of the other
+  uint32_t* flag;          // [tokens][q_heads] what mark_row says of a row's own keys
+  uint32_t* where;         // [tokens][q_heads] and of its prefix
   float* part;             // sums of every row over the prefix, then over its own keys: [2][tokens][q_heads][head_dim]
   float2* part_ml;         // their m and l: [2][tokens][q_heads]
 };
@@ -101,79 +113,181 @@ struct Req {
   int late;         // token i of it sees the keys before min(seq, late + i + 1)
   int k0;           // its first key: those before are its group's prefix
   int row;          // of the block table
+  int other;        // calls with prefixes: rows, if the other launch's
 };
 
 template <bool SHARED>
 __device__ __forceinline__ int req_count(const AttnParams& p) { return SHARED ? p.groups + p.requests : p.requests; }
 
-__device__ __forceinline__ int first_token(const AttnParams& p, int b) { return min(max(p.q_start[b], 0), p.tokens); }
-__device__ __forceinline__ int cached_tokens(const AttnParams& p, int b) {
-  return static_cast<int>(min(static_cast<long long>(max(p.seq_len[b], 0)), p.most));
+// The lists that a call's work is found from: the caller's, or a copy in shared memory.  (What
+// is shared takes a chain of a dozen reads; from memory it took 4.5 us of either kernel.)
+struct Lists {
+  const int32_t *q_start, *seq_len, *group_start, *prefix_len;
+  __device__ __forceinline__ explicit Lists(const AttnParams& p)
+      : q_start(p.q_start), seq_len(p.seq_len), group_start(p.group_start), prefix_len(p.prefix_len) {}
+  // Room for 2 * req_count + 2 numbers; the block's threads meet before it is read.
+  __device__ __forceinline__ void copy_to(const AttnParams& p, int32_t* room, int threads) {
+    const int n = p.requests, g = p.groups;
+    int32_t *q = room, *s = q + n + 1, *a = s + n, *l = a + g + 1;
+    for (int i = threadIdx.x; i <= n; i += threads) {
+      q[i] = q_start[i];
+      if (i < n) s[i] = seq_len[i];
+    }
+    for (int i = threadIdx.x; i <= g; i += threads) {
+      a[i] = group_start[i];
+      if (i < g) l[i] = prefix_len[i];
+    }
+    q_start = q;
+    seq_len = s;
+    group_start = a;
+    prefix_len = l;
+  }
+};
+
+__device__ __forceinline__ int first_token(const AttnParams& p, const Lists& l, int b) { return min(max(l.q_start[b], 0), p.tokens); }
+__device__ __forceinline__ int cached_tokens(const AttnParams& p, const Lists& l, int b) {
+  return static_cast<int>(min(static_cast<long long>(max(l.seq_len[b], 0)), p.most));
 }
-__device__ __forceinline__ void set_rows(const AttnParams& p, Req& r, int lo, int hi) {
-  const long long rows = static_cast<long long>(r.n) * p.group;
-  r.rows = rows >= lo && rows <= hi ? static_cast<int>(rows) : 0;
+// A request's rows, which are this launch's or the other's.
+template <bool SHARED>
+__device__ __forceinline__ void set_rows(const AttnParams& p, Req& r, int most_few) {
+  const long long all = static_cast<long long>(r.n) * p.group;
+  if constexpr (SHARED) {
+    const int rows = static_cast<int>(min(all, 0x7FFFFFFFLL));
+    const bool mine = (rows > most_few) == (p.many != 0);
+    r.rows = mine ? rows : 0;
+    r.other = mine ? 0 : rows;
+  } else {
+    r.rows = all >= p.rows_lo && all <= p.rows_hi ? static_cast<int>(all) : 0;
+  }
 }
 
 struct Group {
   int a, e, prefix;  // requests a .. e - 1; the shared keys, 0 where one request alone would share them
 };
-__device__ __forceinline__ Group load_group(const AttnParams& p, int g) {
+__device__ __forceinline__ Group load_group(const AttnParams& p, const Lists& l, int g) {
   Group x;
-  x.a = min(max(p.group_start[g], 0), p.requests);
-  x.e = min(max(p.group_start[g + 1], x.a), p.requests);
-  const long long len = min(static_cast<long long>(max(p.prefix_len[g], 0)), p.most);
+  x.a = min(max(l.group_start[g], 0), p.requests);
+  x.e = min(max(l.group_start[g + 1], x.a), p.requests);
+  const long long len = min(static_cast<long long>(max(l.prefix_len[g], 0)), p.most);
   x.prefix = x.e - x.a > 1 ? static_cast<int>(len) & ~(p.align - 1) : 0;
   return x;
 }
 
 // A prefix: its pages are those of the first request that holds all of it.
-__device__ __forceinline__ Req load_prefix(const AttnParams& p, int g) {
-  Req r{0, 0, 0, 0, 0, 0, 0};
-  const Group x = load_group(p, g);
+__device__ __forceinline__ Req load_prefix(const AttnParams& p, const Lists& l, int g) {
+  Req r{0, 0, 0, 0, 0, 0, 0, 0};
+  const Group x = load_group(p, l, g);
   if (x.prefix == 0) return r;
   for (int b = x.a; b < x.e; ++b) {
-    const int n = max(first_token(p, b + 1) - first_token(p, b), 0);
-    if (cached_tokens(p, b) - n < x.prefix) continue;
-    r.t0 = first_token(p, x.a);
-    r.n = max(first_token(p, x.e) - r.t0, 0);
+    const int n = max(first_token(p, l, b + 1) - first_token(p, l, b), 0);
+    if (cached_tokens(p, l, b) - n < x.prefix) continue;
+    r.t0 = first_token(p, l, x.a);
+    r.n = max(first_token(p, l, x.e) - r.t0, 0);
     r.seq = r.late = x.prefix;
     r.row = b;
-    set_rows(p, r, p.prefix_lo, p.prefix_hi);
+    set_rows<true>(p, r, p.prefix_hi);
     break;
   }
   return r;
 }
 
 template <bool SHARED>
-__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
-  Req r{0, 0, 0, 0, 0, 0, 0};
+__device__ __forceinline__ Req make_req(const AttnParams& p, const Lists& l, int b) {
+  Req r{0, 0, 0, 0, 0, 0, 0, 0};
   if constexpr (SHARED) {
-    if (b < p.groups) return load_prefix(p, b);
+    if (b < p.groups) return load_prefix(p, l, b);
     b -= p.groups;
   }
   if (b < p.requests) {
-    const int a = first_token(p, b);
-    const int e = first_token(p, b + 1);
+    const int a = first_token(p, l, b);
+    const int e = first_token(p, l, b + 1);
     r.t0 = a;
     r.n = max(e - a, 0);
-    set_rows(p, r, p.rows_lo, p.rows_hi);
-    r.seq = cached_tokens(p, b);
+    set_rows<SHARED>(p, r, p.rows_hi);
+    r.seq = cached_tokens(p, l, b);
     r.late = r.seq - r.n;
     r.row = b;
     if constexpr (SHARED) {
       int g = -1, hi = p.groups;   // the last group that begins at b or before
       while (hi - g > 1) {
         const int mid = (g + hi) >> 1;
-        if (p.group_start[mid] <= b) g = mid; else hi = mid;
+        if (l.group_start[mid] <= b) g = mid; else hi = mid;
       }
       if (g >= 0) {
-        const Group x = load_group(p, g);
+        const Group x = load_group(p, l, g);
         if (b < x.e && r.late >= x.prefix) r.k0 = x.prefix;
       }
     }
   }
   return r;
+}
+
+static __device__ __noinline__ Req load_shared(const AttnParams& p, int b) { return make_req<true>(p, Lists(p), b); }
+
+// From a copy of the lists where there may be one.  (Their pointers want registers that a
+// call without prefixes does not have to spare.)
+template <bool SHARED>
+__device__ __forceinline__ Req load_from(const AttnParams& p, const Lists& l, int b) {
+  if constexpr (SHARED) return make_req<true>(p, l, b);
+  return make_req<false>(p, Lists(p), b);
+}
+// Where it is seldom needed.
+template <bool SHARED>
+__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
+  if constexpr (SHARED) return load_shared(p, b);
+  return make_req<false>(p, Lists(p), b);
+}
+
+// Up to 32 groups and requests: lane b's, from one round of reads and exchanges.
+__device__ __forceinline__ Req load_lanes(const AttnParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int b = lane - p.groups;   // its request
+  const bool group = b < 0, own = b >= 0 && b < p.requests;
+  const int32_t* two = group ? p.group_start + lane : p.q_start + (own ? b : 0);
+  const int first = two[0], second = two[1];
+  const int len = group ? p.prefix_len[lane] : own ? p.seq_len[b] : 0;
+  const int a = min(max(first, 0), group ? p.requests : p.tokens);
+  const int e = min(max(second, 0), group ? p.requests : p.tokens);
+  const int cut = static_cast<int>(min(static_cast<long long>(max(len, 0)), p.most));
+  Req r{0, 0, 0, 0, 0, 0, 0, 0};
+  const int prefix = group && e - a > 1 ? cut & ~(p.align - 1) : 0;
+  if (own) {
+    r.t0 = a;
+    r.n = max(e - a, 0);
+    r.seq = cut;
+    r.late = r.seq - r.n;
+    r.row = b;
+  }
+  for (int g = 0; g < p.groups; ++g) {
+    const int shared = __shfl_sync(0xFFFFFFFFu, prefix, g);
+    if (shared == 0) continue;
+    const int from = __shfl_sync(0xFFFFFFFFu, a, g), to = __shfl_sync(0xFFFFFFFFu, e, g);
+    const bool holds = own && b >= from && b < to && r.late >= shared;
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, holds);
+    if (holds) r.k0 = shared;
+    const int t0 = __shfl_sync(0xFFFFFFFFu, a, p.groups + from), t1 = __shfl_sync(0xFFFFFFFFu, e, p.groups + to - 1);
+    if (lane == g && who != 0u) {
+      r.t0 = t0;
+      r.n = max(t1 - t0, 0);
+      r.seq = r.late = shared;
+      r.row = __ffs(static_cast<int>(who)) - 1 - p.groups;
+    }
+  }
+  set_rows<true>(p, r, group ? p.prefix_hi : p.rows_hi);
+  return r;
+}
+
+// Where a row's sums lie, for the kernel that puts them together: 0, in p.part as a whole;
+// 1 + c, in parts that begin with the slots of range c of this launch (the many-rows kernel's
+// ranges are numbered behind the other's).  For its own keys besides: whether
+// it has a prefix, whether it sees a key at all.
+constexpr uint32_t kHasPrefix = 1, kSees = 2;
+__device__ __forceinline__ void mark_row(const AttnParams& p, const Req& r, bool own, int tok, size_t at, uint32_t code) {
+  if (own)
+    p.flag[at] = code << 2 | (r.k0 > 0 ? kHasPrefix : 0u) | (r.late + tok + 1 > 0 ? kSees : 0u);
+  else
+    p.where[at] = code;
 }
 
 // The first key that token `tok` of a request does not see.
@@ -211,6 +325,9 @@ __device__ __forceinline__ PageScale page_scale(const AttnParams& p, float ks, f
   // of the rounded logarithm, so that l and the sums agree; finite, so that it spoils no row whose P is 0
   s.iv = vs != vs ? 1.f : exp2f(-s.lv);
   return s;
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void tensor_g2s_at(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -272,10 +389,46 @@ constexpr int kStepTile = 16;
 constexpr size_t step_slot_floats(int head_dim) { return static_cast<size_t>(kStepTile) * (head_dim + 2); }
 
 // More: tiles of 256 rows.
+// A slot of partial results: for either MMA tile four columns of all 128 rows after one
+// another, then the rows' m, then their l.
 constexpr size_t prompt_slot_floats(int head_dim) { return static_cast<size_t>(256) * (head_dim + 2); }
-// Keys of a unit of the few-rows kernel (`step`) and of the other.
+inline int prompt_ctas() {
+  const int sms = device_sm_count();
+  return sms < kMaxPromptCtas ? sms : kMaxPromptCtas;
+}
+// Keys of a unit of the few-rows kernel (`step`) and of the other; what an item costs there
+// besides its units, in units.
 constexpr int step_unit(int head_dim) { return 4096 / head_dim; }
 constexpr int kPromptUnit = 128;
+constexpr int kStepItemCost = 4;
+constexpr int kPromptItemCost = 3;
+
+// A call with prefixes that takes both kernels lets them run side by side: the many-rows
+// kernel is bound by its tensor cores and the chain around them, the other by memory and
+// its own latencies, and both begin and end with some microseconds of latency.  The SMs
+// are divided by the time that each kernel's work takes of an SM: a unit of the many-rows
+// kernel 1.97 us, one of the other 0.16 us with three blocks an SM and 0.21 us with two.
+// What a request adds to either (x: many-rows units, y: the other's), for a key/value
+// head; roughly, for the sums only divide the SMs.
+struct Costs {
+  float x, y;
+};
+template <int D>
+__device__ __forceinline__ Costs costs_of(const AttnParams& p, const Req& r) {
+  const int keys = r.seq - r.k0;
+  const int few = p.many ? r.other : r.rows, many = p.many ? r.rows : r.other;
+  Costs c;
+  c.x = static_cast<float>(many + 255 >> 8) * static_cast<float>((keys >> 7) + 1 + kPromptItemCost);
+  c.y = static_cast<float>(few + p.step_tile - 1 >> p.step_shift) * static_cast<float>(keys / step_unit(D) + 1 + kStepItemCost);
+  return c;
+}
+// SMs of the many-rows kernel.
+__device__ __forceinline__ int many_sms(const AttnParams& p, float x, float y) {
+  if (x == 0.f || y == 0.f) return x == 0.f ? 0 : p.sms;
+  x *= p.step_shift > 3 ? 8.f : 12.f;
+  return min(max(__float2int_rn(static_cast<float>(p.sms) * __fdividef(x, x + y)), 1), p.sms - 1);
+}
+
 exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, bool after_step, cudaStream_t stream);
 exl3_status launch_step(const AttnParams& p, const exl3_kv_cache& c, bool wide, cudaStream_t stream);
 

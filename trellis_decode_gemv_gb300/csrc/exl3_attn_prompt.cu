@@ -246,7 +246,7 @@ constexpr int kWhole = 5;
 constexpr int kLeast = 4;   // units that are worth a range of their own
 // Ranges are cut in equal parts of units plus kItemCost for each item: beginning and
 // ending one (Q, the first scores, the output) takes about as long as that.
-constexpr int kItemCost = 3;
+constexpr int kItemCost = kPromptItemCost;
 
 // The items of a range: row tiles in order, the heads of a row tile after one
 // another.
@@ -327,9 +327,12 @@ __device__ __forceinline__ void block_scan(long long* room, long long (&v)[N], l
   }
 }
 
-// `room`: 12 bytes for each request (borrowed from the operand images).  False: the
-// CTA has nothing to do.
-template <bool SHARED>
+// Requests and groups whose lists are copied first in a call with prefixes.
+constexpr int kListed = 1024;
+
+// `room`: 12 bytes for each request, 20 up to kListed of them (borrowed from the operand
+// images).  False: the CTA has nothing to do.
+template <int D, bool SHARED>
 __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void* room, int& ctas, int& count) {
   const int tid = threadIdx.x;
   const int requests = req_count<SHARED>(p);
@@ -338,13 +341,46 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   const int per = (requests + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, requests), b1 = min(b0 + per, requests);
   long long* sums = reinterpret_cast<long long*>(c.top);   // not in use yet
+  Lists lists(p);
+  if constexpr (SHARED) {
+    if (requests <= kListed) {
+      lists.copy_to(p, reinterpret_cast<int32_t*>(req + requests), kThreads);
+      __syncthreads();
+    }
+  }
   long long mine[1] = {0}, tiles[1];
+  Costs costs{0.f, 0.f};
   for (int b = b0; b < b1; ++b) {
-    const Req r = load_req<SHARED>(p, b);
+    const Req r = load_from<SHARED>(p, lists, b);
     req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq - r.k0);
     mine[0] += row_tiles(r.rows);
+    if constexpr (SHARED) {
+      const Costs x = costs_of<D>(p, r);
+      costs.x += x.x;
+      costs.y += x.y;
+    }
+  }
+  if constexpr (SHARED) {   // the warps' sums behind those of the scans
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      costs.x += __shfl_xor_sync(0xFFFFFFFFu, costs.x, d);
+      costs.y += __shfl_xor_sync(0xFFFFFFFFu, costs.y, d);
+    }
+    if ((tid & 31) == 0) reinterpret_cast<Costs*>(sums + 6 * 32)[tid >> 5] = costs;
   }
   block_scan(sums, mine, tiles);
+  int most = static_cast<int>(gridDim.x);
+  if constexpr (SHARED) {
+    costs = Costs{0.f, 0.f};
+    for (int w = 0; w < kThreads / 32; ++w) {
+      costs.x += reinterpret_cast<const Costs*>(sums + 6 * 32)[w].x;
+      costs.y += reinterpret_cast<const Costs*>(sums + 6 * 32)[w].y;
+    }
+    most = min(most, many_sms(p, costs.x, costs.y));
+    // a few items that are split anyway are split evenly, and no range ends one item and begins another
+    const int items = static_cast<int>(min(tiles[0] * p.kv_heads, 0x7FFFFFFFLL));
+    if (items > 0 && 4LL * items <= most) most -= most % items;
+  }
   long long at = mine[0];
   for (int b = b0; b < b1; ++b) {
     first[b] = static_cast<int32_t>(at);
@@ -368,10 +404,10 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
     part[2] += static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads;
   }
   const long long own_cost = part[0];
-  block_scan(sums + 32, part, all);
+  block_scan(sums + 3 * 32, part, all);
   const long long cost = all[0], units = all[1];
   long long before = part[0], before_units = part[1];
-  ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all[2]));
+  ctas = static_cast<int>(min(static_cast<long long>(most), all[2]));
   const int cta = blockIdx.x;
   if (cta >= ctas) return false;
   const long long u[2] = {range_begin(cost, cta, ctas), range_begin(cost, cta + 1, ctas)};
@@ -387,7 +423,8 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (u[e] < before || u[e] >= before + of_tile) continue;
-        const int head = static_cast<int>((u[e] - before) / (len + kItemCost));
+        const long long off = u[e] - before;   // (a 64-bit division takes a few hundred clocks)
+        const int head = off <= 0x7FFFFFFFLL ? static_cast<int>(off) / (len + kItemCost) : static_cast<int>(off / (len + kItemCost));
         const long long start = before + static_cast<long long>(head) * (len + kItemCost);
         int lo = static_cast<int>(u[e] - start);
         if (len <= kWhole)
@@ -401,7 +438,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
           c.first_tile = x - first[b];
           c.first_head = head;
           c.first_lo = lo;
-          c.first_req = load_req<SHARED>(p, b);
+          c.first_req = load_from<SHARED>(p, lists, b);
         }
       }
       before += of_tile;
@@ -644,7 +681,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   const int h = head * p.group + (rr - tok * p.group);
   const size_t part_at = SHARED ? (static_cast<size_t>(own ? p.tokens : 0) + req.t0 + tok) * p.q_heads + h : 0;
   __half* dst = p.out + static_cast<size_t>(req.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + half * (D / 2);
-  constexpr size_t kTileFloats = static_cast<size_t>(kTile) * (D + 2);
+  constexpr size_t kTileFloats = prompt_slot_floats(D) / 2;
   constexpr size_t kMAt = static_cast<size_t>(D) * kTile, kLAt = static_cast<size_t>(D + 1) * kTile;
   float* slot = p.partial + (static_cast<size_t>(2 * blockIdx.x + (lo == 0 ? 1 : 0)) * 2 + x) * kTileFloats;
   const int quad0 = half * (D / 8);   // this half's first four columns
@@ -678,7 +715,10 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   float* lse = p.lse != nullptr && half == 0 ? p.lse + static_cast<size_t>(req.t0 + tok) * p.q_heads + h : nullptr;
   if (whole) {
     if constexpr (SHARED) {
-      if (mine && half == 0) p.part_ml[part_at] = make_float2(m, l);
+      if (mine && half == 0) {
+        p.part_ml[part_at] = make_float2(m, l);
+        mark_row(p, req, own, tok, part_at - (own ? static_cast<size_t>(p.tokens) * p.q_heads : 0), 0u);
+      }
       return;
     }
     if (mine && lse != nullptr) *lse = sees ? kLn2 * (m == -INFINITY ? 0.f : m) + logf(l) : -INFINITY;
@@ -689,8 +729,17 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
     __stcg(slot + kLAt + r, l);
   }
   // the range in which the item begins tells the join about it
+  if constexpr (SHARED) {
+    if (lo == 0 && half == 0) {
+      if (mine)
+        mark_row(p, req, own, tok, part_at - (own ? static_cast<size_t>(p.tokens) * p.q_heads : 0), 1u + kMaxCtas + blockIdx.x);
+      if (x == 0 && r == 0)
+        p.shared_split[kMaxCtas + blockIdx.x] = SharedSplit{static_cast<long long>(req.t0) * p.group + base, ctl.last_range, 0};
+    }
+    return;
+  }
   if (lo == 0 && x == 0 && half == 0 && r == 0)
-    p.split[blockIdx.x] = SplitItem{req.t0, req.n, req.seq, req.rows, base, head, ctl.last_range, own ? 1 : 0};
+    p.split[blockIdx.x] = SplitItem{req.t0, req.n, req.seq, req.rows, base, head, ctl.last_range, 0};
 }
 
 // Items that are spread over several ranges, after the other kernel: block (c, y) the
@@ -700,9 +749,8 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
 constexpr int kJoinRows = 16;
 constexpr int kJoinThreads = 128;
 
-template <int D, bool SHARED>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
-  if constexpr (SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const SplitItem it = p.split[c];
@@ -741,13 +789,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int rr = it.base + row;
   const int tok = rr / p.group;
   const int h = it.head * p.group + (rr - tok * p.group);
-  if constexpr (SHARED) {
-    const size_t at = (static_cast<size_t>(it.own ? p.tokens : 0) + it.t0 + tok) * p.q_heads + h;
-#pragma unroll
-    for (int e = 0; e < kQuads; ++e) reinterpret_cast<float4*>(p.part + at * D)[quad0 + e] = acc[e];
-    if (quad0 == 0) p.part_ml[at] = make_float2(top, sum);
-    return;
-  }
   const bool sees = it.seq - it.n + tok + 1 > 0;
   const float inv = inverse_sum(sum, sees);
   __half* dst = p.out + static_cast<size_t>(it.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + 4 * quad0;
@@ -794,10 +835,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 0) p.split[blockIdx.x].last = -1;   // no item begins here and ends later, so far
+  if (SHARED && tid == 32) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+    prefetch_map(&qmap);
+  }
+  if (!SHARED && tid == 0) p.split[blockIdx.x].last = -1;   // no item begins here and ends later, so far
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int ctas, count;
-  if (!find_range<SHARED>(p, ctl, smem_raw, ctas, count)) {
+  if (!find_range<D, SHARED>(p, ctl, smem_raw, ctas, count)) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // not done before the few-rows kernel is
     return;
   }
@@ -1129,8 +1175,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
   static std::atomic<unsigned long long> allowed{0};
   if (!allow_smem(prompt_kernel<D, SHARED>, kSmem, allowed)) return EXL3_ERR_CUDA;
-  int ctas = device_sm_count();
-  if (ctas > kMaxPromptCtas) ctas = kMaxPromptCtas;
+  const int ctas = prompt_ctas();
   // After the few-rows kernel a CTA begins as soon as an SM is free: the two write
   // nothing in common (one of 100 tokens beside 8 single ones over 300 keys: 38 us, so 31;
   // 2 of 500 beside 11 over up to 8 K: 135, so 132).
@@ -1147,6 +1192,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   if (cudaLaunchKernelEx(&own, prompt_kernel<D, SHARED>, p, kmap, vmap, qmap) != cudaSuccess) return EXL3_ERR_CUDA;
   exl3_status st = launch_status();
   if (st != EXL3_OK) return st;
+  if constexpr (SHARED) return EXL3_OK;   // what puts prefixes and own keys together joins too
   // a table whose rows hold no item that is ever split leaves nothing to join
   if (p.most <= static_cast<long long>(kWhole) * kKeys) return EXL3_OK;
   cudaLaunchConfig_t cfg = {};
@@ -1155,7 +1201,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<D, SHARED>, p) != cudaSuccess) return EXL3_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return EXL3_ERR_CUDA;
   return launch_status();
 }
 

@@ -92,7 +92,7 @@ __device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq -
 // falls into it moves to its nearer end.  Measured on 1 to 200 requests of 300 to
 // 131 K keys; with an item counted as one unit 200 requests of up to 600 keys took
 // 45 us, with four 35; with kWhole 24 a single request of 517 keys 10.2, with 12 8.7.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = kStepItemCost;
 constexpr int kWhole = 12;
 // Units that are worth a range of their own: with 8 in place of 4 33 requests of up to
 // 2011 keys took 12.1 us in place of 11.4, 8 of 1024 11.8 and not 11.0, but one of 2000 10.3
@@ -206,8 +206,20 @@ struct Shared {
   uint64_t q_full[kQSlots], q_empty[kQSlots];
   long long warp_sum[kThreads / 32], warp_ranges[kThreads / 32];
   Edge edge[2];
+  Costs warp_costs[kThreads / 32];
   uint32_t abort, last;
 };
+
+// Calls with prefixes: requests and groups whose lists are copied behind that.
+constexpr int kListed = 256;
+constexpr size_t kListedBytes = sizeof(int32_t) * (2 * kListed + 2);
+
+// The end of a block.  Beside the many-rows kernel this one is not done before that is, so
+// that what follows need wait for this one only.
+template <bool SHARED>
+__device__ __forceinline__ void leave_early(int cta) {
+  if (SHARED && cta == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // The consumers' sums of a row, 4 columns of it: with the row's maximum and sum.
 template <int D, int NT>
@@ -240,9 +252,13 @@ __device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, boo
   const int tok = rr / p.group;
   const int h = head * p.group + (rr - tok * p.group);
   if constexpr (SHARED) {
-    const size_t at = (static_cast<size_t>(own ? p.tokens : 0) + r.t0 + tok) * p.q_heads + h;
-    *reinterpret_cast<float4*>(p.part + at * D + 4 * q4) = acc;
-    if (q4 == 0) p.part_ml[at] = make_float2(top, sum);
+    const size_t at = static_cast<size_t>(r.t0 + tok) * p.q_heads + h;
+    const size_t part = own ? static_cast<size_t>(p.tokens) * p.q_heads + at : at;
+    *reinterpret_cast<float4*>(p.part + part * D + 4 * q4) = acc;
+    if (q4 == 0) {
+      p.part_ml[part] = make_float2(top, sum);
+      mark_row(p, r, own, tok, at, 0u);
+    }
     return;
   }
   const bool sees = r.late + tok + 1 > 0;
@@ -283,6 +299,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
   const int warp = tid >> 5;
   const int cta = blockIdx.x;
 
+  if (SHARED && tid == kThreads - 1) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full[i], 2);   // the copies, the scales
@@ -302,8 +322,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
   int ctas, first = 0;
   Req lanes;
   const int count = req_count<SHARED>(p);
+  Lists lists(p);
+  if constexpr (SHARED) {
+    if (count > 32 && count <= kListed) {
+      lists.copy_to(p, reinterpret_cast<int32_t*>(smem_raw + sizeof(Shared<D, NT>)), kThreads);
+      __syncthreads();
+    }
+  }
+  int most = static_cast<int>(gridDim.x);   // blocks that this call may take
   if (count <= 32) {
-    const Req r = load_req<SHARED>(p, lane);
+    Req r;
+    if constexpr (SHARED) r = load_lanes(p); else r = load_from<SHARED>(p, lists, lane);
     lanes = r;
     long long cost = 0, ranges = 0;
     req_cost<D, NT>(p, r, cost, ranges);
@@ -315,14 +344,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       ranges += __shfl_xor_sync(0xFFFFFFFFu, ranges, d);
     }
     const long long total = __shfl_sync(0xFFFFFFFFu, inc, 31);
-    ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), ranges));
-    if (cta >= ctas) return;
+    if constexpr (SHARED) {
+      if (p.both) {
+        Costs c = costs_of<D>(p, r);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          c.x += __shfl_xor_sync(0xFFFFFFFFu, c.x, d);
+          c.y += __shfl_xor_sync(0xFFFFFFFFu, c.y, d);
+        }
+        most = min(most, C::kCtasPerSm * (p.sms - many_sms(p, c.x, c.y)));
+      }
+    }
+    ctas = static_cast<int>(min(static_cast<long long>(most), ranges));
+    if (cta >= ctas) return leave_early<SHARED>(cta);
     __syncthreads();   // the barriers
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const long long u = range_begin(total, cta + e, ctas);
       const int b = __popc(__ballot_sync(0xFFFFFFFFu, inc <= u));   // the request that holds u
-      Req q{0, 0, 1, 0, 0, 0, 0};
+      Req q{0, 0, 1, 0, 0, 0, 0, 0};
       q.seq = __shfl_sync(0xFFFFFFFFu, r.seq - r.k0, b & 31);
       const long long before = __shfl_sync(0xFFFFFFFFu, inc - cost, b & 31);
       Edge x{count, 0, 0, 0, 0};
@@ -333,17 +373,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const int per = (count + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, count), b1 = min(b0 + per, count);
     long long mine = 0, ranges = 0;
-    for (int b = b0; b < b1; ++b) req_cost<D, NT>(p, load_req<SHARED>(p, b), mine, ranges);
+    Costs costs{0.f, 0.f};
+    Req only;   // this thread's request, if it has one at most
+    for (int b = b0; b < b1; ++b) {
+      const Req r = load_from<SHARED>(p, lists, b);
+      req_cost<D, NT>(p, r, mine, ranges);
+      if constexpr (SHARED) {
+        only = r;
+        const Costs c = costs_of<D>(p, r);
+        costs.x += c.x;
+        costs.y += c.y;
+      }
+    }
     long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
       if (lane >= d) inc += o;
       ranges += __shfl_xor_sync(0xFFFFFFFFu, ranges, d);
+      if constexpr (SHARED) {
+        costs.x += __shfl_xor_sync(0xFFFFFFFFu, costs.x, d);
+        costs.y += __shfl_xor_sync(0xFFFFFFFFu, costs.y, d);
+      }
     }
     if (lane == 31) {
       sh.warp_sum[warp] = inc;
       sh.warp_ranges[warp] = ranges;
+      if constexpr (SHARED) sh.warp_costs[warp] = costs;
     }
     if (tid == 0) sh.edge[1] = Edge{count, 0, 0, 0, 0};   // the last range's end is in no item
     __syncthreads();
@@ -354,12 +410,23 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       total += sh.warp_sum[w];
       all_ranges += sh.warp_ranges[w];
     }
-    ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all_ranges));
-    if (cta >= ctas) return;
+    if constexpr (SHARED) {
+      if (p.both) {
+        Costs c{0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+          c.x += sh.warp_costs[w].x;
+          c.y += sh.warp_costs[w].y;
+        }
+        most = min(most, C::kCtasPerSm * (p.sms - many_sms(p, c.x, c.y)));
+      }
+    }
+    ctas = static_cast<int>(min(static_cast<long long>(most), all_ranges));
+    if (cta >= ctas) return leave_early<SHARED>(cta);
     const long long u[2] = {range_begin(total, cta, ctas), range_begin(total, cta + 1, ctas)};
     if (u[1] >= before && u[0] < before + mine) {
       for (int b = b0; b < b1; ++b) {
-        const Req r = load_req<SHARED>(p, b);
+        const Req r = SHARED && per == 1 ? only : load_from<SHARED>(p, lists, b);
         long long n = 0, unused = 0;
         req_cost<D, NT>(p, r, n, unused);
 #pragma unroll
@@ -372,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     from = sh.edge[0];
     to = sh.edge[1];
     first = from.b;
-    lanes = load_req<SHARED>(p, first + lane);
+    lanes = load_from<SHARED>(p, lists, first + lane);
   }
   Walker<D, NT, SHARED> w(p, from, to, first, lanes);
 
@@ -678,10 +745,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
           store_out<D, SHARED>(p, w.r, SHARED && w.b >= p.groups, w.head, row0 + 8 * nt + row, q4, acc, top, sum);
         } else {
           leave<D, kRows>(slot, 8 * nt + row, q4, acc, top, sum);
+          if (SHARED && q4 == 0 && w.lo == 0) {
+            const int rr = row0 + 8 * nt + row, tok = rr / p.group;
+            mark_row(p, w.r, w.b >= p.groups, tok,
+                     static_cast<size_t>(w.r.t0 + tok) * p.q_heads + w.head * p.group + (rr - tok * p.group), 1u + cta);
+          }
         }
       }
     }
     if (whole) continue;
+    if constexpr (SHARED) {   // the next kernel joins
+      if (tid == 0 && w.lo == 0)
+        p.shared_split[cta] = SharedSplit{static_cast<long long>(w.r.t0) * p.group + row0, to.c1, 0};
+      continue;
+    }
 
     // ---- the item crosses ranges: the last to arrive joins --------------------------
     // Many ranges in two levels: the last of 8, 16 or 32 neighbours joins theirs into
@@ -774,7 +851,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
           const int row = x / kQuads, col = x % kQuads;
           const float4 v = join_warps(sh, row, col, mx, total);
           if (rest)
-            store_out<D, SHARED>(p, w.r, SHARED && w.b >= p.groups, w.head, row0 + r0 + row, col, v, mx, total);
+            store_out<D, SHARED>(p, w.r, false, w.head, row0 + r0 + row, col, v, mx, total);
           else
             leave<D, kRows>(p.partial + static_cast<size_t>(2 * k0 + (k0 == c0 ? 1 : 0)) * kSlot, r0 + row, col, v, mx, total);
         }
@@ -791,17 +868,32 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     atomicOr(&sh.abort, 1u);
     atomicOr(p.status, 1u);
   }
+  leave_early<SHARED>(cta);
 }
 
 template <int D, int NT, bool SHARED>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  const size_t smem = sizeof(Shared<D, NT>);
+  const size_t smem = sizeof(Shared<D, NT>) + (SHARED ? kListedBytes : 0);
   static std::atomic<unsigned long long> allowed{0};
   if (!allow_smem(step_kernel<D, NT, SHARED>, smem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count() * C::kCtasPerSm;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  step_kernel<D, NT, SHARED><<<ctas, C::kThreads, smem, stream>>>(p, kmap, vmap);
+  if constexpr (SHARED) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.both ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, step_kernel<D, NT, true>, p, kmap, vmap) != cudaSuccess) return EXL3_ERR_CUDA;
+  } else {
+    step_kernel<D, NT, SHARED><<<ctas, C::kThreads, smem, stream>>>(p, kmap, vmap);
+  }
   return launch_status();
 }
 
