@@ -136,164 +136,146 @@ SharedLayout shared_layout(int q_heads, int kv_heads, int head_dim, int max_new,
 }
 
 // A row's result from its sums over the prefix and over its own keys, either of which may lie
-// in parts, one for each range that the item was spread over.  A block takes 16 rows (of
-// the tokens' heads of one key/value head), a thread four columns of one: 16
-// neighbouring rows of a part of the many-rows kernel are 256 contiguous bytes.  The
-// parts come in the order of the keys, their factors, 32 parts at a time, while the first
-// sums are on their way.  All that a row needs the other kernels have left beside its sums: finding
-// its request anew took each block 1.5 us.  Rows of no request are left alone.
-constexpr int kMergeRows = 16;
-constexpr int kMergeParts = 32;
-constexpr int kAhead = 8;   // parts of which a thread's columns are on their way
+// in parts, one for each range that the item was spread over.  A warp takes a row; the
+// parts come in the order of the keys, m and l of 32 at a time, a part a lane, and the
+// sums in turn, a row's columns over the lanes.  What a row needs besides the other
+// kernels have left beside its sums: finding its request anew took 1.5 us.  Rows of no
+// request are left alone.
+constexpr int kMergeThreads = 256;
+constexpr int kAhead = 8;   // parts whose sums are on their way
 
-// A row's sums over its prefix or its own keys: of part i the columns lie at x + slot *
-// max(2 i - 1, 0), four of them every `step` floats, the row's m and l in the same way.
+// A row's sums over its prefix or its own keys: of part i this lane's columns lie at x + slot *
+// max(2 i - 1, 0) floats, the row's m and l in the same way.
 struct Parts {
   const float *x, *m;
-  int count, slot, step, to_l;
+  int count, slot, to_l;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMergeRows* D / 4, 1024 / (kMergeRows * D / 4)) merge_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ Parts parts_of[2][kMergeRows];
-  __shared__ bool live_of[kMergeRows], sees_of[kMergeRows];
-  __shared__ float factor[kMergeRows][kMergeParts + 1], keep[kMergeRows];
-  __shared__ float top_of[kMergeRows], sum_of[kMergeRows];
-  const int tid = threadIdx.x;
-  const int row = tid % kMergeRows, quad = tid / kMergeRows;
-  const long long at_row = static_cast<long long>(blockIdx.x) * kMergeRows + row;   // token * group + head of the group
-  const long long t = at_row / p.group;
-  const size_t at = static_cast<size_t>(t) * p.q_heads + static_cast<size_t>(blockIdx.y) * p.group + (at_row - t * p.group);
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, bool own, uint32_t code, bool any, size_t at, long long row, int col) {
+  const int c = static_cast<int>(min(code, static_cast<uint32_t>(kMaxCtas + kMaxPromptCtas))) - 1;
+  Parts x;
+  x.count = any ? 1 : 0;
+  x.slot = 0;
+  x.to_l = 1;
+  if (c < 0) {
+    const size_t part = (own ? static_cast<size_t>(p.tokens) * p.q_heads : 0) + at;
+    x.x = p.part + part * D + col;
+    x.m = &p.part_ml[part].x;
+    return x;
+  }
+  // bounded, whatever the lists were
+  const SharedSplit s = p.shared_split[c];
+  const bool step = c < kMaxCtas;
+  const int range = step ? c : c - kMaxCtas, rows = step ? p.step_tile : 256;
+  if (any) x.count = max(1, min(s.last, (step ? kMaxCtas : kMaxPromptCtas) - 1) - range + 1);
+  const int in = static_cast<int>(max(0LL, min(row - s.first, static_cast<long long>(rows - 1))));
+  x.slot = rows * (D + 2);
+  const float* slot = p.partial + (step ? 0 : 2 * kMaxCtas * step_slot_floats(D)) + static_cast<size_t>(2 * range + 1) * x.slot;
+  if (step) {
+    x.x = slot + in * D + col;
+    x.m = slot + rows * D + in;
+    x.to_l = rows;
+  } else {
+    slot += (in >> 7) * (prompt_slot_floats(D) / 2);
+    x.x = slot + (col >> 3) * 1024 + (in & 127) * 8 + (col & 7);
+    x.m = slot + D * 128 + (in & 127);
+    x.to_l = 128;
+  }
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kCols = D / 32;   // of a lane
+  const int lane = threadIdx.x & 31;
+  const size_t at = static_cast<size_t>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);   // [token][head]
+  const long long t = static_cast<long long>(at / p.q_heads);
+  const int h = static_cast<int>(at - static_cast<size_t>(t) * p.q_heads);
+  const long long row = t * p.group + h % p.group;
   // the requests' tokens: all between the first one's and the last one's
   const Lists lists(p);
   const int begin = first_token(p, lists, 0), end = first_token(p, lists, p.requests);
+  if (t < begin || t >= end) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tid < 2 * kMergeRows) {
-    const int own = tid / kMergeRows;
-    const bool live = t >= begin && t < end;
-    const uint32_t flag = live ? __ldcg(p.flag + at) : 0u;
-    const uint32_t where = live ? __ldcg(p.where + at) : 0u;
-    const int c = static_cast<int>(min(own ? flag >> 2 : where, static_cast<uint32_t>(kMaxCtas + kMaxPromptCtas))) - 1;
-    Parts x;
-    x.count = live && (own || (flag & kHasPrefix) != 0u) ? 1 : 0;
-    x.slot = 0;
-    x.step = 4;
-    x.to_l = 1;
-    if (c < 0) {
-      const size_t part = (own ? static_cast<size_t>(p.tokens) * p.q_heads : 0) + at;
-      x.x = p.part + part * D;
-      x.m = &p.part_ml[part].x;
-    } else {   // bounded, whatever the lists were
-      const SharedSplit s = p.shared_split[c];
-      const bool step = c < kMaxCtas;
-      const int range = step ? c : c - kMaxCtas, rows = step ? p.step_tile : 256;
-      if (x.count != 0) x.count = max(1, min(s.last, (step ? kMaxCtas : kMaxPromptCtas) - 1) - range + 1);
-      const int in = static_cast<int>(max(0LL, min(at_row - s.first, static_cast<long long>(rows - 1))));
-      x.slot = rows * (D + 2);
-      const float* slot = p.partial + (step ? 0 : 2 * kMaxCtas * step_slot_floats(D)) + static_cast<size_t>(2 * range + 1) * x.slot;
-      if (step) {
-        x.x = slot + in * D;
-        x.m = slot + rows * D + in;
-        x.to_l = rows;
-      } else {
-        slot += (in >> 7) * (prompt_slot_floats(D) / 2);
-        x.x = slot + (in & 127) * 4;
-        x.m = slot + D * 128 + (in & 127);
-        x.step = 4 * 128;
-        x.to_l = 128;
-      }
-    }
-    parts_of[own][row] = x;
-    if (own) {
-      live_of[row] = live;
-      sees_of[row] = (flag & kSees) != 0u;
-      top_of[row] = -INFINITY;
-      sum_of[row] = 0.f;
-    }
-  }
-  __syncthreads();
-  const int before = parts_of[0][row].count;
-  const float* at_prefix = parts_of[0][row].x + quad * parts_of[0][row].step;
-  const float* at_own = parts_of[1][row].x + quad * parts_of[1][row].step;
-  const int slot_prefix = parts_of[0][row].slot, slot_own = parts_of[1][row].slot;
-  const int parts = before + parts_of[1][row].count;
-  int most = parts;
-#pragma unroll
-  for (int d = 1; d < kMergeRows; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < most; i0 += kMergeParts) {
-    float4 v[kAhead];
+  const uint32_t flag = __ldcg(p.flag + at), where = __ldcg(p.where + at);
+  const bool sees = (flag & kSees) != 0u;
+  const Parts a = parts_of<D>(p, false, where, (flag & kHasPrefix) != 0u, at, row, kCols * lane);
+  const Parts b = parts_of<D>(p, true, flag >> 2, true, at, row, kCols * lane);
+  const int parts = a.count + b.count;
+  float top = -INFINITY, sum = 0.f;
+  float acc[kCols] = {};
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float v[kAhead][kCols];
     auto fetch = [&](int j) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int n = i0 + j + i;
-        if (n < parts)
-          v[i] = __ldcg(reinterpret_cast<const float4*>(n < before ? at_prefix + static_cast<size_t>(slot_prefix) * max(2 * n - 1, 0)
-                                                                   : at_own + static_cast<size_t>(slot_own) * max(2 * (n - before) - 1, 0)));
+        const int n = i0 + j + i, k = n < a.count ? n : n - a.count;
+        const float* from = (n < a.count ? a.x : b.x) + static_cast<size_t>(n < a.count ? a.slot : b.slot) * max(2 * k - 1, 0);
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) v[i][e] = 0.f;
+        if (n < parts) {
+          if constexpr (kCols == 4)
+            *reinterpret_cast<float4*>(v[i]) = __ldcg(reinterpret_cast<const float4*>(from));
+          else
+            *reinterpret_cast<float2*>(v[i]) = __ldcg(reinterpret_cast<const float2*>(from));
+        }
       }
     };
     fetch(0);
-    for (int r = tid >> 5; r < kMergeRows; r += kMergeRows * D / 4 / 32) {   // a warp for a row: a part a lane
-      const int i = i0 + (tid & 31);
-      float m = -INFINITY, l = 0.f;
-      const int n = parts_of[0][r].count;
-      if (i < n + parts_of[1][r].count) {
-        const Parts& x = parts_of[i < n ? 0 : 1][r];
-        const float* from = x.m + static_cast<size_t>(x.slot) * max(2 * (i < n ? i : i - n) - 1, 0);
+    float m = -INFINITY, l = 0.f;
+    {
+      const int n = i0 + lane, k = n < a.count ? n : n - a.count;
+      if (n < parts) {
+        const float* from = (n < a.count ? a.m : b.m) + static_cast<size_t>(n < a.count ? a.slot : b.slot) * max(2 * k - 1, 0);
         m = __ldcg(from);
-        l = __ldcg(from + x.to_l);
-      }
-      const float was = top_of[r];
-      float top = fmaxf(was, m);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      const float base = top == -INFINITY ? 0.f : top;
-      const float f = ex2(m - base), k = ex2(was - base);
-      float sum = l * f;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      factor[r][tid & 31] = f;
-      __syncwarp();
-      if ((tid & 31) == 0) {
-        keep[r] = k;
-        sum_of[r] = sum_of[r] * k + sum;
-        top_of[r] = top;
+        l = __ldcg(from + (n < a.count ? a.to_l : b.to_l));
       }
     }
-    __syncthreads();
-    const float k = keep[row];
-    acc = make_float4(acc.x * k, acc.y * k, acc.z * k, acc.w * k);
+    float next = fmaxf(top, m);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, d));
+    const float base = next == -INFINITY ? 0.f : next;
+    const float f = ex2(m - base), keep = ex2(top - base);
+    float s = l * f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    sum = sum * keep + s;
+    top = next;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) acc[e] *= keep;
 #pragma unroll 1
-    for (int j = 0; j < kMergeParts && i0 + j < most; j += kAhead) {
+    for (int j = 0; j < 32 && i0 + j < parts; j += kAhead) {
       if (j > 0) fetch(j);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const float f = i0 + j + i < parts ? factor[row][j + i] : 0.f;
-        acc = make_float4(fmaf(v[i].x, f, acc.x), fmaf(v[i].y, f, acc.y), fmaf(v[i].z, f, acc.z), fmaf(v[i].w, f, acc.w));
+        const float w = __shfl_sync(0xFFFFFFFFu, f, j + i);
+        if (i0 + j + i < parts) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
+        }
       }
     }
-    __syncthreads();
   }
-  if (!live_of[row]) return;
-  const bool sees = sees_of[row];
-  const float sum = sum_of[row], top = top_of[row], inv = inverse_sum(sum, sees);
-  const __half2 a = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
-  const __half2 b = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
-  *reinterpret_cast<uint2*>(p.out + t * p.out_stride + (at - t * p.q_heads) * D + 4 * quad) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (p.lse != nullptr && quad == 0) p.lse[at] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
+  const float inv = inverse_sum(sum, sees);
+  __half* to = p.out + t * p.out_stride + static_cast<size_t>(h) * D + kCols * lane;
+#pragma unroll
+  for (int e = 0; e < kCols; e += 2) {
+    const __half2 o = __floats2half2_rn(sees ? acc[e] * inv : 0.f, sees ? acc[e + 1] * inv : 0.f);
+    reinterpret_cast<__half2*>(to)[e / 2] = o;
+  }
+  if (p.lse != nullptr && lane == 0) p.lse[at] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
 }
 
 template <int D>
 exl3_status launch_merge(const AttnParams& p, cudaStream_t cs) {
-  const long long rows = static_cast<long long>(p.tokens) * p.group;
+  const long long rows = static_cast<long long>(p.tokens) * p.q_heads;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows), static_cast<unsigned>(p.kv_heads));
-  cfg.blockDim = dim3(kMergeRows * D / 4);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = cs;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

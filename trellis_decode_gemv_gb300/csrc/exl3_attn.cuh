@@ -419,13 +419,13 @@ __device__ __forceinline__ Costs costs_of(const AttnParams& p, const Req& r) {
   const int few = p.many ? r.other : r.rows, many = p.many ? r.rows : r.other;
   Costs c;
   c.x = static_cast<float>(many + 255 >> 8) * static_cast<float>((keys >> 7) + 1 + kPromptItemCost);
-  c.y = static_cast<float>(few + p.step_tile - 1 >> p.step_shift) * static_cast<float>(keys / step_unit(D) + 1 + kStepItemCost);
+  c.y = static_cast<float>(few + p.step_tile - 1 >> p.step_shift) * static_cast<float>(keys / step_unit(D) + 1 + (p.step_shift > 3 ? 2 : 1) * kStepItemCost);
   return c;
 }
 // SMs of the many-rows kernel.
 __device__ __forceinline__ int many_sms(const AttnParams& p, float x, float y) {
   if (x == 0.f || y == 0.f) return x == 0.f ? 0 : p.sms;
-  x *= p.step_shift > 3 ? 8.f : 12.f;
+  x *= p.step_shift > 3 ? 10.f : 14.f;
   return min(max(__float2int_rn(static_cast<float>(p.sms) * __fdividef(x, x + y)), 1), p.sms - 1);
 }
 

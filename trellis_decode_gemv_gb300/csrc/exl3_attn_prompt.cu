@@ -330,7 +330,7 @@ __device__ __forceinline__ void block_scan(long long* room, long long (&v)[N], l
 // Requests and groups whose lists are copied first in a call with prefixes.
 constexpr int kListed = 1024;
 
-// `room`: 12 bytes for each request, 20 up to kListed of them (borrowed from the operand
+// `room`: 12 bytes for each request, 52 up to kListed of them (borrowed from the operand
 // images).  False: the CTA has nothing to do.
 template <int D, bool SHARED>
 __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void* room, int& ctas, int& count) {
@@ -342,9 +342,11 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   const int b0 = min(tid * per, requests), b1 = min(b0 + per, requests);
   long long* sums = reinterpret_cast<long long*>(c.top);   // not in use yet
   Lists lists(p);
+  Req* kept = nullptr;   // what is found out about each request
   if constexpr (SHARED) {
     if (requests <= kListed) {
-      lists.copy_to(p, reinterpret_cast<int32_t*>(req + requests), kThreads);
+      kept = reinterpret_cast<Req*>(static_cast<unsigned char*>(room) + 12 * kListed + 16);
+      lists.copy_to(p, reinterpret_cast<int32_t*>(kept + requests), kThreads);
       __syncthreads();
     }
   }
@@ -355,6 +357,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
     req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq - r.k0);
     mine[0] += row_tiles(r.rows);
     if constexpr (SHARED) {
+      if (kept != nullptr) kept[b] = r;
       const Costs x = costs_of<D>(p, r);
       costs.x += x.x;
       costs.y += x.y;
@@ -388,6 +391,63 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   }
   __syncthreads();
   const int n = static_cast<int>(tiles[0]);
+  if (SHARED && kept != nullptr && n <= 32) {
+    // As many tiles as lanes, a tile each: every warp finds the range by itself.  (The way
+    // below takes 4 us, most of it for code that comes from memory.)
+    const int x = tid & 31;
+    int b = 0, to = requests;
+    while (to - b > 1) {
+      const int mid = (b + to) >> 1;
+      if (first[mid] <= x) b = mid; else to = mid;
+    }
+    const int tile = x - first[b];
+    const int len = x < n ? tile_units<true>(p, kept[b], tile) : 0;
+    const long long cost = x < n ? static_cast<long long>(len + kItemCost) * p.kv_heads : 0;
+    long long sum = cost, ranges = x < n ? static_cast<long long>(len <= kWhole ? 1 : (len + kLeast - 1) / kLeast) * p.kv_heads : 0;
+    int lens = len;   // of tiles up to this one
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      const int l = __shfl_up_sync(0xFFFFFFFFu, lens, d);
+      if (x >= d) {
+        sum += o;
+        lens += l;
+      }
+      ranges += __shfl_xor_sync(0xFFFFFFFFu, ranges, d);
+    }
+    const long long total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    const long long all_units = static_cast<long long>(__shfl_sync(0xFFFFFFFFu, lens, 31)) * p.kv_heads;
+    ctas = static_cast<int>(min(static_cast<long long>(most), ranges));
+    if (static_cast<int>(blockIdx.x) >= ctas) return false;
+    long long bound[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long u = range_begin(total, blockIdx.x + e, ctas);
+      const uint32_t ended = __popc(__ballot_sync(0xFFFFFFFFu, sum <= u));   // tiles that end before u: it is in the next
+      bound[e] = all_units;
+      if (ended >= static_cast<uint32_t>(n)) continue;   // the last range's end
+      const int its = __shfl_sync(0xFFFFFFFFu, len, ended), before = __shfl_sync(0xFFFFFFFFu, lens - len, ended);
+      const long long off = u - __shfl_sync(0xFFFFFFFFu, sum - cost, ended);
+      const int head = off <= 0x7FFFFFFFLL ? static_cast<int>(off) / (its + kItemCost) : static_cast<int>(off / (its + kItemCost));
+      const long long start = u - off + static_cast<long long>(head) * (its + kItemCost);
+      int lo = static_cast<int>(u - start);
+      lo = its <= kWhole ? (2 * lo < its + kItemCost ? 0 : its) : max(0, lo - kItemCost);
+      bound[e] = static_cast<long long>(before) * p.kv_heads + static_cast<long long>(head) * its + lo;
+      if (tid == static_cast<int>(ended)) {
+        if (e == 1) c.last_range = range_of(total, start + kItemCost + its - 1, ctas);
+        if (e == 0) {
+          c.first_b = b;
+          c.first_tile = tile;
+          c.first_head = head;
+          c.first_lo = lo;
+          c.first_req = kept[b];
+        }
+      }
+    }
+    __syncthreads();   // c; the room is the operands' again
+    count = static_cast<int>(bound[1] - bound[0]);
+    return count > 0;
+  }
   const int share = (n + kThreads - 1) / kThreads;
   const int x0 = min(tid * share, n), x1 = min(x0 + share, n);
   int from = 0, to = requests;   // the last request that begins at or before x0
@@ -650,6 +710,10 @@ __device__ __forceinline__ void store_row(__half* dst, const uint32_t (&a)[N], f
   }
 }
 
+// Where four columns of a row lie in a slot of a call with prefixes: eight columns of all 128 rows
+// after one another, so that the warp that takes a row later reads whole sectors.
+__device__ __forceinline__ size_t shared_quad(int quad, int r) { return static_cast<size_t>(quad >> 1) * (2 * kTile) + 2 * r + (quad & 1); }
+
 // Columns of a row's sums.
 template <int N>
 __device__ __forceinline__ void store_sums(float* dst, const uint32_t (&a)[N]) {
@@ -706,7 +770,8 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
       } else {
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
-          __stcg(reinterpret_cast<float4*>(slot) + static_cast<size_t>(quad0 + 8 * ch + e / 4) * kTile + r,
+          __stcg(reinterpret_cast<float4*>(slot) + (SHARED ? shared_quad(quad0 + 8 * ch + e / 4, r)
+                                                           : static_cast<size_t>(quad0 + 8 * ch + e / 4) * kTile + r),
                  make_float4(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])));
       }
     }
@@ -1173,6 +1238,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   constexpr int kSmem = Cfg<D>::kTiles + static_cast<int>(sizeof(Control));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
+  static_assert(Cfg<D>::kTiles >= 12 * kListed + 16 + (sizeof(Req) + 8) * kListed + 8, "room for what is kept of them");
   static std::atomic<unsigned long long> allowed{0};
   if (!allow_smem(prompt_kernel<D, SHARED>, kSmem, allowed)) return EXL3_ERR_CUDA;
   const int ctas = prompt_ctas();

@@ -92,7 +92,11 @@ __device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq -
 // falls into it moves to its nearer end.  Measured on 1 to 200 requests of 300 to
 // 131 K keys; with an item counted as one unit 200 requests of up to 600 keys took
 // 45 us, with four 35; with kWhole 24 a single request of 517 keys 10.2, with 12 8.7.
+// With two tiles of 8 rows an item costs as much again (calls with prefixes, whose ranges hold
+// many short items: 40 requests of up to 4 tokens 71.5 us, so 75).
 constexpr int kItemCost = kStepItemCost;
+template <int NT, bool SHARED>
+constexpr int item_cost() { return SHARED ? kStepItemCost * NT : kItemCost; }
 constexpr int kWhole = 12;
 // Units that are worth a range of their own: with 8 in place of 4 33 requests of up to
 // 2011 keys took 12.1 us in place of 11.4, 8 of 1024 11.8 and not 11.0, but one of 2000 10.3
@@ -100,11 +104,11 @@ constexpr int kWhole = 12;
 constexpr int kLeast = 4;
 
 // What a request's items cost together, and the ranges that they are worth.
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 __device__ __forceinline__ void req_cost(const AttnParams& p, const Req& r, long long& cost, long long& ranges) {
   const int blocks = req_blocks<D>(r);
   const long long items = static_cast<long long>(req_tiles<NT>(r)) * p.kv_heads;
-  cost += items * (blocks + kItemCost);
+  cost += items * (blocks + item_cost<NT, SHARED>());
   ranges += items * (blocks <= kWhole ? 1 : (blocks + kLeast - 1) / kLeast);
 }
 
@@ -115,17 +119,18 @@ struct Edge {
 };
 
 // The boundary at cost u, in request b, whose items begin at cost `before`.
-template <int D>
+template <int D, int NT, bool SHARED>
 __device__ __forceinline__ Edge edge_at(const Req& r, int b, long long u, long long before, long long total, int ctas) {
+  constexpr int kCost = item_cost<NT, SHARED>();
   const int blocks = req_blocks<D>(r);
-  const int each = blocks + kItemCost;
+  const int each = blocks + kCost;
   Edge e;
   e.b = b;
   e.item = static_cast<int>((u - before) / each);
   const long long start = before + static_cast<long long>(e.item) * each;
   const int off = static_cast<int>(u - start);
-  e.lo = blocks <= kWhole ? (2 * off < each ? 0 : blocks) : max(0, off - kItemCost);
-  e.c0 = range_of(total, start + kItemCost, ctas);
+  e.lo = blocks <= kWhole ? (2 * off < each ? 0 : blocks) : max(0, off - kCost);
+  e.c0 = range_of(total, start + kCost, ctas);
   e.c1 = range_of(total, start + each - 1, ctas);
   return e;
 }
@@ -212,7 +217,10 @@ struct Shared {
 
 // Calls with prefixes: requests and groups whose lists are copied behind that.
 constexpr int kListed = 256;
-constexpr size_t kListedBytes = sizeof(int32_t) * (2 * kListed + 2);
+constexpr size_t kListedBytes = sizeof(int32_t) * (2 * kListed + 4);   // whole 16 bytes
+// Of up to a request a thread what it has found out is kept behind that.
+constexpr int kKept = 128;
+constexpr size_t kSharedBytes = kListedBytes + sizeof(Req) * kKept;
 
 // The end of a block.  Beside the many-rows kernel this one is not done before that is, so
 // that what follows need wait for this one only.
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     if constexpr (SHARED) r = load_lanes(p); else r = load_from<SHARED>(p, lists, lane);
     lanes = r;
     long long cost = 0, ranges = 0;
-    req_cost<D, NT>(p, r, cost, ranges);
+    req_cost<D, NT, SHARED>(p, r, cost, ranges);
     long long inc = cost;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       q.seq = __shfl_sync(0xFFFFFFFFu, r.seq - r.k0, b & 31);
       const long long before = __shfl_sync(0xFFFFFFFFu, inc - cost, b & 31);
       Edge x{count, 0, 0, 0, 0};
-      if (b < 32) x = edge_at<D>(q, b, u, before, total, ctas);
+      if (b < 32) x = edge_at<D, NT, SHARED>(q, b, u, before, total, ctas);
       if (e == 0) from = x; else to = x;
     }
   } else {
@@ -374,12 +382,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const int b0 = min(tid * per, count), b1 = min(b0 + per, count);
     long long mine = 0, ranges = 0;
     Costs costs{0.f, 0.f};
-    Req only;   // this thread's request, if it has one at most
+    Req* kept = reinterpret_cast<Req*>(smem_raw + sizeof(Shared<D, NT>) + kListedBytes);
+    static_assert(kThreads <= kKept && sizeof(Shared<D, NT>) % 16 == 0, "room for a request a thread");
     for (int b = b0; b < b1; ++b) {
       const Req r = load_from<SHARED>(p, lists, b);
-      req_cost<D, NT>(p, r, mine, ranges);
+      req_cost<D, NT, SHARED>(p, r, mine, ranges);
       if constexpr (SHARED) {
-        only = r;
+        if (per == 1) kept[b] = r;
         const Costs c = costs_of<D>(p, r);
         costs.x += c.x;
         costs.y += c.y;
@@ -426,12 +435,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const long long u[2] = {range_begin(total, cta, ctas), range_begin(total, cta + 1, ctas)};
     if (u[1] >= before && u[0] < before + mine) {
       for (int b = b0; b < b1; ++b) {
-        const Req r = SHARED && per == 1 ? only : load_from<SHARED>(p, lists, b);
+        const Req r = SHARED && per == 1 ? kept[b] : load_from<SHARED>(p, lists, b);
         long long n = 0, unused = 0;
-        req_cost<D, NT>(p, r, n, unused);
+        req_cost<D, NT, SHARED>(p, r, n, unused);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          if (u[e] >= before && u[e] < before + n) sh.edge[e] = edge_at<D>(r, b, u[e], before, total, ctas);
+          if (u[e] >= before && u[e] < before + n) sh.edge[e] = edge_at<D, NT, SHARED>(r, b, u[e], before, total, ctas);
         before += n;
       }
     }
@@ -439,7 +448,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     from = sh.edge[0];
     to = sh.edge[1];
     first = from.b;
-    lanes = load_from<SHARED>(p, lists, first + lane);
+    if (SHARED && per == 1)
+      lanes = first + lane < count ? kept[first + lane] : Req{0, 0, 0, 0, 0, 0, 0, 0};
+    else
+      lanes = load_from<SHARED>(p, lists, first + lane);
   }
   Walker<D, NT, SHARED> w(p, from, to, first, lanes);
 
@@ -874,7 +886,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
 template <int D, int NT, bool SHARED>
 exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  const size_t smem = sizeof(Shared<D, NT>) + (SHARED ? kListedBytes : 0);
+  const size_t smem = sizeof(Shared<D, NT>) + (SHARED ? kSharedBytes : 0);
   static std::atomic<unsigned long long> allowed{0};
   if (!allow_smem(step_kernel<D, NT, SHARED>, smem, allowed)) return EXL3_ERR_CUDA;
   int ctas = device_sm_count() * C::kCtasPerSm;
