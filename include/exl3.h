@@ -734,13 +734,15 @@ exl3_status exl3_attention(const exl3_kv_cache *cache, const exl3_half *q, long 
  *       from the pages of the group's first request that holds them all; where the
  *       pages of the others hold something else, the result is that of neither.
  *       A request that holds fewer cached tokens than that, and one that is alone
- *       in its group, is computed from its own pages throughout.
+ *       in its group, is computed from its own pages throughout, and so are all
+ *       where the tables can hold so little (40 or 160 MB of keys and values) that
+ *       reading it once for each request takes no longer.
  *   max_group: the most new tokens that the requests of a group bring together; like
  *       max_new it picks the kernels and sizes the workspace.
  *   workspace: exl3_attention_shared_workspace_bytes of at least these sizes, under
  *       exl3_attention's rules; 0 for sizes that a call would refuse.
  * All else, the precision and the errors as exl3_attention; EXL3_ERR_BATCH also for
- * groups < 0, requests + groups above EXL3_MAX_REQUESTS and max_group < 1.  Two to four
+ * groups < 0, requests + groups above EXL3_MAX_REQUESTS and max_group < 1.  One to three
  * launches.
  */
 size_t exl3_attention_shared_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_new,

@@ -54,7 +54,7 @@ def widened(x):
     """The table with columns that no request reaches: what it could hold is worth sharing, so that the kernels for that run."""
     n, width = x["block_table"].shape
     page_bytes = 2 * x["k"][0].size
-    wide = np.full((n, max(width, -(-70_000_000 // (n * page_bytes)))), 2 ** 30, np.int32)
+    wide = np.full((n, max(width, -(-200_000_000 // (n * page_bytes)))), 2 ** 30, np.int32)
     wide[:, :width] = x["block_table"]
     return wide
 

@@ -111,8 +111,12 @@ exl3_status prepare(AttnParams& p, const exl3_kv_cache* cache, const exl3_half* 
   return EXL3_OK;
 }
 
-// Bytes of keys and values below which a call does not look for shared ones.
-constexpr double kWorthSharing = 64e6;
+// Bytes of keys and values that the tables can hold, up to which a call does not look for
+// shared ones: what it would save is soon read, and what it takes besides are a second kernel, or
+// two.  One: 8 requests behind 2011 tokens (38 MB) 14.7 us, 14.5 without; behind 3000 (54 MB) 14.8 and
+// 16.2; behind 8000 20.3 and 26.9.  Two: 64 requests behind 500 tokens (107 MB) 29.3 and 22.9, behind
+// 1000 (172 MB) 30.1 and 32.0; 16 behind 1000 (43 MB) 25.4 and 15.0.
+constexpr double kWorthOne = 40e6, kWorthBoth = 160e6;
 
 bool few_rows(int tokens, int group) { return static_cast<long long>(tokens) * group <= kStepRows; }
 
@@ -136,31 +140,35 @@ SharedLayout shared_layout(int q_heads, int kv_heads, int head_dim, int max_new,
 }
 
 // A row's result from its sums over the prefix and over its own keys, either of which may lie
-// in parts, one for each range that the item was spread over.  A warp takes a row; the
-// parts come in the order of the keys, m and l of 32 at a time, a part a lane, and the
-// sums in turn, a row's columns over the lanes.  What a row needs besides the other
-// kernels have left beside its sums: finding its request anew took 1.5 us.  Rows of no
-// request are left alone.
-constexpr int kMergeThreads = 256;
-constexpr int kAhead = 8;   // parts whose sums are on their way
+// in parts, one for each range that the item was spread over.  A warp takes 64 columns of
+// four neighbouring rows (of the heads of one key/value head), eight lanes a row: whole
+// sectors of either kernel's slots, the many-rows one's, four columns of all rows after one another, and
+// the other's, row after row.  (A warp a row read half sectors of the former: 64 requests behind 32000
+// tokens 70 us.)  The parts come in the order of the keys, eight at a time, m and l a part a
+// lane.  What a row needs besides the other kernels have left beside its sums: finding
+// its request anew took 1.5 us.  Rows of no request are left alone.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeRows = 4;
+constexpr int kMergeLanes = 32 / kMergeRows;   // of a row; parts at a time
 
-// A row's sums over its prefix or its own keys: of part i this lane's columns lie at x + slot *
-// max(2 i - 1, 0) floats, the row's m and l in the same way.
+// A row's sums over its prefix or its own keys: of part i columns 0..3 lie at x + slot *
+// max(2 i - 1, 0) floats, the others four by four `step` floats apart, m and l like x.
 struct Parts {
   const float *x, *m;
-  int count, slot, to_l;
+  int count, slot, step, to_l;
 };
 
 template <int D>
-__device__ __forceinline__ Parts parts_of(const AttnParams& p, bool own, uint32_t code, bool any, size_t at, long long row, int col) {
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, bool own, uint32_t code, bool any, size_t at, long long row) {
   const int c = static_cast<int>(min(code, static_cast<uint32_t>(kMaxCtas + kMaxPromptCtas))) - 1;
   Parts x;
   x.count = any ? 1 : 0;
   x.slot = 0;
+  x.step = 4;
   x.to_l = 1;
   if (c < 0) {
     const size_t part = (own ? static_cast<size_t>(p.tokens) * p.q_heads : 0) + at;
-    x.x = p.part + part * D + col;
+    x.x = p.part + part * D;
     x.m = &p.part_ml[part].x;
     return x;
   }
@@ -173,12 +181,13 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, bool own, uint32_
   x.slot = rows * (D + 2);
   const float* slot = p.partial + (step ? 0 : 2 * kMaxCtas * step_slot_floats(D)) + static_cast<size_t>(2 * range + 1) * x.slot;
   if (step) {
-    x.x = slot + in * D + col;
+    x.x = slot + in * D;
     x.m = slot + rows * D + in;
     x.to_l = rows;
   } else {
     slot += (in >> 7) * (prompt_slot_floats(D) / 2);
-    x.x = slot + (col >> 3) * 1024 + (in & 127) * 8 + (col & 7);
+    x.x = slot + (in & 127) * 4;
+    x.step = 4 * 128;
     x.m = slot + D * 128 + (in & 127);
     x.to_l = 128;
   }
@@ -187,94 +196,94 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, bool own, uint32_
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kCols = D / 32;   // of a lane
-  const int lane = threadIdx.x & 31;
-  const size_t at = static_cast<size_t>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);   // [token][head]
-  const long long t = static_cast<long long>(at / p.q_heads);
-  const int h = static_cast<int>(at - static_cast<size_t>(t) * p.q_heads);
-  const long long row = t * p.group + h % p.group;
+  constexpr int kHalves = D / 64;   // warps of a row
+  const int lane = threadIdx.x & 31, in_row = lane % kMergeLanes;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int half = static_cast<int>(unit % kHalves);
+  const long long row = unit / kHalves * kMergeRows + lane / kMergeLanes;   // token * group + head of the group
+  const long long t = row / p.group;
+  const int h = static_cast<int>(blockIdx.y) * p.group + static_cast<int>(row - t * p.group);
+  const size_t at = static_cast<size_t>(t) * p.q_heads + h;
   // the requests' tokens: all between the first one's and the last one's
   const Lists lists(p);
-  const int begin = first_token(p, lists, 0), end = first_token(p, lists, p.requests);
-  if (t < begin || t >= end) return;
+  const bool live = t >= first_token(p, lists, 0) && t < first_token(p, lists, p.requests);
+  if (!__any_sync(0xFFFFFFFFu, live)) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t flag = __ldcg(p.flag + at), where = __ldcg(p.where + at);
+  const uint32_t flag = live ? __ldcg(p.flag + at) : 0u, where = live ? __ldcg(p.where + at) : 0u;
   const bool sees = (flag & kSees) != 0u;
-  const Parts a = parts_of<D>(p, false, where, (flag & kHasPrefix) != 0u, at, row, kCols * lane);
-  const Parts b = parts_of<D>(p, true, flag >> 2, true, at, row, kCols * lane);
+  const Parts a = parts_of<D>(p, false, where, live && (flag & kHasPrefix) != 0u, at, row);
+  const Parts b = parts_of<D>(p, true, flag >> 2, live, at, row);
   const int parts = a.count + b.count;
+  const int most = __reduce_max_sync(0xFFFFFFFFu, parts);
+  const int quad = half * 16 + in_row;   // and quad + 8
   float top = -INFINITY, sum = 0.f;
-  float acc[kCols] = {};
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float v[kAhead][kCols];
-    auto fetch = [&](int j) {
+  float4 acc[2] = {};
+#pragma unroll 1
+  for (int i0 = 0; i0 < most; i0 += kMergeLanes) {
+    float4 v[kMergeLanes][2];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int n = i0 + j + i, k = n < a.count ? n : n - a.count;
-        const float* from = (n < a.count ? a.x : b.x) + static_cast<size_t>(n < a.count ? a.slot : b.slot) * max(2 * k - 1, 0);
+    for (int i = 0; i < kMergeLanes; ++i) {
+      const int n = i0 + i;
+      const bool first = n < a.count;
+      const float* from = (first ? a.x : b.x) + static_cast<size_t>(first ? a.slot : b.slot) * max(2 * (first ? n : n - a.count) - 1, 0);
+      const int step = first ? a.step : b.step;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) v[i][e] = 0.f;
-        if (n < parts) {
-          if constexpr (kCols == 4)
-            *reinterpret_cast<float4*>(v[i]) = __ldcg(reinterpret_cast<const float4*>(from));
-          else
-            *reinterpret_cast<float2*>(v[i]) = __ldcg(reinterpret_cast<const float2*>(from));
-        }
-      }
-    };
-    fetch(0);
+      for (int e = 0; e < 2; ++e)
+        v[i][e] = n < parts ? __ldcg(reinterpret_cast<const float4*>(from + static_cast<size_t>(quad + 8 * e) * step))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float m = -INFINITY, l = 0.f;
-    {
-      const int n = i0 + lane, k = n < a.count ? n : n - a.count;
-      if (n < parts) {
-        const float* from = (n < a.count ? a.m : b.m) + static_cast<size_t>(n < a.count ? a.slot : b.slot) * max(2 * k - 1, 0);
-        m = __ldcg(from);
-        l = __ldcg(from + (n < a.count ? a.to_l : b.to_l));
-      }
+    const int n = i0 + in_row;
+    if (n < parts) {
+      const bool first = n < a.count;
+      const float* from = (first ? a.m : b.m) + static_cast<size_t>(first ? a.slot : b.slot) * max(2 * (first ? n : n - a.count) - 1, 0);
+      m = __ldcg(from);
+      l = __ldcg(from + (first ? a.to_l : b.to_l));
     }
     float next = fmaxf(top, m);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, d));
+    for (int d = 1; d < kMergeLanes; d <<= 1) next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, d));
     const float base = next == -INFINITY ? 0.f : next;
     const float f = ex2(m - base), keep = ex2(top - base);
     float s = l * f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    for (int d = 1; d < kMergeLanes; d <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
     sum = sum * keep + s;
     top = next;
 #pragma unroll
-    for (int e = 0; e < kCols; ++e) acc[e] *= keep;
-#pragma unroll 1
-    for (int j = 0; j < 32 && i0 + j < parts; j += kAhead) {
-      if (j > 0) fetch(j);
+    for (int e = 0; e < 2; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const float w = __shfl_sync(0xFFFFFFFFu, f, j + i);
-        if (i0 + j + i < parts) {
+    for (int i = 0; i < kMergeLanes; ++i) {
+      const float w = __shfl_sync(0xFFFFFFFFu, f, i, kMergeLanes);
+      if (i0 + i < parts) {
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
-        }
+        for (int e = 0; e < 2; ++e)
+          acc[e] = make_float4(fmaf(v[i][e].x, w, acc[e].x), fmaf(v[i][e].y, w, acc[e].y), fmaf(v[i][e].z, w, acc[e].z),
+                               fmaf(v[i][e].w, w, acc[e].w));
       }
     }
   }
+  if (!live) return;
   const float inv = inverse_sum(sum, sees);
-  __half* to = p.out + t * p.out_stride + static_cast<size_t>(h) * D + kCols * lane;
+  __half* to = p.out + t * p.out_stride + static_cast<size_t>(h) * D;
 #pragma unroll
-  for (int e = 0; e < kCols; e += 2) {
-    const __half2 o = __floats2half2_rn(sees ? acc[e] * inv : 0.f, sees ? acc[e + 1] * inv : 0.f);
-    reinterpret_cast<__half2*>(to)[e / 2] = o;
+  for (int e = 0; e < 2; ++e) {
+    const __half2 x = __floats2half2_rn(sees ? acc[e].x * inv : 0.f, sees ? acc[e].y * inv : 0.f);
+    const __half2 y = __floats2half2_rn(sees ? acc[e].z * inv : 0.f, sees ? acc[e].w * inv : 0.f);
+    *reinterpret_cast<uint2*>(to + 4 * (quad + 8 * e)) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
-  if (p.lse != nullptr && lane == 0) p.lse[at] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
+  if (p.lse != nullptr && in_row == 0 && half == 0) p.lse[at] = sees ? kLn2 * (top == -INFINITY ? 0.f : top) + logf(sum) : -INFINITY;
 }
 
 template <int D>
 exl3_status launch_merge(const AttnParams& p, cudaStream_t cs) {
-  const long long rows = static_cast<long long>(p.tokens) * p.q_heads;
+  const long long rows = static_cast<long long>(p.tokens) * p.group;
+  const long long warps = (rows + kMergeRows - 1) / kMergeRows * (D / 64);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)), static_cast<unsigned>(p.kv_heads));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = cs;
   cfg.attrs = attr;
@@ -348,16 +357,13 @@ extern "C" exl3_status exl3_attention_shared(const exl3_kv_cache* cache, const e
   p.part = reinterpret_cast<float*>(ws + at.part);
   p.part_ml = reinterpret_cast<float2*>(ws + at.ml);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  // Where all that the tables can hold is soon read, it is not worth the second kernel: 8
-  // requests behind 2011 tokens (38 MB) 14 us, so 18; two behind 4000 (17 MB) 14 and 18; 8
-  // behind 16000 (267 MB) 43 us, so 35.
-  if (static_cast<double>(requests) * static_cast<double>(p.most) * cache->kv_heads * cache->head_dim * 2 <= attn::kWorthSharing)
-    return exl3_attention(cache, q, q_stride, q_heads, q_start, seq_len, requests, tokens, max_new, block_table, table_stride, scale,
-                          out, out_stride, lse, workspace, workspace_bytes, stream);
   // The few-rows kernel takes the requests if they all have few rows, and the prefixes that
   // have few; the other kernel the rest, first, so that its blocks begin on SMs of their own.
   const bool own_few = attn::few_rows(max_new, p.group), prefix_few = attn::few_rows(max_group, p.group);
   p.both = !own_few || !prefix_few;
+  if (2.0 * requests * static_cast<double>(p.most) * cache->kv_heads * cache->head_dim <= (p.both ? attn::kWorthBoth : attn::kWorthOne))
+    return exl3_attention(cache, q, q_stride, q_heads, q_start, seq_len, requests, tokens, max_new, block_table, table_stride, scale,
+                          out, out_stride, lse, workspace, workspace_bytes, stream);
   p.align = own_few ? attn::step_unit(cache->head_dim) : attn::kPromptUnit;
   p.rows_hi = own_few ? 0x7FFFFFFF : attn::kStepRows;
   p.prefix_hi = prefix_few ? 0x7FFFFFFF : attn::kStepRows;

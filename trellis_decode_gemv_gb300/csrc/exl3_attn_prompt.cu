@@ -710,10 +710,6 @@ __device__ __forceinline__ void store_row(__half* dst, const uint32_t (&a)[N], f
   }
 }
 
-// Where four columns of a row lie in a slot of a call with prefixes: eight columns of all 128 rows
-// after one another, so that the warp that takes a row later reads whole sectors.
-__device__ __forceinline__ size_t shared_quad(int quad, int r) { return static_cast<size_t>(quad >> 1) * (2 * kTile) + 2 * r + (quad & 1); }
-
 // Columns of a row's sums.
 template <int N>
 __device__ __forceinline__ void store_sums(float* dst, const uint32_t (&a)[N]) {
@@ -770,8 +766,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
       } else {
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
-          __stcg(reinterpret_cast<float4*>(slot) + (SHARED ? shared_quad(quad0 + 8 * ch + e / 4, r)
-                                                           : static_cast<size_t>(quad0 + 8 * ch + e / 4) * kTile + r),
+          __stcg(reinterpret_cast<float4*>(slot) + static_cast<size_t>(quad0 + 8 * ch + e / 4) * kTile + r,
                  make_float4(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])));
       }
     }
