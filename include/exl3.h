@@ -547,9 +547,10 @@ exl3_status exl3_rms_norm(const exl3_half *x, long long x_stride, const exl3_hal
 /**
  * The same for the int8 projections (exl3_gemm_i8) that read y: for each of
  * `outs` (1 to EXL3_MAX_NORM_OUTS) the signs of its input side, the blockwise
- * transform and the quantizer of exl3_quantize_act, all on binary32 values:
+ * transform and int8 with a scale as from exl3_quantize_act, all on binary32 values:
  *   z = Hb(signs[o] (.) y)  (z = y where signs[o] is NULL),
- *   qscale = max|z| / 127 over a block of 128,  q = nearest integer to z / qscale.
+ *   qscale = max|z| / 127 over a block of 128,  q = nearest integer to z / qscale
+ * (next to a tie either integer: the quotient is good to 2^-21 of its value).
  * A block of zeros has scale 0 and q 0, one that holds an infinity or a NaN scale
  * NaN and q 0.
  *   signs   host array of `outs` device pointers (length n each, or NULL)

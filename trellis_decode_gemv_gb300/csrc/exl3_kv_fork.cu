@@ -14,8 +14,10 @@ namespace cg = cooperative_groups;
 // ---- fork ----------------------------------------------------------------------
 
 constexpr int kForkThreads = 1024;
+constexpr int kFewThreads = 256;   // up to as many rows and requests
 constexpr int kForkCluster = 8;
 constexpr int kMostClusters = 16;
+constexpr int kAtOnce = 4;   // entries of a table that a lane has on their way
 constexpr int kNobody = 0x7FFFFFFF;
 
 struct ForkParams {
@@ -32,6 +34,7 @@ struct ForkParams {
   int32_t* copy_tokens;
   unsigned char* gone;   // [pages rounded up to 16] held before, by a request that no row continues
   unsigned char* kept;   // [the same] held after
+  uint32_t* arrived;     // clusters whose bytes are set
   int rows, requests, page_shift, pages, capacity, stride;
 };
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ int fork_scan(int v, int* warp_sums, int& total) {
   __syncthreads();   // the sums' readers of the scan before
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  const int sums = warp_inclusive(warp_sums[lane]);
+  const int sums = warp_inclusive(lane < static_cast<int>(blockDim.x >> 5) ? warp_sums[lane] : 0);
   total = __shfl_sync(0xFFFFFFFFu, sums, 31);
   const int before = __shfl_sync(0xFFFFFFFFu, sums, (warp + 31) & 31);
   return inc - v + (warp > 0 ? before : 0);
@@ -64,16 +67,24 @@ __device__ __forceinline__ int tokens_of(const ForkParams& p, int b) {
   return static_cast<int>(min(static_cast<long long>(max(p.ctx_len[b], 0)), most));
 }
 
+// Place `by` <= cap behind `head` < cap in the ring.
+__device__ __forceinline__ int wrapped(int head, int by, int cap) {
+  const uint32_t at = static_cast<uint32_t>(head) + static_cast<uint32_t>(by);
+  return static_cast<int>(at >= static_cast<uint32_t>(cap) ? at - static_cast<uint32_t>(cap) : at);
+}
+
 __device__ __forceinline__ int flags_of(uint32_t gone, uint32_t kept) { return __popc(gone & ~kept & 0x01010101u); }
 
 // One launch.  Every block goes over all rows for itself (the first row of each
 // parent, then the ranks of the rows that need a page: a few KB that stay in
 // L2), so that the rows' tables, which are most of the bytes, need no hand-over.
-// The first cluster finds the pages that go back besides: each entry of the old table sets a
-// byte for its page (held by a request that ends, or by one that goes on), and
-// after a barrier of the cluster its blocks count, and append in ascending order,
-// the pages with the one and not the other.  Plain stores of the same byte need no
-// atomics; the bytes are zero again when the call ends.
+// Where a request ends, each entry of the old table sets a byte for its page (held by a
+// request that ends, or by one that goes on), and the cluster of blocks that is done last
+// counts, and appends in ascending order, the pages with the one and not the other, a range of
+// them for each of its blocks; none waits for another cluster.  Plain stores of the same byte need
+// no atomics; the bytes are zero again when the call ends.  16 requests of up to 125 pages
+// into 64 rows take 7 us, the latency of a dozen dependent steps; 500 of up to 500 pages 25
+// (65 where one block appends what all have marked, 33 with one cluster for all of it).
 __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1, 1)
     fork_kernel(const __grid_constant__ ForkParams p) {
   extern __shared__ int32_t fork_smem[];
@@ -81,6 +92,8 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
   int32_t* rank = fork_smem + p.requests;    // [rows] pages taken before it, -1: it needs none
   __shared__ int warp_sums[kForkThreads / 32];
   __shared__ int counts[kForkCluster];       // pages that go back, of the cluster's blocks
+  __shared__ int last;
+  const int threads = static_cast<int>(blockDim.x);
   const int tid = threadIdx.x;
   const int lane = tid & 31;
   const int cap = p.capacity;
@@ -88,14 +101,14 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
   const int count = min(max(p.state[1], 0), cap);
   const int size = 1 << p.page_shift;
 
-  for (int b = tid; b < p.requests; b += kForkThreads) first[b] = kNobody;
+  for (int b = tid; b < p.requests; b += threads) first[b] = kNobody;
   __syncthreads();
-  for (int i = tid; i < p.rows; i += kForkThreads) {
+  for (int i = tid; i < p.rows; i += threads) {
     const int b = p.parent[i];
     if (b >= 0 && b < p.requests) atomicMin(&first[b], i);
   }
   __syncthreads();
-  const int per = (p.rows + kForkThreads - 1) / kForkThreads;
+  const int per = (p.rows + threads - 1) / threads;
   const int i0 = min(tid * per, p.rows), i1 = min(i0 + per, p.rows);
   int mine = 0, need_total;
   for (int i = i0; i < i1; ++i) {
@@ -109,27 +122,30 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
     if (rank[i] >= 0) rank[i] += before;
   // whether any request that holds pages ends: the same answer in every block
   bool ends = false;
-  for (int b = tid; b < p.requests; b += kForkThreads) ends |= first[b] == kNobody && tokens_of(p, b) > 0;
+  for (int b = tid; b < p.requests; b += threads) ends |= first[b] == kNobody && tokens_of(p, b) > 0;
   ends = __syncthreads_or(ends) != 0;
   const int taken = min(need_total, count);
 
   // rows of the new table, a warp each
-  const int warps = static_cast<int>(gridDim.x) * (kForkThreads / 32);
-  const bool release = ends && blockIdx.x < kForkCluster;
-  for (int i = static_cast<int>(blockIdx.x) * (kForkThreads / 32) + (tid >> 5); i < p.rows; i += warps) {
+  const int warps = static_cast<int>(gridDim.x) * (threads / 32);
+  const int warp = static_cast<int>(blockIdx.x) * (threads / 32) + (tid >> 5);
+  for (int i = warp; i < p.rows; i += warps) {
     const int b = p.parent[i];
     const bool live = b >= 0 && b < p.requests;
     const int r = rank[i];
     const int c = live && r < count ? tokens_of(p, b) : 0;
     const int full = c >> p.page_shift, part = c & (size - 1);
     const int32_t* old = p.table + static_cast<size_t>(live ? b : 0) * p.stride;
-    const int fresh = r >= 0 && c > 0 ? p.ring[(head + r) % cap] : -1;   // a rank below `count`: cap is not 0
+    const int fresh = r >= 0 && c > 0 ? p.ring[wrapped(head, r, cap)] : -1;   // a rank below `count`: cap is not 0
     int32_t* to = p.table_out + static_cast<size_t>(i) * p.stride;
-    for (int j = lane; j < p.stride; j += 32) {
-      int v = -1;
-      if (j < full || (j == full && part > 0 && fresh < 0)) v = old[j];
-      if (j == full && part > 0 && r >= 0) v = fresh;
-      to[j] = v;
+    const int copied = full + (part > 0 && r < 0 ? 1 : 0);
+    for (int j = lane; j < p.stride; j += 32 * kAtOnce) {
+      int v[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) v[k] = j + 32 * k < copied ? old[j + 32 * k] : -1;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (j + 32 * k < p.stride) to[j + 32 * k] = j + 32 * k == full && r >= 0 && c > 0 ? fresh : v[k];
     }
     if (lane == 0) {
       const bool copy = r >= 0 && c > 0;
@@ -139,36 +155,49 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
       p.copy_tokens[i] = copy ? part : 0;
     }
   }
-  if (blockIdx.x >= kForkCluster) return;   // whole clusters
 
   int back_total = 0;
-  if (release) {
-    cg::cluster_group cluster = cg::this_cluster();
-    const int me = static_cast<int>(blockIdx.x);
-    for (int b = me * (kForkThreads / 32) + (tid >> 5); b < p.requests; b += kForkCluster * (kForkThreads / 32)) {
+  if (ends) {
+    // (from the last warp on: the first ones have a row)
+    for (int b = warps - 1 - warp; b < p.requests; b += warps) {
       unsigned char* flags = first[b] == kNobody ? p.gone : p.kept;
       const int held = (tokens_of(p, b) + size - 1) >> p.page_shift;
       const int32_t* old = p.table + static_cast<size_t>(b) * p.stride;
-      for (int j = lane; j < held; j += 32) {
-        const int pg = old[j];
-        if (pg >= 0 && pg < p.pages) flags[pg] = 1;
+      for (int j = lane; j < held; j += 32 * kAtOnce) {
+        int v[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) v[k] = j + 32 * k < held ? old[j + 32 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if (v[k] >= 0 && v[k] < p.pages) flags[v[k]] = 1;
       }
     }
-    for (int i = me * kForkThreads + tid; i < taken; i += kForkCluster * kForkThreads) {
-      const int pg = p.ring[(head + i) % cap];
+    for (int i = static_cast<int>(blockIdx.x) * threads + tid; i < taken; i += static_cast<int>(gridDim.x) * threads) {
+      const int pg = p.ring[wrapped(head, i, cap)];
       if (pg >= 0 && pg < p.pages) p.kept[pg] = 1;
     }
+    cg::cluster_group cluster = cg::this_cluster();
+    const int me = static_cast<int>(cluster.block_rank());
     __threadfence();
     cluster.sync();
+    if (me == 0 && tid == 0) {
+      const int done = atomicAdd(p.arrived, 1u) == gridDim.x / kForkCluster - 1 ? 1 : 0;
+      if (done) *p.arrived = 0u;
+      for (int i = 0; i < kForkCluster; ++i) *cluster.map_shared_rank(&last, i) = done;
+    }
+    cluster.sync();
+    if (last == 0) return;
+    __threadfence();
     // the bytes in sixteens: a range of them for every block, and of that for every thread
     const int words = (p.pages - 1) / 16 + 1;
-    const int share = (words + kForkCluster - 1) / kForkCluster;
+    const int share = (words - 1) / kForkCluster + 1;
     const int w0 = min(me * share, words), w1 = min(w0 + share, words);
-    const int each = (w1 - w0 + kForkThreads - 1) / kForkThreads;
+    const int each = (w1 - w0 + threads - 1) / threads;
     const int a = min(w0 + tid * each, w1), e = min(a + each, w1);
     uint4* gone = reinterpret_cast<uint4*>(p.gone);
     uint4* kept = reinterpret_cast<uint4*>(p.kept);
     int found = 0, of_block;
+#pragma unroll 4
     for (int w = a; w < e; ++w) {
       const uint4 g = __ldcg(gone + w), k = __ldcg(kept + w);
       found += flags_of(g.x, k.x) + flags_of(g.y, k.y) + flags_of(g.z, k.z) + flags_of(g.w, k.w);
@@ -189,13 +218,13 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
       for (int i = 0; i < 4; ++i)
         for (uint32_t m = bits[i] & 0x01010101u; m != 0u; m &= m - 1, ++at)
           if (at < room)
-            p.ring[(static_cast<long long>(head) + count + at) % cap] = 16 * w + 4 * i + ((__ffs(static_cast<int>(m)) - 1) >> 3);
+            p.ring[wrapped(head, count + at, cap)] = 16 * w + 4 * i + ((__ffs(static_cast<int>(m)) - 1) >> 3);
       __stcg(gone + w, make_uint4(0u, 0u, 0u, 0u));
       __stcg(kept + w, make_uint4(0u, 0u, 0u, 0u));
     }
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.state_out[0] = cap > 0 ? static_cast<int32_t>((static_cast<long long>(head) + taken) % cap) : 0;
+  if (tid == 0 && (ends ? blockIdx.x % kForkCluster == 0 : blockIdx.x == 0)) {
+    p.state_out[0] = cap > 0 ? wrapped(head, taken, cap) : 0;
     p.state_out[1] = count - taken + min(back_total, cap - count);
     p.state_out[2] = need_total - taken;
   }
@@ -274,7 +303,7 @@ exl3_status launch_copy(const exl3_kv_cache* caches, int layers, const int32_t* 
 
 using namespace exl3;
 
-extern "C" size_t exl3_kv_fork_workspace_bytes(int pages) { return pages < 1 ? 0 : 2 * kv::fork_flags(pages); }
+extern "C" size_t exl3_kv_fork_workspace_bytes(int pages) { return pages < 1 ? 0 : 2 * kv::fork_flags(pages) + 16; }
 
 extern "C" exl3_status exl3_kv_fork(const int32_t* parent, int rows, const int32_t* ctx_len, int requests, int page_size,
                                     int pages, int32_t* free_pages, int free_capacity, const int32_t* free_state,
@@ -310,6 +339,7 @@ extern "C" exl3_status exl3_kv_fork(const int32_t* parent, int rows, const int32
   p.copy_tokens = copy_tokens;
   p.gone = static_cast<unsigned char*>(workspace);
   p.kept = p.gone + kv::fork_flags(pages);
+  p.arrived = reinterpret_cast<uint32_t*>(p.kept + kv::fork_flags(pages));
   p.rows = rows;
   p.requests = requests;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
@@ -319,11 +349,12 @@ extern "C" exl3_status exl3_kv_fork(const int32_t* parent, int rows, const int32
   const size_t smem = sizeof(int32_t) * (static_cast<size_t>(requests) + rows);
   static std::atomic<unsigned long long> allowed{0};
   if (smem > 47 * 1024 && !allow_smem(kv::fork_kernel, sizeof(int32_t) * 2 * EXL3_MAX_REQUESTS, allowed)) return EXL3_ERR_CUDA;
-  const long long entries = static_cast<long long>(rows) * table_stride;
-  const long long want = entries / (8LL * kv::kForkCluster * kv::kForkThreads);
-  const int clusters = want < 1 ? 1 : want > kv::kMostClusters ? kv::kMostClusters : static_cast<int>(want);
-  kv::fork_kernel<<<static_cast<unsigned>(clusters * kv::kForkCluster), kv::kForkThreads, smem,
-                    reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  // a warp for each row and each request
+  const int threads = rows <= kv::kFewThreads && requests <= kv::kFewThreads ? kv::kFewThreads : kv::kForkThreads;
+  const int warps = kv::kForkCluster * threads / 32;
+  const int want = (rows + requests + warps - 1) / warps;
+  const int clusters = want < 1 ? 1 : want > kv::kMostClusters ? kv::kMostClusters : want;
+  kv::fork_kernel<<<static_cast<unsigned>(clusters * kv::kForkCluster), threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return launch_status();
 }
 

@@ -60,28 +60,52 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The 128-point transform of the values of 16 lanes, 8 each in order.
-__device__ __forceinline__ void hadamard128(float (&f)[8], int lane) {
+// sqrt(128) times the 128-point transform of the values of 16 lanes, 8 each in order, two to a
+// register pair.  Instructions bound a large call with rotations, so: two values to an
+// addition, and shuffles whose sums are one fused operation.  (Exchanging half of the
+// registers halves the shuffles, but its selections cost more: 43 us where this takes 27, 2000 rows
+// of 4096 for three projections.)
+__device__ __forceinline__ void hadamard128(uint64_t (&f)[4], int lane) {
+  const uint64_t minus = pair(-1.f, -1.f);
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1)
+  for (int d = 1; d < 4; d <<= 1)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
       if ((i & d) == 0) {
-        const float a = f[i], b = f[i + d];
-        f[i] = a + b;
-        f[i + d] = a - b;
+        const uint64_t a = f[i], b = f[i + d];
+        f[i] = add2(a, b);
+        f[i + d] = fma2(b, minus, a);
       }
 #pragma unroll
-  for (int d = 1; d < 16; d <<= 1) {
-    const bool up = (lane & d) != 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_xor_sync(0xFFFFFFFFu, f[i], d);
-      f[i] = up ? o - f[i] : f[i] + o;
-    }
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpair(f[i], a, b);
+    f[i] = pair(a + b, a - b);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] *= 0.08838834764831845f;   // 1 / sqrt(128)
+  for (int d = 1; d < 16; d <<= 1) {
+    const float sign = (lane & d) != 0 ? -1.f : 1.f;
+    const uint64_t signs = pair(sign, sign);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unpair(f[i], a, b);
+      a = __shfl_xor_sync(0xFFFFFFFFu, a, d);
+      b = __shfl_xor_sync(0xFFFFFFFFu, b, d);
+      f[i] = fma2(f[i], signs, pair(a, b));
+    }
+  }
+}
+
+// The largest |value| of three, NaN if there is one.
+__device__ __forceinline__ float most3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // GROUP threads a row, ROWS rows a block, VECS vectors of eight values a thread.
@@ -119,7 +143,7 @@ __global__ void __launch_bounds__(most_threads<VECS, WARP>()) norm_kernel(const 
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[k][i] += g[i];
       const int v = at + k * group;
-      if (v < vecs && p.h != nullptr) *reinterpret_cast<uint4*>(p.h + row * p.n + 8 * v) = narrow8(f[k]);
+      if (v < vecs && p.h != nullptr && blockIdx.y == 0) *reinterpret_cast<uint4*>(p.h + row * p.n + 8 * v) = narrow8(f[k]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = fmaf(f[k][i], f[k][i], sum);
@@ -147,39 +171,47 @@ __global__ void __launch_bounds__(most_threads<VECS, WARP>()) norm_kernel(const 
   }
   if constexpr (I8) {
 #pragma unroll 1
-    for (int o = 0; o < p.outs; ++o) {
+    for (int o = blockIdx.y; o < p.outs; o += gridDim.y) {
       const __half* s = p.signs[o];
       const size_t to = static_cast<size_t>(o) * p.rows + row;
 #pragma unroll
       for (int k = 0; k < VECS; ++k) {
         const int v = at + k * group;   // 16 lanes of a block of 128 are all in the row or all past it
-        float z[8];
+        uint64_t z[4];
+        float unit = 1.f / 127.f;   // of the scale, for a largest value of 1
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = f[k][i];
+        for (int i = 0; i < 4; ++i) z[i] = pair(f[k][2 * i], f[k][2 * i + 1]);
         if (s != nullptr) {
           float g[8];
           widen8(v < vecs ? __ldg(reinterpret_cast<const uint4*>(s + 8 * v)) : make_uint4(0u, 0u, 0u, 0u), g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] *= g[i];
+          for (int i = 0; i < 4; ++i) z[i] = mul2(z[i], pair(g[2 * i], g[2 * i + 1]));
           hadamard128(z, lane);
+          unit = 0.08838834764831845f / 127.f;   // 1 / sqrt(128)
         }
-        // |z| as bits orders as numbers do, infinity and NaN above them
-        uint32_t top = 0;
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i) unpair(z[i], x[2 * i], x[2 * i + 1]);
+        // |z| as bits orders as numbers do, infinity and NaN above them
+        uint32_t top = __float_as_uint(most3(most3(x[0], x[1], x[2]), most3(x[3], x[4], x[5]), most3(x[6], x[7], 0.f)));
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         const bool bad = top >= 0x7F800000u;
-        const float scale = bad ? __int_as_float(0x7FC00000) : __fdiv_rn(__uint_as_float(top), 127.f);
-        uint32_t b[8];
+        const float most = __uint_as_float(top);
+        // (anything but 0 is far above 2^-120: the product of two binary16 numbers and a root)
+        const float inv = bad || !(most > 0x1p-120f) ? 0.f : __fdiv_rn(127.f, most);
+        const uint64_t by = pair(inv, inv), magic = pair(12582912.f, 12582912.f);   // 1.5 * 2^23: a sum's last bits are the integer
+        uint32_t q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          b[i] = bad || !(scale > 0.f) ? 0u : static_cast<uint32_t>(__float2int_rn(__fdiv_rn(z[i], scale)));
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t n = fma2(z[i], by, magic);
+          q[2 * i] = static_cast<uint32_t>(n);
+          q[2 * i + 1] = static_cast<uint32_t>(n >> 32);
+        }
         if (v < vecs) {
-          const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-          const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-          *reinterpret_cast<uint2*>(p.q + to * p.n + 8 * v) = make_uint2(lo, hi);
-          if ((lane & 15) == 0) p.qscale[to * (p.n >> 7) + (v >> 4)] = scale;
+          *reinterpret_cast<uint2*>(p.q + to * p.n + 8 * v) =
+              bad ? make_uint2(0u, 0u) : make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+          if ((lane & 15) == 0) p.qscale[to * (p.n >> 7) + (v >> 4)] = bad ? __int_as_float(0x7FC00000) : most * unit;
         }
       }
     }
@@ -188,7 +220,11 @@ __global__ void __launch_bounds__(most_threads<VECS, WARP>()) norm_kernel(const 
 
 template <int VECS, bool I8>
 exl3_status launch_block(const NormParams& p, int threads, cudaStream_t cs) {
-  norm_kernel<VECS, I8, false><<<static_cast<unsigned>(p.rows), threads, 0, cs>>>(p);
+  // few rows: the outputs side by side, the norm computed for each of them (not where one of
+  // them writes h over what the others read)
+  const bool apart = p.h == nullptr || (p.h != p.x && p.h != p.residual);
+  const unsigned outs = I8 && apart && static_cast<long long>(p.rows) * p.outs <= 2 * device_sm_count() ? p.outs : 1;
+  norm_kernel<VECS, I8, false><<<dim3(static_cast<unsigned>(p.rows), outs), threads, 0, cs>>>(p);
   return launch_status();
 }
 
