@@ -383,6 +383,7 @@ extern "C" exl3_status exl3_gemm_small(const uint32_t* codes, int K, int codeboo
   char* ws = static_cast<char*>(workspace);
   uint32_t* status = reinterpret_cast<uint32_t*>(ws) + m / kRowBlock;
   float* zacc = reinterpret_cast<float*>(ws + zacc_offset(m));
+  const size_t scratch = single_scratch_offset(m, n, workspace_bytes, need - bimg_offset(m, M));
   if (!use_shuffle(M)) {
     MvParams p{};
     p.count = 1;
@@ -393,8 +394,8 @@ extern "C" exl3_status exl3_gemm_small(const uint32_t* codes, int K, int codeboo
     L.codes = codes;
     L.x = a.x;
     L.s_in = a.s_in;
-    L.bimg = reinterpret_cast<const __half*>(ws + bimg_offset(m, M));
-    L.bsum = reinterpret_cast<const float*>(ws + bsum_offset(m, n, M));
+    L.bimg = reinterpret_cast<const __half*>(ws + scratch);
+    L.bsum = reinterpret_cast<const float*>(ws + scratch + (bsum_offset(m, n, M) - bimg_offset(m, M)));
     L.scales = a.scales;
     L.s_out = a.s_out;
     L.y = a.y;
@@ -406,7 +407,7 @@ extern "C" exl3_status exl3_gemm_small(const uint32_t* codes, int K, int codeboo
   }
   // x pairs of each batch chunk go where the tensor path keeps its operand
   // images (at least 32 n bytes, enough for 8 rows of n 32-bit pairs).
-  return run_shuffle(a, M, zacc, reinterpret_cast<uint32_t*>(ws + bimg_offset(m, M)), cs);
+  return run_shuffle(a, M, zacc, reinterpret_cast<uint32_t*>(ws + scratch), cs);
 }
 
 namespace {
@@ -717,11 +718,11 @@ namespace {
 
 // Fused prefill: x-tilde into operand-B images, then the dense kernel that
 // decodes its operand A from the codes in shared memory.
-exl3_status run_fused(const LayerArgs& a, int M, char* ws, cudaStream_t cs) {
+exl3_status run_fused(const LayerArgs& a, int M, char* ws, size_t ws_bytes, cudaStream_t cs) {
   uint32_t* status = reinterpret_cast<uint32_t*>(ws) + a.m / kRowBlock;
   float* zacc = reinterpret_cast<float*>(ws + zacc_offset(a.m));
-  __half* bimg = reinterpret_cast<__half*>(ws + dense_bimg_offset(a.m, M));
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(ws + dense_cnt_offset(a.m, a.n, M));
+  __half* bimg = reinterpret_cast<__half*>(ws + single_scratch_offset(a.m, a.n, ws_bytes, dense_scratch_bytes(a.m, a.n, M)));
+  uint32_t* cnt = reinterpret_cast<uint32_t*>(ws + single_cnt_offset(a.m, a.n, ws_bytes));
   const int nb = fused_nb(M);
   exl3_status st = launch_bimg(a.x, a.s_in, bimg, nullptr, M, nb, a.n, cs);
   if (st != EXL3_OK) return st;
@@ -733,12 +734,13 @@ exl3_status run_fused(const LayerArgs& a, int M, char* ws, cudaStream_t cs) {
 
 // Decode once, dense GEMM: W-hat into operand-A images, x-tilde into
 // operand-B images, then the dense kernel.
-exl3_status run_dense(const LayerArgs& a, int M, char* ws, cudaStream_t cs) {
+exl3_status run_dense(const LayerArgs& a, int M, char* ws, size_t ws_bytes, cudaStream_t cs) {
   uint32_t* status = reinterpret_cast<uint32_t*>(ws) + a.m / kRowBlock;
   float* zacc = reinterpret_cast<float*>(ws + zacc_offset(a.m));
-  __half* bimg = reinterpret_cast<__half*>(ws + dense_bimg_offset(a.m, M));
-  unsigned char* aimg = reinterpret_cast<unsigned char*>(ws + dense_aimg_offset(a.m, a.n, M));
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(ws + dense_cnt_offset(a.m, a.n, M));
+  char* scratch = ws + single_scratch_offset(a.m, a.n, ws_bytes, dense_scratch_bytes(a.m, a.n, M));
+  __half* bimg = reinterpret_cast<__half*>(scratch);
+  unsigned char* aimg = reinterpret_cast<unsigned char*>(scratch + dense_bimg_bytes(a.n, M));
+  uint32_t* cnt = reinterpret_cast<uint32_t*>(ws + single_cnt_offset(a.m, a.n, ws_bytes));
   exl3_status st = launch_decode_aimg(a.codes, a.K, a.codebook, a.m, a.n, aimg, cs);
   if (st != EXL3_OK) return st;
   const int nb = dense_nb(M);
@@ -783,7 +785,7 @@ extern "C" exl3_status exl3_gemm(const uint32_t* codes, int K, int codebook, int
     a.x = reinterpret_cast<const __half*>(x);
     a.y = reinterpret_cast<__half*>(y);
     a.debug_stall = g_debug_stall.load(std::memory_order_relaxed);
-    return prefill_fused(M) ? run_fused(a, M, ws, cs) : run_dense(a, M, ws, cs);
+    return prefill_fused(M) ? run_fused(a, M, ws, workspace_bytes, cs) : run_dense(a, M, ws, workspace_bytes, cs);
   }
   // EXL3_PATH_TENSOR: passes of up to 128 batch rows through the tensor-core
   // kernel at N = 128; each pass decodes the tiles once into tensor memory for
@@ -791,8 +793,9 @@ extern "C" exl3_status exl3_gemm(const uint32_t* codes, int K, int codebook, int
   const int R = kPrefillRows;
   uint32_t* status = reinterpret_cast<uint32_t*>(ws) + m / kRowBlock;
   float* zacc = reinterpret_cast<float*>(ws + zacc_offset(m));
-  __half* bimg = reinterpret_cast<__half*>(ws + bimg_offset(m, R));
-  float* bsum = reinterpret_cast<float*>(ws + bsum_offset(m, n, R));
+  char* scratch = ws + single_scratch_offset(m, n, workspace_bytes, workspace_total(m, n, R) - bimg_offset(m, R));
+  __half* bimg = reinterpret_cast<__half*>(scratch);
+  float* bsum = reinterpret_cast<float*>(scratch + (bsum_offset(m, n, R) - bimg_offset(m, R)));
   for (int done = 0; done < M; done += R) {
     const int rows = M - done < R ? M - done : R;
     LayerArgs a{};

@@ -78,7 +78,11 @@ EncodeTiledFn encode_tiled();
 //             operand B, one (tc_nb(M) x 128) image per 128 input columns;
 //   bsum      fp32 [M][n/128]: sums of the binary16 rotated x per 128 block
 //             (1MAD correction of the tensor-core kernel).
-// counters and zacc must be zero before a call and are zero after it.
+// counters and zacc must be zero before a call and are zero after it; they lie at
+// the front.  The rest (scratch) lies at the end of what the caller gives, so that
+// calls of other batches on the same workspace leave each other's zeros alone: with front
+// and scratch both growing with M, the front of one and the scratch of another fit
+// beside one another wherever the larger call fits.
 inline size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 // Batch columns of the tensor-core MMAs (N of the 128 x N x 16 shape).
 inline int tc_nb(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 128; }
@@ -390,25 +394,39 @@ exl3_status launch_fused(const uint32_t* codes, int K, int codebook, const __hal
 
 // Dense prefill path (exl3_gemm above EXL3_MAX_BATCH): batch rows per MMA tile
 // (N of 128 x N x 16) and the workspace layout: counters and status as above,
-// zacc fp32 [M][m], bimg one (nb x n) operand-B image per tile of nb batch
-// rows, aimg the decoded matrix as m * n binary16 operand-A images, cnt one
-// uint32 per (128-row block, tile): K-split arrivals.  The regions are sized
+// zacc fp32 [M][m], as scratch bimg, one (nb x n) operand-B image per tile of nb batch
+// rows, and aimg, the decoded matrix as m * n binary16 operand-A images; behind it cnt, one
+// uint32 per (128-row block, tile): K-split arrivals, zero between calls like the front, so
+// every call keeps clear of as many of them as any batch that the workspace is large
+// enough for has.  The regions are sized
 // for tiles of kDenseNB rows; a batch of M <= 128 rows runs as one tile of
 // dense_nb(M) <= M rounded up, which fits in them.
 constexpr int kDenseNB = 256;
 inline int dense_nb(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : kDenseNB; }
 inline int dense_tiles(int M) { return (M + kDenseNB - 1) / kDenseNB; }
-inline size_t dense_bimg_offset(int m, int M) { return bimg_offset(m, M); }
-inline size_t dense_aimg_offset(int m, int n, int M) {
-  return dense_bimg_offset(m, M) +
-         align256(sizeof(__half) * static_cast<size_t>(dense_tiles(M)) * kDenseNB * n);
-}
-inline size_t dense_cnt_offset(int m, int n, int M) {
-  return dense_aimg_offset(m, n, M) + align256(sizeof(__half) * static_cast<size_t>(m) * n);
+inline size_t dense_cnt_bytes(int m, int tiles) { return align256(sizeof(uint32_t) * static_cast<size_t>(m / kRowBlock) * tiles); }
+inline size_t dense_bimg_bytes(int n, int M) { return align256(sizeof(__half) * static_cast<size_t>(dense_tiles(M)) * kDenseNB * n); }
+inline size_t dense_scratch_bytes(int m, int n, int M) {
+  return dense_bimg_bytes(n, M) + align256(sizeof(__half) * static_cast<size_t>(m) * n);
 }
 inline size_t dense_total(int m, int n, int M) {
-  return dense_cnt_offset(m, n, M) +
-         align256(sizeof(uint32_t) * static_cast<size_t>(m / kRowBlock) * dense_tiles(M));
+  return bimg_offset(m, M) + dense_scratch_bytes(m, n, M) + dense_cnt_bytes(m, dense_tiles(M));
+}
+// Where cnt begins in a workspace of a single layer (its end where no batch of this path fits),
+// and where `bytes` (a multiple of 256) of scratch before it do.
+inline size_t single_cnt_offset(int m, int n, size_t workspace_bytes) {
+  const size_t end = workspace_bytes & ~static_cast<size_t>(255);
+  if (end < dense_total(m, n, EXL3_MAX_BATCH + 1)) return end;
+  // the most tiles: about so many more than one, a tile more from 256 t + 1 rows on
+  const size_t each = sizeof(float) * static_cast<size_t>(kDenseNB) * m + sizeof(__half) * static_cast<size_t>(kDenseNB) * n;
+  size_t more = (end - dense_total(m, n, 1)) / each;
+  if (more > (1u << 22)) more = 1u << 22;
+  int tiles = 1 + static_cast<int>(more);
+  while (tiles > 1 && dense_total(m, n, kDenseNB * (tiles - 1) + 1) > end) --tiles;
+  return end - dense_cnt_bytes(m, tiles);
+}
+inline size_t single_scratch_offset(int m, int n, size_t workspace_bytes, size_t bytes) {
+  return single_cnt_offset(m, n, workspace_bytes) - bytes;
 }
 // K splits of the dense kernel: with fewer units than CTAs, the largest s
 // with units * s <= grid, at least 16 stages of 64 columns per split, at most

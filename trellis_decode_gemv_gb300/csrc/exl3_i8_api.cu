@@ -193,10 +193,9 @@ size_t i8_layer_bytes(int m, int n, int M) {
          align256(sizeof(int32_t) * static_cast<size_t>(M) * (n / 16)) +
          align256(sizeof(float) * static_cast<size_t>(M) * (n / kRowBlock));
 }
-I8Region i8_region(char* ws, size_t at, int m, int n, int M) {
+I8Region i8_region(char* ws, size_t zacc_at, size_t at, int m, int n, int M) {
   I8Region r;
-  r.zacc = reinterpret_cast<float*>(ws + at);
-  at += align256(sizeof(float) * static_cast<size_t>(M) * m);
+  r.zacc = reinterpret_cast<float*>(ws + zacc_at);
   r.q4 = reinterpret_cast<int32_t*>(ws + at);
   at += align256(sizeof(int32_t) * static_cast<size_t>(M) * n);
   r.tcorr = reinterpret_cast<int32_t*>(ws + at);
@@ -204,8 +203,16 @@ I8Region i8_region(char* ws, size_t at, int m, int n, int M) {
   r.cs = reinterpret_cast<float*>(ws + at);
   return r;
 }
-// Single layer: counters and status word, then the layer's region.
+I8Region i8_region(char* ws, size_t at, int m, int n, int M) {
+  return i8_region(ws, at, at + align256(sizeof(float) * static_cast<size_t>(M) * m), m, n, M);
+}
+// Single layer: counters and status word, then the row sums; the operands at the end of the
+// workspace, so that a call of another batch finds its zeros.
 size_t i8_total(int m, int n, int M) { return zacc_offset(m) + i8_layer_bytes(m, n, M); }
+I8Region i8_single(char* ws, size_t ws_bytes, int m, int n, int M) {
+  const size_t scratch = i8_layer_bytes(m, n, M) - align256(sizeof(float) * static_cast<size_t>(M) * m);
+  return i8_region(ws, zacc_offset(m), (ws_bytes & ~static_cast<size_t>(255)) - scratch, m, n, M);
+}
 
 exl3_status check_i8(const uint32_t* codes, int K, int codebook, int m, int n, const exl3_half* s_out,
                      const exl3_half* scales, int M, const void* xin, exl3_half* y) {
@@ -363,7 +370,7 @@ extern "C" exl3_status exl3_gemm_i8(const uint32_t* codes, int K, int codebook, 
   if (!aligned16(workspace)) return EXL3_ERR_ALIGN;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  const I8Region reg = i8_region(ws, zacc_offset(m), m, n, M);
+  const I8Region reg = i8_single(ws, workspace_bytes, m, n, M);
   PrepGroup g{};
   g.count = 1;
   g.rows = M;
@@ -410,7 +417,7 @@ extern "C" exl3_status exl3_gemm_int8act(const uint32_t* codes, int K, int codeb
   if (s_in && !aligned16(s_in)) return EXL3_ERR_ALIGN;
   if (!workspace || workspace_bytes < i8_total(m, n, M)) return EXL3_ERR_WORKSPACE;
   if (!aligned16(workspace)) return EXL3_ERR_ALIGN;
-  const I8Region reg = i8_region(static_cast<char*>(workspace), zacc_offset(m), m, n, M);
+  const I8Region reg = i8_single(static_cast<char*>(workspace), workspace_bytes, m, n, M);
   const exl3_layer L = layer_of(codes, m, n, s_in, s_out, scales, x, y);
   return run_int8act(&L, &reg, 1, &K, &codebook, M, reinterpret_cast<cudaStream_t>(stream));
 }
