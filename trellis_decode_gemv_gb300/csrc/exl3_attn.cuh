@@ -408,25 +408,42 @@ constexpr int kPromptItemCost = 3;
 // its own latencies, and both begin and end with some microseconds of latency.  The SMs
 // are divided by the time that each kernel's work takes of an SM: a unit of the many-rows
 // kernel 1.97 us, one of the other 0.16 us with three blocks an SM and 0.21 us with two.
-// What a request adds to either (x: many-rows units, y: the other's), for a key/value
-// head; roughly, for the sums only divide the SMs.
+// What a request adds to either (x: many-rows units, y: the other's, and the many-rows kernel's
+// row tiles), for a key/value head; roughly, for the sums only divide the SMs.
 struct Costs {
-  float x, y;
+  float x, y, tiles;
+  __device__ __forceinline__ void add(const Costs& c) {
+    x += c.x;
+    y += c.y;
+    tiles += c.tiles;
+  }
+  __device__ __forceinline__ void add_lanes() {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+      add(Costs{__shfl_xor_sync(0xFFFFFFFFu, x, d), __shfl_xor_sync(0xFFFFFFFFu, y, d), __shfl_xor_sync(0xFFFFFFFFu, tiles, d)});
+  }
 };
 template <int D>
 __device__ __forceinline__ Costs costs_of(const AttnParams& p, const Req& r) {
   const int keys = r.seq - r.k0;
   const int few = p.many ? r.other : r.rows, many = p.many ? r.rows : r.other;
   Costs c;
-  c.x = static_cast<float>(many + 255 >> 8) * static_cast<float>((keys >> 7) + 1 + kPromptItemCost);
+  c.tiles = static_cast<float>(many + 255 >> 8);
+  c.x = c.tiles * static_cast<float>((keys >> 7) + 1 + kPromptItemCost);
   c.y = static_cast<float>(few + p.step_tile - 1 >> p.step_shift) * static_cast<float>(keys / step_unit(D) + 1 + (p.step_shift > 3 ? 2 : 1) * kStepItemCost);
   return c;
 }
-// SMs of the many-rows kernel.
-__device__ __forceinline__ int many_sms(const AttnParams& p, float x, float y) {
-  if (x == 0.f || y == 0.f) return x == 0.f ? 0 : p.sms;
-  x *= p.step_shift > 3 ? 10.f : 14.f;
-  return min(max(__float2int_rn(static_cast<float>(p.sms) * __fdividef(x, x + y)), 1), p.sms - 1);
+// SMs of the many-rows kernel.  A few items, which are split anyway, are split evenly, so that no
+// range ends one item and begins another.
+__device__ __forceinline__ int many_sms(const AttnParams& p, const Costs& c) {
+  const float x = c.x * (p.step_shift > 3 ? 10.f : 13.f), items = c.tiles * static_cast<float>(p.kv_heads);
+  if (x == 0.f) return 0;
+  float n = static_cast<float>(p.sms) * __fdividef(x, x + c.y);
+  if (4.f * items <= n) {
+    n = rintf(__fdividef(n, items)) * items;
+    if (n > static_cast<float>(p.sms)) n -= items;
+  }
+  return c.y == 0.f ? min(__float2int_rn(n), p.sms) : min(max(__float2int_rn(n), 1), p.sms - 1);
 }
 
 exl3_status launch_prompt(const AttnParams& p, const exl3_kv_cache& c, bool after_step, cudaStream_t stream);

@@ -351,38 +351,27 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
     }
   }
   long long mine[1] = {0}, tiles[1];
-  Costs costs{0.f, 0.f};
+  Costs costs{0.f, 0.f, 0.f};
   for (int b = b0; b < b1; ++b) {
     const Req r = load_from<SHARED>(p, lists, b);
     req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq - r.k0);
     mine[0] += row_tiles(r.rows);
     if constexpr (SHARED) {
       if (kept != nullptr) kept[b] = r;
-      const Costs x = costs_of<D>(p, r);
-      costs.x += x.x;
-      costs.y += x.y;
+      costs.add(costs_of<D>(p, r));
     }
   }
   if constexpr (SHARED) {   // the warps' sums behind those of the scans
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      costs.x += __shfl_xor_sync(0xFFFFFFFFu, costs.x, d);
-      costs.y += __shfl_xor_sync(0xFFFFFFFFu, costs.y, d);
-    }
+    costs.add_lanes();
     if ((tid & 31) == 0) reinterpret_cast<Costs*>(sums + 6 * 32)[tid >> 5] = costs;
   }
   block_scan(sums, mine, tiles);
   int most = static_cast<int>(gridDim.x);
   if constexpr (SHARED) {
-    costs = Costs{0.f, 0.f};
-    for (int w = 0; w < kThreads / 32; ++w) {
-      costs.x += reinterpret_cast<const Costs*>(sums + 6 * 32)[w].x;
-      costs.y += reinterpret_cast<const Costs*>(sums + 6 * 32)[w].y;
-    }
-    most = min(most, many_sms(p, costs.x, costs.y));
-    // a few items that are split anyway are split evenly, and no range ends one item and begins another
-    const int items = static_cast<int>(min(tiles[0] * p.kv_heads, 0x7FFFFFFFLL));
-    if (items > 0 && 4LL * items <= most) most -= most % items;
+    const int lane = tid & 31;
+    costs = lane < kThreads / 32 ? reinterpret_cast<const Costs*>(sums + 6 * 32)[lane] : Costs{0.f, 0.f, 0.f};
+    costs.add_lanes();
+    most = min(most, many_sms(p, costs));
   }
   long long at = mine[0];
   for (int b = b0; b < b1; ++b) {

@@ -355,12 +355,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     if constexpr (SHARED) {
       if (p.both) {
         Costs c = costs_of<D>(p, r);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          c.x += __shfl_xor_sync(0xFFFFFFFFu, c.x, d);
-          c.y += __shfl_xor_sync(0xFFFFFFFFu, c.y, d);
-        }
-        most = min(most, C::kCtasPerSm * (p.sms - many_sms(p, c.x, c.y)));
+        c.add_lanes();
+        most = min(most, C::kCtasPerSm * (p.sms - many_sms(p, c)));
       }
     }
     ctas = static_cast<int>(min(static_cast<long long>(most), ranges));
@@ -381,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const int per = (count + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, count), b1 = min(b0 + per, count);
     long long mine = 0, ranges = 0;
-    Costs costs{0.f, 0.f};
+    Costs costs{0.f, 0.f, 0.f};
     Req* kept = reinterpret_cast<Req*>(smem_raw + sizeof(Shared<D, NT>) + kListedBytes);
     static_assert(kThreads <= kKept && sizeof(Shared<D, NT>) % 16 == 0, "room for a request a thread");
     for (int b = b0; b < b1; ++b) {
@@ -389,9 +385,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       req_cost<D, NT, SHARED>(p, r, mine, ranges);
       if constexpr (SHARED) {
         if (per == 1) kept[b] = r;
-        const Costs c = costs_of<D>(p, r);
-        costs.x += c.x;
-        costs.y += c.y;
+        costs.add(costs_of<D>(p, r));
       }
     }
     long long inc = mine;
@@ -400,11 +394,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
       if (lane >= d) inc += o;
       ranges += __shfl_xor_sync(0xFFFFFFFFu, ranges, d);
-      if constexpr (SHARED) {
-        costs.x += __shfl_xor_sync(0xFFFFFFFFu, costs.x, d);
-        costs.y += __shfl_xor_sync(0xFFFFFFFFu, costs.y, d);
-      }
     }
+    if constexpr (SHARED) costs.add_lanes();
     if (lane == 31) {
       sh.warp_sum[warp] = inc;
       sh.warp_ranges[warp] = ranges;
@@ -421,13 +412,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     }
     if constexpr (SHARED) {
       if (p.both) {
-        Costs c{0.f, 0.f};
+        Costs c = sh.warp_costs[0];
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-          c.x += sh.warp_costs[w].x;
-          c.y += sh.warp_costs[w].y;
-        }
-        most = min(most, C::kCtasPerSm * (p.sms - many_sms(p, c.x, c.y)));
+        for (int w = 1; w < kThreads / 32; ++w) c.add(sh.warp_costs[w]);
+        most = min(most, C::kCtasPerSm * (p.sms - many_sms(p, c)));
       }
     }
     ctas = static_cast<int>(min(static_cast<long long>(most), all_ranges));

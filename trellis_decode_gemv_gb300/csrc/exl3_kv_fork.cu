@@ -235,10 +235,10 @@ size_t fork_flags(int pages) { return (static_cast<size_t>(pages) + 15) & ~stati
 // ---- copy ----------------------------------------------------------------------
 
 // A warp takes the tokens of one page and head, of the keys or the values of one
-// layer, eight 16-byte vectors a lane in flight; a block a pair's in one layer.
+// layer, eight 16-byte vectors a lane in flight; a block a pair's keys or values in one layer.
 // Bytes bound it.  The caches come by value, so a captured call needs no array that
 // outlives it.
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 128;
 
 template <int LAYERS>
 struct CopyParams {
@@ -262,9 +262,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
   const int lane = threadIdx.x & 31;
   const int vecs = tokens * p.head_dim / 16;
   const size_t of_head = static_cast<size_t>(p.page_size) * p.head_dim;
-  for (int w = threadIdx.x >> 5; w < 2 * p.kv_heads; w += kCopyThreads / 32) {
-    const int side = w >= p.kv_heads ? 1 : 0;
-    const int head = w - (side ? p.kv_heads : 0);
+  const int side = blockIdx.z;
+  for (int head = threadIdx.x >> 5; head < p.kv_heads; head += kCopyThreads / 32) {
     const size_t src = static_cast<size_t>(from) * p.kv_heads + head, dst = static_cast<size_t>(to) * p.kv_heads + head;
     const uint4* a = reinterpret_cast<const uint4*>(c.x[side] + src * of_head);
     uint4* b = reinterpret_cast<uint4*>(c.x[side] + dst * of_head);
@@ -293,7 +292,7 @@ exl3_status launch_copy(const exl3_kv_cache* caches, int layers, const int32_t* 
   p.kv_heads = caches->kv_heads;
   p.page_size = caches->page_size;
   p.head_dim = caches->head_dim;
-  copy_kernel<LAYERS><<<dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(layers)), kCopyThreads, 0, cs>>>(p);
+  copy_kernel<LAYERS><<<dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(layers), 2), kCopyThreads, 0, cs>>>(p);
   return launch_status();
 }
 
