@@ -110,11 +110,30 @@ struct AttnParams {
 struct Req {
   int t0, n, rows;  // first token, new tokens, rows (new * group), 0 if another launch's
   int seq;          // cached tokens, the new ones included; a prefix's length
+};
+struct SharedReq : Req {
   int late;         // token i of it sees the keys before min(seq, late + i + 1)
   int k0;           // its first key: those before are its group's prefix
   int row;          // of the block table
-  int other;        // calls with prefixes: rows, if the other launch's
+  int other;        // rows, if the other launch's
 };
+template <bool SHARED>
+struct ReqType {
+  using type = Req;
+};
+template <>
+struct ReqType<true> {
+  using type = SharedReq;
+};
+template <bool SHARED>
+using ReqOf = typename ReqType<SHARED>::type;
+
+__device__ __forceinline__ int late_of(const Req& r) { return r.seq - r.n; }
+__device__ __forceinline__ int late_of(const SharedReq& r) { return r.late; }
+__device__ __forceinline__ int first_key(const Req&) { return 0; }
+__device__ __forceinline__ int first_key(const SharedReq& r) { return r.k0; }
+__device__ __forceinline__ int table_row(const Req&, int b) { return b; }
+__device__ __forceinline__ int table_row(const SharedReq& r, int) { return r.row; }
 
 template <bool SHARED>
 __device__ __forceinline__ int req_count(const AttnParams& p) { return SHARED ? p.groups + p.requests : p.requests; }
@@ -150,7 +169,7 @@ __device__ __forceinline__ int cached_tokens(const AttnParams& p, const Lists& l
 }
 // A request's rows, which are this launch's or the other's.
 template <bool SHARED>
-__device__ __forceinline__ void set_rows(const AttnParams& p, Req& r, int most_few) {
+__device__ __forceinline__ void set_rows(const AttnParams& p, ReqOf<SHARED>& r, int most_few) {
   const long long all = static_cast<long long>(r.n) * p.group;
   if constexpr (SHARED) {
     const int rows = static_cast<int>(min(all, 0x7FFFFFFFLL));
@@ -175,8 +194,8 @@ __device__ __forceinline__ Group load_group(const AttnParams& p, const Lists& l,
 }
 
 // A prefix: its pages are those of the first request that holds all of it.
-__device__ __forceinline__ Req load_prefix(const AttnParams& p, const Lists& l, int g) {
-  Req r{0, 0, 0, 0, 0, 0, 0, 0};
+__device__ __forceinline__ SharedReq load_prefix(const AttnParams& p, const Lists& l, int g) {
+  SharedReq r{};
   const Group x = load_group(p, l, g);
   if (x.prefix == 0) return r;
   for (int b = x.a; b < x.e; ++b) {
@@ -193,8 +212,8 @@ __device__ __forceinline__ Req load_prefix(const AttnParams& p, const Lists& l, 
 }
 
 template <bool SHARED>
-__device__ __forceinline__ Req make_req(const AttnParams& p, const Lists& l, int b) {
-  Req r{0, 0, 0, 0, 0, 0, 0, 0};
+__device__ __forceinline__ ReqOf<SHARED> make_req(const AttnParams& p, const Lists& l, int b) {
+  ReqOf<SHARED> r{};
   if constexpr (SHARED) {
     if (b < p.groups) return load_prefix(p, l, b);
     b -= p.groups;
@@ -206,9 +225,9 @@ __device__ __forceinline__ Req make_req(const AttnParams& p, const Lists& l, int
     r.n = max(e - a, 0);
     set_rows<SHARED>(p, r, p.rows_hi);
     r.seq = cached_tokens(p, l, b);
-    r.late = r.seq - r.n;
-    r.row = b;
     if constexpr (SHARED) {
+      r.late = r.seq - r.n;
+      r.row = b;
       int g = -1, hi = p.groups;   // the last group that begins at b or before
       while (hi - g > 1) {
         const int mid = (g + hi) >> 1;
@@ -223,24 +242,28 @@ __device__ __forceinline__ Req make_req(const AttnParams& p, const Lists& l, int
   return r;
 }
 
-static __device__ __noinline__ Req load_shared(const AttnParams& p, int b) { return make_req<true>(p, Lists(p), b); }
+static __device__ __noinline__ SharedReq load_shared(const AttnParams& p, int b) { return make_req<true>(p, Lists(p), b); }
 
 // From a copy of the lists where there may be one.  (Their pointers want registers that a
 // call without prefixes does not have to spare.)
 template <bool SHARED>
-__device__ __forceinline__ Req load_from(const AttnParams& p, const Lists& l, int b) {
-  if constexpr (SHARED) return make_req<true>(p, l, b);
-  return make_req<false>(p, Lists(p), b);
+__device__ __forceinline__ ReqOf<SHARED> load_from(const AttnParams& p, const Lists& l, int b) {
+  if constexpr (SHARED)
+    return make_req<true>(p, l, b);
+  else
+    return make_req<false>(p, Lists(p), b);
 }
 // Where it is seldom needed.
 template <bool SHARED>
-__device__ __forceinline__ Req load_req(const AttnParams& p, int b) {
-  if constexpr (SHARED) return load_shared(p, b);
-  return make_req<false>(p, Lists(p), b);
+__device__ __forceinline__ ReqOf<SHARED> load_req(const AttnParams& p, int b) {
+  if constexpr (SHARED)
+    return load_shared(p, b);
+  else
+    return make_req<false>(p, Lists(p), b);
 }
 
 // Up to 32 groups and requests: lane b's, from one round of reads and exchanges.
-__device__ __forceinline__ Req load_lanes(const AttnParams& p) {
+__device__ __forceinline__ SharedReq load_lanes(const AttnParams& p) {
   const int lane = threadIdx.x & 31;
   const int b = lane - p.groups;   // its request
   const bool group = b < 0, own = b >= 0 && b < p.requests;
@@ -250,7 +273,7 @@ __device__ __forceinline__ Req load_lanes(const AttnParams& p) {
   const int a = min(max(first, 0), group ? p.requests : p.tokens);
   const int e = min(max(second, 0), group ? p.requests : p.tokens);
   const int cut = static_cast<int>(min(static_cast<long long>(max(len, 0)), p.most));
-  Req r{0, 0, 0, 0, 0, 0, 0, 0};
+  SharedReq r{};
   const int prefix = group && e - a > 1 ? cut & ~(p.align - 1) : 0;
   if (own) {
     r.t0 = a;
@@ -283,7 +306,7 @@ __device__ __forceinline__ Req load_lanes(const AttnParams& p) {
 // ranges are numbered behind the other's).  For its own keys besides: whether
 // it has a prefix, whether it sees a key at all.
 constexpr uint32_t kHasPrefix = 1, kSees = 2;
-__device__ __forceinline__ void mark_row(const AttnParams& p, const Req& r, bool own, int tok, size_t at, uint32_t code) {
+__device__ __forceinline__ void mark_row(const AttnParams& p, const SharedReq& r, bool own, int tok, size_t at, uint32_t code) {
   if (own)
     p.flag[at] = code << 2 | (r.k0 > 0 ? kHasPrefix : 0u) | (r.late + tok + 1 > 0 ? kSees : 0u);
   else
@@ -292,7 +315,9 @@ __device__ __forceinline__ void mark_row(const AttnParams& p, const Req& r, bool
 
 // The first key that token `tok` of a request does not see.
 template <bool SHARED>
-__device__ __forceinline__ int sees_before(const Req& r, int tok) { return SHARED ? min(r.seq, r.late + tok + 1) : r.late + tok + 1; }
+__device__ __forceinline__ int sees_before(const ReqOf<SHARED>& r, int tok) {
+  return SHARED ? min(r.seq, late_of(r) + tok + 1) : late_of(r) + tok + 1;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -424,7 +449,7 @@ struct Costs {
   }
 };
 template <int D>
-__device__ __forceinline__ Costs costs_of(const AttnParams& p, const Req& r) {
+__device__ __forceinline__ Costs costs_of(const AttnParams& p, const SharedReq& r) {
   const int keys = r.seq - r.k0;
   const int few = p.many ? r.other : r.rows, many = p.many ? r.rows : r.other;
   Costs c;

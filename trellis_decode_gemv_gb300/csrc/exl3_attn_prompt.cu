@@ -99,10 +99,15 @@ struct Control {
   alignas(8) float top[2][2][kTile];          // per tile and half of the keys: a row's largest score; at an item's end its sum
   long long bounds[2];
   int last_range;                             // of the item that ends after this range
-  Req first_req;
+  SharedReq first_req;
   int first_b, first_tile, first_head, first_lo;
   uint32_t tmem_base, abort;
 };
+
+template <bool SHARED>
+__device__ __forceinline__ ReqOf<SHARED>& first_req(Control& c) { return c.first_req; }
+template <bool SHARED>
+__device__ __forceinline__ const ReqOf<SHARED>& first_req(const Control& c) { return c.first_req; }
 
 __device__ __forceinline__ bool aborted(const Control& c) { return *reinterpret_cast<const volatile uint32_t*>(&c.abort) != 0u; }
 
@@ -233,8 +238,8 @@ __device__ __forceinline__ int tile_units(const AttnParams& p, int n, int late, 
   return max(1, ((SHARED ? min(seq, late + last + 1) : late + last + 1) + kKeys - 1) / kKeys);
 }
 template <bool SHARED>
-__device__ __forceinline__ int tile_units(const AttnParams& p, const Req& r, int rt) {
-  return tile_units<SHARED>(p, r.n, r.late - r.k0, r.seq - r.k0, rt);
+__device__ __forceinline__ int tile_units(const AttnParams& p, const ReqOf<SHARED>& r, int rt) {
+  return tile_units<SHARED>(p, r.n, late_of(r) - first_key(r), r.seq - first_key(r), rt);
 }
 
 // An item of at most kWhole units is not split: leaving and joining partial results
@@ -255,9 +260,9 @@ struct Walker {
   const AttnParams& p;
   int left;   // units of the range from the current item's first on
   int b, rt, head, lo, hi, units;
-  Req r;
+  ReqOf<SHARED> r;
   __device__ __forceinline__ Walker(const AttnParams& params, const Control& c, int count)
-      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(c.first_req) {
+      : p(params), left(count), b(c.first_b), rt(c.first_tile), head(c.first_head), lo(c.first_lo), r(first_req<SHARED>(c)) {
     units = tile_units<SHARED>(p, r, rt);
     if (lo == units) advance();
     hi = min(units, lo + left);
@@ -342,10 +347,10 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   const int b0 = min(tid * per, requests), b1 = min(b0 + per, requests);
   long long* sums = reinterpret_cast<long long*>(c.top);   // not in use yet
   Lists lists(p);
-  Req* kept = nullptr;   // what is found out about each request
+  SharedReq* kept = nullptr;   // what is found out about each request
   if constexpr (SHARED) {
     if (requests <= kListed) {
-      kept = reinterpret_cast<Req*>(static_cast<unsigned char*>(room) + 12 * kListed + 16);
+      kept = reinterpret_cast<SharedReq*>(static_cast<unsigned char*>(room) + 12 * kListed + 16);
       lists.copy_to(p, reinterpret_cast<int32_t*>(kept + requests), kThreads);
       __syncthreads();
     }
@@ -353,8 +358,8 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
   long long mine[1] = {0}, tiles[1];
   Costs costs{0.f, 0.f, 0.f};
   for (int b = b0; b < b1; ++b) {
-    const Req r = load_from<SHARED>(p, lists, b);
-    req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq - r.k0);
+    const ReqOf<SHARED> r = load_from<SHARED>(p, lists, b);
+    req[b] = make_int2(r.rows > 0 ? r.n : 0, r.seq - first_key(r));
     mine[0] += row_tiles(r.rows);
     if constexpr (SHARED) {
       if (kept != nullptr) kept[b] = r;
@@ -487,7 +492,7 @@ __device__ __forceinline__ bool find_range(const AttnParams& p, Control& c, void
           c.first_tile = x - first[b];
           c.first_head = head;
           c.first_lo = lo;
-          c.first_req = load_from<SHARED>(p, lists, b);
+          first_req<SHARED>(c) = load_from<SHARED>(p, lists, b);
         }
       }
       before += of_tile;
@@ -710,7 +715,7 @@ __device__ __forceinline__ void store_sums(float* dst, const uint32_t (&a)[N]) {
 // for the range whose arrival completes the item.  Not inlined: its registers are
 // not the unit loop's.
 template <int D, bool SHARED>
-__device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req req, bool own, int head, int base, int lo, bool whole,
+__device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, ReqOf<SHARED> req, bool own, int head, int base, int lo, bool whole,
                                          bool busy, bool ok, uint32_t o_at, float m, float l) {
   const int r = threadIdx.x & (kTile - 1);
   const int sw = (threadIdx.x >> 5) - kSoftmaxWarp0;
@@ -726,7 +731,7 @@ __device__ __noinline__ void finish_item(const AttnParams& p, Control& ctl, Req 
   const bool mine = base + r < req.rows;
   const int rr = base + r;
   const int tok = rr / p.group;
-  const bool sees = req.late + tok + 1 > 0;
+  const bool sees = late_of(req) + tok + 1 > 0;
   const int h = head * p.group + (rr - tok * p.group);
   const size_t part_at = SHARED ? (static_cast<size_t>(own ? p.tokens : 0) + req.t0 + tok) * p.q_heads + h : 0;
   __half* dst = p.out + static_cast<size_t>(req.t0 + tok) * p.out_stride + static_cast<size_t>(h) * D + half * (D / 2);
@@ -998,10 +1003,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto look_up = [&]() -> Look {
       Look k{-1, 0, 0};
       if (live) {
-        const int key = w.r.k0 + blk * kKeys + key16;
+        const int key = first_key(w.r) + blk * kKeys + key16;
         k.head = w.head;
-        k.keys = w.r.seq - w.r.k0 - blk * kKeys;
-        if (key < w.r.seq) k.page = __ldg(p.table + static_cast<size_t>(w.r.row) * p.table_stride + (key >> p.page_shift));
+        k.keys = w.r.seq - first_key(w.r) - blk * kKeys;
+        if (key < w.r.seq) k.page = __ldg(p.table + static_cast<size_t>(table_row(w.r, w.b)) * p.table_stride + (key >> p.page_shift));
         if (++blk == w.hi) {
           w.next();
           live = w.more();
@@ -1177,7 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (busy) {
           if (ok) tc_fence_after();
           const float4* sc = &ctl.scale[n % kScaleSlots][half * (kGroups / 2)];
-          const int key0 = w.r.k0 + (w.lo + j) * kKeys;
+          const int key0 = first_key(w.r) + (w.lo + j) * kKeys;
           const int left = lim - key0 - half * kHalf;     // of this half of the unit
           // from its first masked unit on an item is masked
           exact = exact || key0 + kKeys > lim_min;
@@ -1222,7 +1227,7 @@ exl3_status launch(const AttnParams& p, const CUtensorMap& kmap, const CUtensorM
   constexpr int kSmem = Cfg<D>::kTiles + static_cast<int>(sizeof(Control));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(Cfg<D>::kTiles >= 12 * EXL3_MAX_REQUESTS + 8, "room for the requests before the tiles");
-  static_assert(Cfg<D>::kTiles >= 12 * kListed + 16 + (sizeof(Req) + 8) * kListed + 8, "room for what is kept of them");
+  static_assert(Cfg<D>::kTiles >= 12 * kListed + 16 + (sizeof(SharedReq) + 8) * kListed + 8, "room for what is kept of them");
   static std::atomic<unsigned long long> allowed{0};
   if (!allow_smem(prompt_kernel<D, SHARED>, kSmem, allowed)) return EXL3_ERR_CUDA;
   const int ctas = prompt_ctas();

@@ -84,8 +84,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 template <int NT>
 __device__ __forceinline__ int req_tiles(const Req& r) { return (r.rows + 8 * NT - 1) / (8 * NT); }
-template <int D>
-__device__ __forceinline__ int req_blocks(const Req& r) { return max(1, (r.seq - r.k0 + unit_keys<D>() - 1) / unit_keys<D>()); }
+template <int D, typename R>
+__device__ __forceinline__ int req_blocks(const R& r) { return max(1, (r.seq - first_key(r) + unit_keys<D>() - 1) / unit_keys<D>()); }
 
 // Ranges are cut in equal parts of units plus kItemCost for each item (its Q, the
 // join of the warps).  An item of at most kWhole units is not split: a boundary that
@@ -105,7 +105,7 @@ constexpr int kLeast = 4;
 
 // What a request's items cost together, and the ranges that they are worth.
 template <int D, int NT, bool SHARED>
-__device__ __forceinline__ void req_cost(const AttnParams& p, const Req& r, long long& cost, long long& ranges) {
+__device__ __forceinline__ void req_cost(const AttnParams& p, const ReqOf<SHARED>& r, long long& cost, long long& ranges) {
   const int blocks = req_blocks<D>(r);
   const long long items = static_cast<long long>(req_tiles<NT>(r)) * p.kv_heads;
   cost += items * (blocks + item_cost<NT, SHARED>());
@@ -119,8 +119,8 @@ struct Edge {
 };
 
 // The boundary at cost u, in request b, whose items begin at cost `before`.
-template <int D, int NT, bool SHARED>
-__device__ __forceinline__ Edge edge_at(const Req& r, int b, long long u, long long before, long long total, int ctas) {
+template <int D, int NT, bool SHARED, typename R>
+__device__ __forceinline__ Edge edge_at(const R& r, int b, long long u, long long before, long long total, int ctas) {
   constexpr int kCost = item_cost<NT, SHARED>();
   const int blocks = req_blocks<D>(r);
   const int each = blocks + kCost;
@@ -141,15 +141,15 @@ template <int D, int NT, bool SHARED>
 struct Walker {
   const AttnParams& p;
   int base, b;        // request of lane 0, current request
-  Req mine;
+  ReqOf<SHARED> mine;
   int item;
   int end_b, end_item, end_lo;
   // current segment
-  Req r;
+  ReqOf<SHARED> r;
   int blocks, tiles, head, tile, lo, hi;
 
   // `lanes` holds the requests from `first` on
-  __device__ __forceinline__ Walker(const AttnParams& params, const Edge& from, const Edge& to, int first, const Req& lanes)
+  __device__ __forceinline__ Walker(const AttnParams& params, const Edge& from, const Edge& to, int first, const ReqOf<SHARED>& lanes)
       : p(params), base(first), b(from.b), mine(lanes), item(from.item), end_b(to.b), end_item(to.item), end_lo(to.lo), lo(from.lo) {
     fetch();
     if (lo == blocks) advance();
@@ -165,10 +165,6 @@ struct Walker {
       r.late = __shfl_sync(0xFFFFFFFFu, mine.late, src);
       r.k0 = __shfl_sync(0xFFFFFFFFu, mine.k0, src);
       r.row = __shfl_sync(0xFFFFFFFFu, mine.row, src);
-    } else {
-      r.late = r.seq - r.n;
-      r.k0 = 0;
-      r.row = b;
     }
     blocks = req_blocks<D>(r);
     tiles = req_tiles<NT>(r);
@@ -220,7 +216,7 @@ constexpr int kListed = 256;
 constexpr size_t kListedBytes = sizeof(int32_t) * (2 * kListed + 4);   // whole 16 bytes
 // Of up to a request a thread what it has found out is kept behind that.
 constexpr int kKept = 128;
-constexpr size_t kSharedBytes = kListedBytes + sizeof(Req) * kKept;
+constexpr size_t kSharedBytes = kListedBytes + sizeof(SharedReq) * kKept;
 
 // The end of a block.  Beside the many-rows kernel this one is not done before that is, so
 // that what follows need wait for this one only.
@@ -255,7 +251,7 @@ __device__ __forceinline__ float4 join_warps(const Shared<D, NT>& sh, int row, i
 // 4 columns of row `rr` of a request's item, finished; with prefixes, its sums over the
 // prefix or (`own`) its own keys.
 template <int D, bool SHARED>
-__device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, bool own, int head, int rr, int q4, const float4& acc,
+__device__ __forceinline__ void store_out(const AttnParams& p, const ReqOf<SHARED>& r, bool own, int head, int rr, int q4, const float4& acc,
                                           float top, float sum) {
   const int tok = rr / p.group;
   const int h = head * p.group + (rr - tok * p.group);
@@ -269,7 +265,7 @@ __device__ __forceinline__ void store_out(const AttnParams& p, const Req& r, boo
     }
     return;
   }
-  const bool sees = r.late + tok + 1 > 0;
+  const bool sees = late_of(r) + tok + 1 > 0;
   const float inv = inverse_sum(sum, sees);
   const __half2 ha = __floats2half2_rn(sees ? acc.x * inv : 0.f, sees ? acc.y * inv : 0.f);
   const __half2 hb = __floats2half2_rn(sees ? acc.z * inv : 0.f, sees ? acc.w * inv : 0.f);
@@ -328,7 +324,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
   // This CTA's range.  Up to 32 requests every warp finds it by itself.
   Edge from, to;
   int ctas, first = 0;
-  Req lanes;
+  ReqOf<SHARED> lanes;
   const int count = req_count<SHARED>(p);
   Lists lists(p);
   if constexpr (SHARED) {
@@ -339,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
   }
   int most = static_cast<int>(gridDim.x);   // blocks that this call may take
   if (count <= 32) {
-    Req r;
+    ReqOf<SHARED> r;
     if constexpr (SHARED) r = load_lanes(p); else r = load_from<SHARED>(p, lists, lane);
     lanes = r;
     long long cost = 0, ranges = 0;
@@ -366,8 +362,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     for (int e = 0; e < 2; ++e) {
       const long long u = range_begin(total, cta + e, ctas);
       const int b = __popc(__ballot_sync(0xFFFFFFFFu, inc <= u));   // the request that holds u
-      Req q{0, 0, 1, 0, 0, 0, 0, 0};
-      q.seq = __shfl_sync(0xFFFFFFFFu, r.seq - r.k0, b & 31);
+      Req q{0, 0, 1, 0};
+      q.seq = __shfl_sync(0xFFFFFFFFu, r.seq - first_key(r), b & 31);
       const long long before = __shfl_sync(0xFFFFFFFFu, inc - cost, b & 31);
       Edge x{count, 0, 0, 0, 0};
       if (b < 32) x = edge_at<D, NT, SHARED>(q, b, u, before, total, ctas);
@@ -378,10 +374,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const int b0 = min(tid * per, count), b1 = min(b0 + per, count);
     long long mine = 0, ranges = 0;
     Costs costs{0.f, 0.f, 0.f};
-    Req* kept = reinterpret_cast<Req*>(smem_raw + sizeof(Shared<D, NT>) + kListedBytes);
+    ReqOf<SHARED>* kept = reinterpret_cast<ReqOf<SHARED>*>(smem_raw + sizeof(Shared<D, NT>) + kListedBytes);
     static_assert(kThreads <= kKept && sizeof(Shared<D, NT>) % 16 == 0, "room for a request a thread");
     for (int b = b0; b < b1; ++b) {
-      const Req r = load_from<SHARED>(p, lists, b);
+      const ReqOf<SHARED> r = load_from<SHARED>(p, lists, b);
       req_cost<D, NT, SHARED>(p, r, mine, ranges);
       if constexpr (SHARED) {
         if (per == 1) kept[b] = r;
@@ -423,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     const long long u[2] = {range_begin(total, cta, ctas), range_begin(total, cta + 1, ctas)};
     if (u[1] >= before && u[0] < before + mine) {
       for (int b = b0; b < b1; ++b) {
-        const Req r = SHARED && per == 1 ? kept[b] : load_from<SHARED>(p, lists, b);
+        const ReqOf<SHARED> r = SHARED && per == 1 ? kept[b] : load_from<SHARED>(p, lists, b);
         long long n = 0, unused = 0;
         req_cost<D, NT, SHARED>(p, r, n, unused);
 #pragma unroll
@@ -437,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
     to = sh.edge[1];
     first = from.b;
     if (SHARED && per == 1)
-      lanes = first + lane < count ? kept[first + lane] : Req{0, 0, 0, 0, 0, 0, 0, 0};
+      lanes = first + lane < count ? kept[first + lane] : ReqOf<SHARED>{};
     else
       lanes = load_from<SHARED>(p, lists, first + lane);
   }
@@ -468,9 +464,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
                  p.q + static_cast<size_t>(w.r.t0 + tok) * p.q_stride + static_cast<size_t>(w.head * p.group + (ra - tok * p.group)) * D,
                  static_cast<uint32_t>(rb - ra) * D * 2, &sh.q_full[qs]);
       // units, 32 at a time: lane l looks up unit g0 + l
-      const int32_t* row = p.table + static_cast<size_t>(w.r.row) * p.table_stride;
+      const int32_t* row = p.table + static_cast<size_t>(table_row(w.r, w.b)) * p.table_stride;
       for (int g0 = w.lo; g0 < w.hi && ok; g0 += 32) {
-        const int mykey = w.r.k0 + (g0 + lane) * kUnit;
+        const int mykey = first_key(w.r) + (g0 + lane) * kUnit;
         int block[kGroups];                            // of the tensor map, per 16 keys
         float ks[kGroups], vs[kGroups];
         PageScale scale[kGroups];
@@ -617,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       float4 sc[kGroups];
 #pragma unroll
       for (int hf = 0; hf < kGroups; ++hf) sc[hf] = sh.scale[st][hf];
-      const int key0 = w.r.k0 + blk * kUnit;
+      const int key0 = first_key(w.r) + blk * kUnit;
       const bool mask = key0 + kUnit > lim_min;
       bool over = false;
 #pragma unroll
@@ -745,10 +741,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
           store_out<D, SHARED>(p, w.r, SHARED && w.b >= p.groups, w.head, row0 + 8 * nt + row, q4, acc, top, sum);
         } else {
           leave<D, kRows>(slot, 8 * nt + row, q4, acc, top, sum);
-          if (SHARED && q4 == 0 && w.lo == 0) {
-            const int rr = row0 + 8 * nt + row, tok = rr / p.group;
-            mark_row(p, w.r, w.b >= p.groups, tok,
-                     static_cast<size_t>(w.r.t0 + tok) * p.q_heads + w.head * p.group + (rr - tok * p.group), 1u + cta);
+          if constexpr (SHARED) {
+            if (q4 == 0 && w.lo == 0) {
+              const int rr = row0 + 8 * nt + row, tok = rr / p.group;
+              mark_row(p, w.r, w.b >= p.groups, tok,
+                       static_cast<size_t>(w.r.t0 + tok) * p.q_heads + w.head * p.group + (rr - tok * p.group), 1u + cta);
+            }
           }
         }
       }
