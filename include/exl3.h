@@ -636,6 +636,7 @@ typedef struct {
  *     the last two reasons), so no later, smaller request overtakes it.
  *   - Pages of finished requests go to the ring's end (usable by the next call;
  *     beyond the ring's capacity they are dropped).
+ *     A row that shares pages with another (exl3_kv_fork) is not finished this way.
  * Outputs:
  *   seq_len  [requests]     c + n; c if refused; 0 if finished
  *   q_start  [requests + 1] running sum of max(n, 0), at most `tokens`: request
@@ -738,6 +739,8 @@ exl3_status exl3_attention(const exl3_kv_cache *cache, const exl3_half *q, long 
  *       (head_dim 128), 64 (head_dim 64) or 128 (max_new * q_heads / kv_heads above 48),
  *       from the pages of the group's first request that holds them all; where the
  *       pages of the others hold something else, the result is that of neither.
+ *       (A copied page of a fork is quantized anew as tokens come to it: a
+ *       prefix_len of whole shared pages leaves it to the request.)
  *       A request that holds fewer cached tokens than that, and one that is alone
  *       in its group, is computed from its own pages throughout, and so are all
  *       where the tables can hold so little (40 or 160 MB of keys and values) that
@@ -782,6 +785,9 @@ exl3_status exl3_attention_shared(const exl3_kv_cache *cache, const exl3_half *q
  *                                    that got no page
  * No output overlaps an input but the ring.  Page numbers outside 0..pages-1 are
  * copied with the table and never returned.
+ * From then on rows may hold the same pages: a row that does is ended by a fork that
+ * does not continue it, not by exl3_kv_plan's new_len < 0, which gives a row's pages
+ * back whoever else holds them.
  * workspace: exl3_kv_fork_workspace_bytes(pages) bytes (0 for pages < 1),
  * zero-filled once after allocation; every call leaves it zero again.  Calls that
  * may run concurrently must not share one.  One launch.

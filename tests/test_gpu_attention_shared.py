@@ -128,6 +128,16 @@ def test_many_requests_and_groups(requests, groups):
     check(x[0], run(*x))
 
 
+@pytest.mark.parametrize("groups,each,chunk", [(36, 25, 1), (41, 25, 1), (3, 4, 40), (9, 5, 60)])
+def test_many_row_tiles(groups, each, chunk):
+    """More row tiles than a warp has lanes, more requests and groups than are kept in shared memory; prefixes of one call on
+    both sides of what either kernel takes."""
+    rng = np.random.default_rng(groups)
+    x = make(rng, 4, 2, 64, 32, [(int(rng.integers(64, 200)), [(int(rng.integers(chunk, chunk + 40)), chunk) for _ in range(each - g % 3)])
+                                 for g in range(groups)])
+    check(x[0], run(*x))
+
+
 @pytest.mark.parametrize("requests", [8, 40])
 def test_long_prefix(requests):
     """A prefix split between many blocks, in both kernels; twice from one workspace with the same bits, the counters left zero."""

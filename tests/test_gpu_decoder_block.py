@@ -104,7 +104,8 @@ def test_block_with_forks_against_oracle(part, width):
     groups = ([0, 4, 7], [71, 34])
     step([1] * 7, groups + (4,))
     step([1, 2, 1, 1, 0, 1, 3], groups + (5,))
-    step([1, 1, -1, 1, 1, 1, 1], groups + (4,))       # one ends, its place stays
+    fork([0, 1, -1, 3, 4, 5, 6])                      # one ends, its place stays
+    step([1, 1, 0, 1, 1, 1, 1], groups + (4,))
     fork([0, 1, 3, 3, -1, 6])
     step([1, 1, 1, 1, 0, 1], ([0, 4], [71], 4))       # the last belongs to no group
     step([1, 1, 1, 1, 0, 1])

@@ -133,6 +133,9 @@ def test_fork_captured_and_into_given_outputs():
         assert np.array_equal(ring.cpu().numpy(), want["free_pages"])
     with pytest.raises(ValueError):
         B.exl3_kv_fork(parent, ctx, 16, x["pages"], ring, state, table, workspace=ws, out=B.Exl3KvFork(39, table.shape[1], table.device))
+    for args in ((f.ctx_len[:20], state, table), (ctx, f.free_state, table), (ctx, state, f.block_table)):
+        with pytest.raises(ValueError):                # its own results as inputs
+            B.exl3_kv_fork(parent, args[0], 16, x["pages"], ring, *args[1:], workspace=ws, out=f)
 
 
 # ---- copy ----------------------------------------------------------------------------

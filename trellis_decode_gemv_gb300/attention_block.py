@@ -8,9 +8,9 @@ output projection.  Shows the operators around the projections as a server uses 
         add = None                               # what the block before adds to x
         for block in blocks:
             x, add = block(x, step, max_new, add)    # x [tokens, hidden] halves
-    pool.step with -1 new tokens gives a finished request's pages back.
+    pool.step with -1 new tokens gives a finished request's pages back, if it shares none.
     pool.fork(parent) goes on with rows of other requests (samples of one prompt, beams): their
-    pages are shared but for the last one; with shared=(group_start, prefix_len, max_group)
+    pages are shared but for the last one, and rows that are not gone on with end; with shared=(group_start, prefix_len, max_group)
     the blocks then read the keys that a group's requests have in common once.
 
     python -m trellis_decode_gemv_gb300.attention_block --layers 4 --requests 8 --prompt 500 --steps 32 --samples 4
@@ -42,7 +42,7 @@ class PagePool:
 
     def step(self, new_len, tokens):
         """Pages and slots for new_len [requests] int32 new tokens (`tokens` of them
-        in all; -1: the request is finished).  step.state[2] counts pages that were
+        in all; -1: the request is finished, and none of its pages is another's).  step.state[2] counts pages that were
         lacking; requests that got none keep their length."""
         seq_len, q_start, slot, position, self.state = B.exl3_kv_plan(
             self.ctx_len, new_len, tokens, self.page_size, self.ring, self.state, self.table)
@@ -154,7 +154,7 @@ def main(argv=None):
         parent = torch.arange(a.requests, dtype=torch.int32, device=dev).repeat_interleave(a.samples)
         pool.fork(parent, caches)
         shared = (torch.arange(0, rows + 1, a.samples, dtype=torch.int32, device=dev),
-                  torch.full((a.requests,), a.prompt, dtype=torch.int32, device=dev), a.samples)
+                  torch.full((a.requests,), a.prompt // a.page * a.page, dtype=torch.int32, device=dev), a.samples)
     x = x.repeat_interleave(a.samples, 0).contiguous()
     for _ in range(a.steps):
         x = run(x, rows, 1, shared)

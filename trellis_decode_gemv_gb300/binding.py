@@ -1211,6 +1211,9 @@ def exl3_kv_fork(parent, ctx_len, page_size, pages, free_pages, free_state, bloc
     elif out.block_table.shape != (rows, width) or out.block_table.device != dev:
         raise ValueError(f"out holds a table of {tuple(out.block_table.shape)} on {out.block_table.device}, "
                          f"expected {(rows, width)} on {dev}")
+    elif any(t.data_ptr() == u.data_ptr() for t, u in ((out.block_table, block_table), (out.ctx_len, ctx_len),
+                                                       (out.free_state, free_state)) if t.numel() and u.numel()):
+        raise ValueError("out holds the call's own inputs")
     if workspace is None:
         workspace = alloc_kv_fork_workspace(pages, dev)
     _check(load_library().exl3_kv_fork(
