@@ -743,7 +743,7 @@ exl3_status exl3_attention(const exl3_kv_cache *cache, const exl3_half *q, long 
  *       prefix_len of whole shared pages leaves it to the request.)
  *       A request that holds fewer cached tokens than that, and one that is alone
  *       in its group, is computed from its own pages throughout, and so are all
- *       where the tables can hold so little (40 or 160 MB of keys and values) that
+ *       where the tables can hold so little (48 or 160 MB of keys and values) that
  *       reading it once for each request takes no longer.
  *   max_group: the most new tokens that the requests of a group bring together; like
  *       max_new it picks the kernels and sizes the workspace.

@@ -114,9 +114,9 @@ exl3_status prepare(AttnParams& p, const exl3_kv_cache* cache, const exl3_half* 
 // Bytes of keys and values that the tables can hold, up to which a call does not look for
 // shared ones: what it would save is soon read, and what it takes besides are a second kernel, or
 // two.  One: 8 requests behind 2011 tokens (38 MB) 14.7 us, 14.5 without; behind 3000 (54 MB) 14.8 and
-// 16.2; behind 8000 20.3 and 26.9.  Two: 64 requests behind 500 tokens (107 MB) 29.3 and 22.9, behind
+// 16.2; two behind 8000 (34 MB) 19.9 and 17.0, behind 16000 (67 MB) 20.1 and 21.6.  Two: 64 requests behind 500 tokens (107 MB) 29.3 and 22.9, behind
 // 1000 (172 MB) 30.1 and 32.0; 16 behind 1000 (43 MB) 25.4 and 15.0.
-constexpr double kWorthOne = 40e6, kWorthBoth = 160e6;
+constexpr double kWorthOne = 48e6, kWorthBoth = 160e6;
 
 bool few_rows(int tokens, int group) { return static_cast<long long>(tokens) * group <= kStepRows; }
 
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   // the requests' tokens: all between the first one's and the last one's
   const Lists lists(p);
   const bool live = t >= first_token(p, lists, 0) && t < first_token(p, lists, p.requests);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // (the next call may not begin yet: its blocks took 4 us of SMs from these)
   if (!__any_sync(0xFFFFFFFFu, live)) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t flag = live ? __ldcg(p.flag + at) : 0u, where = live ? __ldcg(p.where + at) : 0u;
   const bool sees = (flag & kSees) != 0u;
   const Parts a = parts_of<D>(p, false, where, live && (flag & kHasPrefix) != 0u, at, row);

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
   __shared__ int warp_sums[kForkThreads / 32];
   __shared__ int counts[kForkCluster];       // pages that go back, of the cluster's blocks
   __shared__ int last;
+  chained_begin();
   const int threads = static_cast<int>(blockDim.x);
   const int tid = threadIdx.x;
   const int lane = tid & 31;
@@ -254,6 +255,7 @@ struct CopyParams {
 
 template <int LAYERS>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams<LAYERS> p) {
+  chained_begin();
   const int pair = blockIdx.x;
   const int from = p.from[pair], to = p.to[pair];
   const int tokens = min(max(p.tokens[pair], 0), p.page_size);
@@ -292,8 +294,7 @@ exl3_status launch_copy(const exl3_kv_cache* caches, int layers, const int32_t* 
   p.kv_heads = caches->kv_heads;
   p.page_size = caches->page_size;
   p.head_dim = caches->head_dim;
-  copy_kernel<LAYERS><<<dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(layers), 2), kCopyThreads, 0, cs>>>(p);
-  return launch_status();
+  return launch_chained(copy_kernel<LAYERS>, dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(layers), 2), kCopyThreads, 0, cs, p);
 }
 
 }  // namespace
@@ -353,8 +354,8 @@ extern "C" exl3_status exl3_kv_fork(const int32_t* parent, int rows, const int32
   const int warps = kv::kForkCluster * threads / 32;
   const int want = (rows + requests + warps - 1) / warps;
   const int clusters = want < 1 ? 1 : want > kv::kMostClusters ? kv::kMostClusters : want;
-  kv::fork_kernel<<<static_cast<unsigned>(clusters * kv::kForkCluster), threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return launch_status();
+  return launch_chained(kv::fork_kernel, dim3(static_cast<unsigned>(clusters * kv::kForkCluster)), threads, smem,
+                        reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 extern "C" exl3_status exl3_kv_copy(const exl3_kv_cache* caches, int layers, const int32_t* from, const int32_t* to,

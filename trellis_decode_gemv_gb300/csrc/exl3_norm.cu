@@ -112,6 +112,7 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
 template <int VECS, bool I8, bool WARP>
 __global__ void __launch_bounds__(most_threads<VECS, WARP>()) norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float sums[32];
+  chained_begin();
   const int lane = threadIdx.x & 31;
   const int group = WARP ? 32 : static_cast<int>(blockDim.x);
   const int at = WARP ? lane : static_cast<int>(threadIdx.x);
@@ -224,8 +225,7 @@ exl3_status launch_block(const NormParams& p, int threads, cudaStream_t cs) {
   // them writes h over what the others read)
   const bool apart = p.h == nullptr || (p.h != p.x && p.h != p.residual);
   const unsigned outs = I8 && apart && static_cast<long long>(p.rows) * p.outs <= 2 * device_sm_count() ? p.outs : 1;
-  norm_kernel<VECS, I8, false><<<dim3(static_cast<unsigned>(p.rows), outs), threads, 0, cs>>>(p);
-  return launch_status();
+  return launch_chained(norm_kernel<VECS, I8, false>, dim3(static_cast<unsigned>(p.rows), outs), threads, 0, cs, p);
 }
 
 template <bool I8>
@@ -233,13 +233,9 @@ exl3_status launch(const NormParams& p, cudaStream_t cs) {
   const int vecs = p.n / 8;
   if (vecs <= 128) {
     const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.rows) + 3) / 4);
-    if (vecs <= 32)
-      norm_kernel<1, I8, true><<<blocks, 128, 0, cs>>>(p);
-    else if (vecs <= 64)
-      norm_kernel<2, I8, true><<<blocks, 128, 0, cs>>>(p);
-    else
-      norm_kernel<4, I8, true><<<blocks, 128, 0, cs>>>(p);
-    return launch_status();
+    if (vecs <= 32) return launch_chained(norm_kernel<1, I8, true>, dim3(blocks), 128, 0, cs, p);
+    if (vecs <= 64) return launch_chained(norm_kernel<2, I8, true>, dim3(blocks), 128, 0, cs, p);
+    return launch_chained(norm_kernel<4, I8, true>, dim3(blocks), 128, 0, cs, p);
   }
   // One vector a thread while the rows leave SMs idle, else as many as a thread takes.
   const bool few = p.rows <= device_sm_count();

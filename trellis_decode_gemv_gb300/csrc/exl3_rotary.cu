@@ -64,6 +64,7 @@ __device__ __forceinline__ void turn16(uint4& x, uint4& y, const float2* cs) {
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   __shared__ __align__(16) float2 table[kMostTable];
+  chained_begin();
   const int tid = threadIdx.x;
   const int t0 = static_cast<int>(blockIdx.x) * p.each;
   const int here = min(p.each, p.tokens - t0);
@@ -155,9 +156,6 @@ extern "C" exl3_status exl3_rotary(const exl3_half* q, long long q_stride, exl3_
     p.each *= 2;
   const unsigned blocks = static_cast<unsigned>((tokens + p.each - 1) / p.each);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (interleaved != 0)
-    rotary::rotary_kernel<true><<<blocks, rotary::kThreads, 0, cs>>>(p);
-  else
-    rotary::rotary_kernel<false><<<blocks, rotary::kThreads, 0, cs>>>(p);
-  return launch_status();
+  return interleaved != 0 ? launch_chained(rotary::rotary_kernel<true>, dim3(blocks), rotary::kThreads, 0, cs, p)
+                          : launch_chained(rotary::rotary_kernel<false>, dim3(blocks), rotary::kThreads, 0, cs, p);
 }
