@@ -432,7 +432,9 @@ constexpr int kPromptItemCost = 3;
 // kernel is bound by its tensor cores and the chain around them, the other by memory and
 // its own latencies, and both begin and end with some microseconds of latency.  The SMs
 // are divided by the time that each kernel's work takes of an SM: a unit of the many-rows
-// kernel 1.97 us, one of the other 0.16 us with three blocks an SM and 0.21 us with two.
+// kernel 1.97 us, one of the other 0.16 us with three blocks an SM and 0.21 us with two. (Of
+// ratios from 8 to 20 13 and 10 were best over nine calls: 64 requests behind 32000 tokens 71, 68, 67
+// and 77 us with 10, 12, 14 and 18; 40 with drafted tokens 68, 66 and 72 with 8, 10 and 12.)
 // What a request adds to either (x: many-rows units, y: the other's, and the many-rows kernel's
 // row tiles), for a key/value head; roughly, for the sums only divide the SMs.
 struct Costs {
@@ -453,9 +455,9 @@ __device__ __forceinline__ Costs costs_of(const AttnParams& p, const SharedReq& 
   const int keys = r.seq - r.k0;
   const int few = p.many ? r.other : r.rows, many = p.many ? r.rows : r.other;
   Costs c;
-  c.tiles = static_cast<float>(many + 255 >> 8);
+  c.tiles = static_cast<float>((static_cast<uint32_t>(many) + 255u) >> 8);
   c.x = c.tiles * static_cast<float>((keys >> 7) + 1 + kPromptItemCost);
-  c.y = static_cast<float>(few + p.step_tile - 1 >> p.step_shift) * static_cast<float>(keys / step_unit(D) + 1 + (p.step_shift > 3 ? 2 : 1) * kStepItemCost);
+  c.y = static_cast<float>((static_cast<uint32_t>(few) + p.step_tile - 1u) >> p.step_shift) * static_cast<float>(keys / step_unit(D) + 1 + (p.step_shift > 3 ? 2 : 1) * kStepItemCost);
   return c;
 }
 // SMs of the many-rows kernel.  A few items, which are split anyway, are split evenly, so that no
