@@ -63,13 +63,6 @@ struct Cfg {
   static constexpr int kPartStride = D + 4;
 };
 
-// Before a warp announces that it has read a slot: the next copy into it is of the other
-// proxy, which an arrival alone does not hold back behind loads that are still on their way.
-// Without it up to a fifth of the calls with 112 requests of up to 5 tokens and 120 keys, whose
-// query slots are reused quickly, took the last 16 bytes of some lane's query row from the item
-// two later.
-__device__ __forceinline__ void reads_done() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 template <int kConsumers>
 __device__ __forceinline__ void join_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(kJoinBarrier), "n"(32 * kConsumers) : "memory");
@@ -693,7 +686,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
           }
         }
         if (hf == kGroups - 1) {
-          reads_done();
+          tc::reads_done();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.empty[st]);  // the stage is in registers
         }
@@ -715,9 +708,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtasPerSm)
       }
     }
     i += w.hi - w.lo;
-    // The slot is free only now: announced right behind the loads, the fence cost what is saved
-    // here (112 requests of up to 5 tokens and 120 keys 44.1 us, so 42.2).
-    reads_done();
+    // Without the fence up to a fifth of the calls with 112 requests of up to 5 tokens and 120
+    // keys, whose slots are reused quickly, took the last 16 bytes of some lane's query row from
+    // the item two later.  The slot is given back only here: right behind the loads, the
+    // fence made such calls slower (44.1 us; here 42.2; 43.4 without it there).
+    tc::reads_done();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_empty[qs]);
 

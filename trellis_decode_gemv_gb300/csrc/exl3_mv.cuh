@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) mv_kernel(const __grid_constant__
           }
         }
         if (g == 1) {
+          tc::reads_done();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.ring_empty[rslot]);
         }

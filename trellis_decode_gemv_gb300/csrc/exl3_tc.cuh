@@ -150,6 +150,10 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       : "memory");
 }
 
+// Before the arrival that gives a slot back to bulk copies: those are of the other proxy, which
+// the arrival alone does not hold back behind loads that are still on their way.
+__device__ __forceinline__ void reads_done() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
                "r"(ncols)
@@ -502,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_layer_kernel(TcParams p) {
           raw[3][i] = rw[24 * K + idx];
         }
       }
+      reads_done();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ring_empty[slot]);
       uint32_t v0[16], v1[16];
