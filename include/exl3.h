@@ -117,9 +117,11 @@ exl3_status exl3_decode_tiles(const uint32_t *codes, int K, int codebook, int m,
  * rows of n halves) with M*(n/128) fp32 block sums.
  * Returns 0 for an invalid shape or batch.  The workspace must be zero-filled
  * once after allocation; every call leaves what it needs zero so again.  The
- * calls of a single layer (exl3_gemv, exl3_gemm_small, exl3_gemm, and among them
- * exl3_gemm_i8 and exl3_gemm_int8act) may use one workspace at changing batches if
- * each is given its full size; a workspace of a grouped or whole-rotation call, and one
+ * calls of a single layer (exl3_gemv, exl3_gemm_small, exl3_gemm, exl3_gemm_i8,
+ * exl3_gemm_int8act) may use one workspace at changing batches if each is given its
+ * full size.  Where int8 calls and others share one, that is at least what both
+ * exl3_workspace_bytes and exl3_gemm_i8_workspace_bytes say for the largest batch up to
+ * EXL3_MAX_BATCH of either.  A workspace of a grouped or whole-rotation call, and one
  * that goes to another layer, is zero-filled when batch or shapes change.  Two calls
  * that may run concurrently must not share a workspace.  The uint32 at byte
  * offset 4*(m/128) is a status word: the tensor-core kernel ORs 1 into it if

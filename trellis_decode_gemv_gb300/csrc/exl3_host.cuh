@@ -413,7 +413,10 @@ inline size_t dense_total(int m, int n, int M) {
   return bimg_offset(m, M) + dense_scratch_bytes(m, n, M) + dense_cnt_bytes(m, dense_tiles(M));
 }
 // Where cnt begins in a workspace of a single layer (its end where no batch of this path fits),
-// and where `bytes` (a multiple of 256) of scratch before it do.
+// and where `bytes` (a multiple of 256) of scratch before it do.  (There is a cnt only in a workspace
+// that a prefill of 33 rows fits in; the largest scratch of another call, the int8 operands of 32
+// rows, 32 * 4.3 * n bytes, then fits between the front of 33 rows and it, where that prefill has
+// 512 * n and more.)
 inline size_t single_cnt_offset(int m, int n, size_t workspace_bytes) {
   const size_t end = workspace_bytes & ~static_cast<size_t>(255);
   if (end < dense_total(m, n, EXL3_MAX_BATCH + 1)) return end;

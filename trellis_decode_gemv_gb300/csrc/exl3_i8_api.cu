@@ -206,12 +206,13 @@ I8Region i8_region(char* ws, size_t zacc_at, size_t at, int m, int n, int M) {
 I8Region i8_region(char* ws, size_t at, int m, int n, int M) {
   return i8_region(ws, at, at + align256(sizeof(float) * static_cast<size_t>(M) * m), m, n, M);
 }
-// Single layer: counters and status word, then the row sums; the operands at the end of the
-// workspace, so that a call of another batch finds its zeros.
+// Single layer: counters and status word, then the row sums; the operands where the binary16
+// calls of the layer have their scratch, before the counters of its prefills, so that a
+// call of another batch or of the other kind finds its zeros.
 size_t i8_total(int m, int n, int M) { return zacc_offset(m) + i8_layer_bytes(m, n, M); }
 I8Region i8_single(char* ws, size_t ws_bytes, int m, int n, int M) {
   const size_t scratch = i8_layer_bytes(m, n, M) - align256(sizeof(float) * static_cast<size_t>(M) * m);
-  return i8_region(ws, zacc_offset(m), (ws_bytes & ~static_cast<size_t>(255)) - scratch, m, n, M);
+  return i8_region(ws, zacc_offset(m), single_scratch_offset(m, n, ws_bytes, scratch), m, n, M);
 }
 
 exl3_status check_i8(const uint32_t* codes, int K, int codebook, int m, int n, const exl3_half* s_out,
