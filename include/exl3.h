@@ -637,7 +637,7 @@ typedef struct {
  *     slot.  A refused request's need still counts for those after it (but for
  *     the last two reasons), so no later, smaller request overtakes it.
  *   - Pages of finished requests go to the ring's end (usable by the next call;
- *     beyond the ring's capacity they are dropped).
+ *     what does not fit beside the pages that were free before is dropped).
  *     A row that shares pages with another (exl3_kv_fork) is not finished this way.
  * Outputs:
  *   seq_len  [requests]     c + n; c if refused; 0 if finished
@@ -775,7 +775,8 @@ exl3_status exl3_attention_shared(const exl3_kv_cache *cache, const exl3_half *q
  *     head, rows in order, and a copy (exl3_kv_copy).  A row for which the ring
  *     holds no page any more becomes empty.
  *   - Pages that a request held before and no row holds after go to the ring's
- *     end, in ascending order (beyond the ring's capacity they are dropped).
+ *     end, in ascending order (beyond the ring's capacity they are dropped; the
+ *     places of the pages that the call takes count as free).
  * Outputs:
  *   ctx_out     [rows]               the parent's ctx_len (cut to what the table
  *                                    row holds); 0 of an empty row

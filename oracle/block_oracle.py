@@ -103,7 +103,7 @@ def fork(parent, ctx_len, page_size, pages, free_pages, free_state, block_table)
     held = [set(int(p) for p in table[b, :-(-tokens[b] // page_size)]) for b in range(requests)]
     before = set().union(*[held[b] for b in range(requests) if b not in continued] or [set()])
     after = set().union(*[held[b] for b in continued] or [set()]) | {int(p) for p in dst}
-    back = sorted(p for p in before - after if 0 <= p < pages)[:cap - count]
+    back = sorted(p for p in before - after if 0 <= p < pages)[:cap - count + taken]
     for j, p in enumerate(back):
         ring[(head + count + j) % cap] = p
     state = [(head + taken) % cap if cap else 0, count - taken + len(back), lacking]

@@ -211,22 +211,23 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
       at += i < me ? counts[i] : 0;
       back_total += counts[i];
     }
-    const int room = cap - count;
+    // behind what is left in the ring: the places of the pages that were taken, which every cluster has read, are free
+    const int left = count - taken, rest = wrapped(head, taken, cap);
     for (int w = a; w < e; ++w) {
       const uint4 g = __ldcg(gone + w), k = __ldcg(kept + w);
       const uint32_t bits[4] = {g.x & ~k.x, g.y & ~k.y, g.z & ~k.z, g.w & ~k.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         for (uint32_t m = bits[i] & 0x01010101u; m != 0u; m &= m - 1, ++at)
-          if (at < room)
-            p.ring[wrapped(head, count + at, cap)] = 16 * w + 4 * i + ((__ffs(static_cast<int>(m)) - 1) >> 3);
+          if (at < cap - left)
+            p.ring[wrapped(rest, left + at, cap)] = 16 * w + 4 * i + ((__ffs(static_cast<int>(m)) - 1) >> 3);
       __stcg(gone + w, make_uint4(0u, 0u, 0u, 0u));
       __stcg(kept + w, make_uint4(0u, 0u, 0u, 0u));
     }
   }
   if (tid == 0 && (ends ? blockIdx.x % kForkCluster == 0 : blockIdx.x == 0)) {
     p.state_out[0] = cap > 0 ? wrapped(head, taken, cap) : 0;
-    p.state_out[1] = count - taken + min(back_total, cap - count);
+    p.state_out[1] = count - taken + min(back_total, cap - count + taken);
     p.state_out[2] = need_total - taken;
   }
 }
