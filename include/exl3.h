@@ -541,10 +541,11 @@ exl3_status exl3_device_status(const void *status_word, exl3_stream_t stream);
  *   x, residual [rows][n] halves, row r at x + r * x_stride halves (strides
  *   multiples of 8, at least n); residual may be NULL.  weight [n].
  *   y [rows][n]; h [rows][n] or NULL, written only with a residual.
- * y and h may be x or residual themselves (of stride n), but not one another.
+ * y and h may be x or residual themselves (of stride n), but not one another; otherwise
+ * they overlap no input.
  * n a multiple of 8 up to EXL3_MAX_NORM.  One launch.
  * Errors: EXL3_ERR_BATCH (rows < 0), EXL3_ERR_SHAPE (n, strides, eps negative or
- * not finite), EXL3_ERR_NULL, EXL3_ERR_ALIGN.
+ * not finite, outputs that overlap), EXL3_ERR_NULL, EXL3_ERR_ALIGN.
  */
 exl3_status exl3_rms_norm(const exl3_half *x, long long x_stride, const exl3_half *residual,
                           long long residual_stride, const exl3_half *weight, float eps, int rows,
@@ -561,7 +562,8 @@ exl3_status exl3_rms_norm(const exl3_half *x, long long x_stride, const exl3_hal
  * NaN and q 0.
  *   signs   host array of `outs` device pointers (length n each, or NULL)
  *   q       [outs][rows][n] int8;  qscale [outs][rows][n / 128]
- * n a multiple of 128 up to EXL3_MAX_NORM; the rest as exl3_rms_norm.  One launch.
+ * n a multiple of 128 up to EXL3_MAX_NORM; q and qscale overlap nothing else; the rest as
+ * exl3_rms_norm.  One launch.
  * Errors: as exl3_rms_norm, and EXL3_ERR_BATCH (outs).
  */
 exl3_status exl3_rms_norm_i8(const exl3_half *x, long long x_stride, const exl3_half *residual,

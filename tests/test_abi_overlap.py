@@ -1,0 +1,34 @@
+"""Outputs that overlap one another or an input in a way that the kernels cannot serve are refused, on
+the host before anything reaches a GPU (fake device addresses, never dereferenced)."""
+import ctypes
+
+import pytest
+
+from trellis_decode_gemv_gb300 import binding as B
+
+X, R, W, Y, H = (i << 24 for i in range(1, 6))
+SHAPE = 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return B.load_library()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=H), dict(y=X, h=X), dict(y=R, h=R), dict(y=H + 512), dict(y=H + 2 * 256 * 3 - 16), dict(h=Y + 16),     # one another
+    dict(y=X, xs=512), dict(h=X, xs=512), dict(y=R, rs=264), dict(h=R, rs=264),                                   # an input of another stride
+    dict(y=X + 16), dict(y=X - 16), dict(h=R + 512), dict(y=X + 2 * 1024, xs=1024), dict(h=R + 2 * 2048 + 496, rs=2048),
+    dict(y=X + 528, xs=1024), dict(y=W), dict(h=W - 2 * 256 * 3 + 16)])
+def test_norm(lib, kw):
+    a = dict(x=X, xs=256, r=R, rs=256, w=W, eps=1e-5, rows=3, n=256, y=Y, h=H) | kw
+    assert lib.exl3_rms_norm(*a.values(), None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(h=X, xs=512), dict(h=R, rs=512), dict(h=X + 16), dict(h=W), dict(q=X), dict(q=R), dict(q=W), dict(q=H), dict(q=H + 2 * 256 * 3 - 16),
+    dict(qs=X), dict(qs=R + 512 * 3 - 16), dict(qs=W + 16), dict(qs=H), dict(q=Y, qs=Y), dict(qs=Y + 2 * 256 * 3 - 4),
+    dict(q=X + 512, xs=512)])
+def test_norm_i8(lib, kw):
+    a = dict(x=X, xs=256, r=R, rs=256, w=W, eps=1e-5, rows=3, n=256, s=(ctypes.c_void_p * 2)(None, None), outs=2, q=Y, qs=6 << 24, h=H) | kw
+    assert lib.exl3_rms_norm_i8(*a.values(), None) == SHAPE

@@ -70,6 +70,27 @@ inline exl3_status check_cache(const exl3_kv_cache* c) {
   return EXL3_OK;
 }
 
+// `rows` rows of `len` bytes, `stride` bytes apart, that a call reads or writes.
+struct Span {
+  const void* at;
+  long long rows, len, stride;
+};
+inline Span halves(const void* at, long long rows, long long n, long long stride) { return {at, rows, 2 * n, 2 * stride}; }
+inline Span bytes(const void* at, long long len) { return {at, 1, len, len}; }
+// Whether any of their bytes are the same.  (Rows of different strides that lie between one
+// another count as that.)
+inline bool meet(const Span& a, const Span& b) {
+  if (a.at == nullptr || b.at == nullptr) return false;
+  const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b.at)) - static_cast<long long>(reinterpret_cast<uintptr_t>(a.at));
+  if (d >= (a.rows - 1) * a.stride + a.len || -d >= (b.rows - 1) * b.stride + b.len) return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
+  // row i of a and row j of b: d - a.len < (i - j) * stride < d + b.len
+  const long long s = a.rows > 1 ? a.stride : b.stride, low = d - a.len;
+  long long k = low >= 0 ? low / s + 1 : -((s - 1 - low) / s) + 1;
+  if (k < 1 - b.rows) k = 1 - b.rows;
+  return k < a.rows && k * s < d + b.len;
+}
+
 // Strides of [tokens][heads][dim] halves: whole tokens apart, 16-byte loads.
 inline exl3_status check_stride(long long stride, int heads, int dim) {
   if (stride < static_cast<long long>(heads) * dim || (stride & 7) != 0) return EXL3_ERR_SHAPE;

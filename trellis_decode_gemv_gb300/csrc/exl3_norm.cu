@@ -261,6 +261,17 @@ exl3_status check(const exl3_half* x, long long x_stride, const exl3_half* resid
   return EXL3_OK;
 }
 
+// Whether what is written of `to` (rows of n) meets an input other than as that input itself.
+bool over_inputs(const kv::Span& to, const NormParams& p) {
+  const struct {
+    const __half* at;
+    long long stride;
+  } in[2] = {{p.x, p.x_stride}, {p.residual, p.residual_stride}};
+  for (const auto& i : in)
+    if (!(i.at == to.at && (i.stride == p.n || p.rows == 1)) && kv::meet(to, kv::halves(i.at, p.rows, p.n, i.stride))) return true;
+  return kv::meet(to, kv::halves(p.weight, 1, p.n, p.n));
+}
+
 }  // namespace
 }  // namespace norm
 }  // namespace exl3
@@ -285,6 +296,9 @@ extern "C" exl3_status exl3_rms_norm(const exl3_half* x, long long x_stride, con
   p.eps = eps;
   p.rows = rows;
   p.n = n;
+  // y and h lie apart, and over an input only as that input itself: every row is read before it is written
+  const kv::Span of_y = kv::bytes(y, 2ll * rows * n), of_h = kv::bytes(residual != nullptr ? h : nullptr, 2ll * rows * n);
+  if (kv::meet(of_y, of_h) || norm::over_inputs(of_y, p) || norm::over_inputs(of_h, p)) return EXL3_ERR_SHAPE;
   return norm::launch<false>(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -314,5 +328,14 @@ extern "C" exl3_status exl3_rms_norm_i8(const exl3_half* x, long long x_stride, 
   p.rows = rows;
   p.n = n;
   p.outs = outs;
+  const long long values = 1ll * rows * n;
+  const kv::Span of_h = kv::bytes(residual != nullptr ? h : nullptr, 2 * values), of_q = kv::bytes(q, outs * values),
+                 of_scale = kv::bytes(qscale, outs * (values / 32));
+  if (kv::meet(of_q, of_scale) || norm::over_inputs(of_h, p)) return EXL3_ERR_SHAPE;
+  for (const kv::Span& to : {of_q, of_scale}) {
+    if (kv::meet(to, of_h) || kv::meet(to, kv::halves(x, rows, n, x_stride)) || kv::meet(to, kv::halves(residual, rows, n, residual_stride)) ||
+        kv::meet(to, kv::halves(weight, 1, n, n)))
+      return EXL3_ERR_SHAPE;
+  }
   return norm::launch<true>(p, reinterpret_cast<cudaStream_t>(stream));
 }
