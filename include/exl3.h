@@ -583,13 +583,14 @@ exl3_status exl3_rms_norm_i8(const exl3_half *x, long long x_stride, const exl3_
  *   q [tokens][q_heads][head_dim] halves, token t at q + t * q_stride (strides
  *         multiples of 8, at least heads * head_dim), k the same with its own
  *         stride; k_heads 0: no keys (k, k_out may be NULL).  q_out and k_out may
- *         be q and k (with the same strides).
+ *         be q and k (with the same strides); otherwise they overlap neither those
+ *         nor one another.
  *   position [tokens]: a token of a negative position belongs to no request
  *         (exl3_kv_plan); it is copied as it is.
  * Angles, cosines, sines and products are binary32, the results rounded once.
  * head_dim and rotary_dim <= head_dim multiples of 16, head_dim up to 512.  One launch.
  * Errors: EXL3_ERR_BATCH (tokens < 0), EXL3_ERR_SHAPE (heads, dims, strides, factor
- * not finite), EXL3_ERR_NULL, EXL3_ERR_ALIGN.
+ * not finite, outputs that overlap), EXL3_ERR_NULL, EXL3_ERR_ALIGN.
  */
 exl3_status exl3_rotary(const exl3_half *q, long long q_stride, exl3_half *q_out,
                         long long q_out_stride, int q_heads, const exl3_half *k, long long k_stride,

@@ -32,3 +32,13 @@ def test_norm(lib, kw):
 def test_norm_i8(lib, kw):
     a = dict(x=X, xs=256, r=R, rs=256, w=W, eps=1e-5, rows=3, n=256, s=(ctypes.c_void_p * 2)(None, None), outs=2, q=Y, qs=6 << 24, h=H) | kw
     assert lib.exl3_rms_norm_i8(*a.values(), None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=Y, ko=Y), dict(ko=Y + 2 * 512 * 3 - 16), dict(qo=X, qos=1024), dict(ko=R, kos=512),      # one another; an input of another stride
+    dict(qo=X + 16), dict(qo=R), dict(ko=X), dict(ko=R - 16),
+    dict(q=X, qs=768, k=X + 1024, ks=768, qo=X + 16, qos=768, ko=Y), dict(q=X, qs=768, k=X + 1024, ks=768, qo=X, qos=768, ko=X + 1008, kos=768),
+    dict(q=X, qs=768, k=X + 1024, ks=768, qo=X + 1024, qos=768, ko=X, kos=768)])
+def test_rotary(lib, kw):
+    a = dict(q=X, qs=512, qo=Y, qos=512, qh=4, k=R, ks=256, ko=H, kos=256, kh=2, dim=128, part=64, inter=0, pos=W, f=W, factor=1.0, tokens=3) | kw
+    assert lib.exl3_rotary(*a.values(), None) == SHAPE

@@ -131,6 +131,17 @@ extern "C" exl3_status exl3_rotary(const exl3_half* q, long long q_stride, exl3_
   if (!aligned16(q) || !aligned16(q_out) || (k_heads > 0 && (!aligned16(k) || !aligned16(k_out))) ||
       !kv::aligned_to(position, 4) || !kv::aligned_to(freqs, 8))
     return EXL3_ERR_ALIGN;
+  // the outputs lie apart, and over an input only as q and k themselves: every element is read before it is written
+  kv::Span in[2] = {kv::halves(q, tokens, 1ll * q_heads * head_dim, q_stride), {}};
+  kv::Span out[2] = {kv::halves(q_out, tokens, 1ll * q_heads * head_dim, q_out_stride), {}};
+  if (k_heads > 0) {
+    in[1] = kv::halves(k, tokens, 1ll * k_heads * head_dim, k_stride);
+    out[1] = kv::halves(k_out, tokens, 1ll * k_heads * head_dim, k_out_stride);
+  }
+  if (kv::meet(out[0], out[1])) return EXL3_ERR_SHAPE;
+  for (int o = 0; o < 2; ++o)
+    for (int i = 0; i < 2; ++i)
+      if (!(o == i && in[i].at == out[o].at && (in[i].stride == out[o].stride || tokens == 1)) && kv::meet(out[o], in[i])) return EXL3_ERR_SHAPE;
   rotary::RotaryParams p{};
   p.in[0] = reinterpret_cast<const __half*>(q);
   p.in[1] = reinterpret_cast<const __half*>(k);
