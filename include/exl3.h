@@ -789,7 +789,7 @@ exl3_status exl3_attention_shared(const exl3_kv_cache *cache, const exl3_half *q
  *   free_pages                       the ring: returned pages are entered
  *   free_state_out [3]               {head, count} after the call, and the rows
  *                                    that got no page
- * No output overlaps an input but the ring.  Page numbers outside 0..pages-1 are
+ * No output overlaps another or an input (EXL3_ERR_SHAPE).  Page numbers outside 0..pages-1 are
  * copied with the table and never returned.
  * From then on rows may hold the same pages: a row that does is ended by a fork that
  * does not continue it, not by exl3_kv_plan's new_len < 0, which gives a row's pages
@@ -798,8 +798,8 @@ exl3_status exl3_attention_shared(const exl3_kv_cache *cache, const exl3_half *q
  * zero-filled once after allocation; every call leaves it zero again.  Calls that
  * may run concurrently must not share one.  One launch.
  * Errors: EXL3_ERR_BATCH (rows or requests outside 0..EXL3_MAX_REQUESTS),
- * EXL3_ERR_SHAPE (page_size, pages < 1, table_stride < 1, free_capacity < 0),
- * EXL3_ERR_NULL, EXL3_ERR_ALIGN, EXL3_ERR_WORKSPACE.
+ * EXL3_ERR_SHAPE (page_size, pages < 1, table_stride < 1, free_capacity < 0, outputs that
+ * overlap), EXL3_ERR_NULL, EXL3_ERR_ALIGN, EXL3_ERR_WORKSPACE.
  */
 size_t exl3_kv_fork_workspace_bytes(int pages);
 exl3_status exl3_kv_fork(const int32_t *parent, int rows, const int32_t *ctx_len, int requests,

@@ -42,3 +42,24 @@ def test_norm_i8(lib, kw):
 def test_rotary(lib, kw):
     a = dict(q=X, qs=512, qo=Y, qos=512, qh=4, k=R, ks=256, ko=H, kos=256, kh=2, dim=128, part=64, inter=0, pos=W, f=W, factor=1.0, tokens=3) | kw
     assert lib.exl3_rotary(*a.values(), None) == SHAPE
+
+
+FORK = dict(parent=1, ctx=2, ring=3, state=4, state_out=5, table=6, ctx_out=7, table_out=8, src=9, dst=10, n=11, ws=12)
+WRITTEN = ("ring", "state_out", "ctx_out", "table_out", "src", "dst", "n", "ws")
+
+
+@pytest.mark.parametrize("one,other", [(a, b) for a in WRITTEN for b in FORK if a != b])
+def test_fork(lib, one, other):
+    at = {name: i << 24 for name, i in FORK.items()} | {one: FORK[other] << 24}
+    a = dict(parent=0, rows=3, ctx=0, requests=2, size=16, pages=8, ring=0, cap=8, state=0, state_out=0, table=0, stride=4, ctx_out=0,
+             table_out=0, src=0, dst=0, n=0, ws=0, wsb=64) | at
+    assert lib.exl3_kv_fork(*a.values(), None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [dict(table_out=(6 << 24) + 4 * 4 * 2 - 4), dict(src=(9 << 24) - 8, n=(9 << 24) - 12), dict(ring=(12 << 24) + 32),
+                                dict(state_out=(4 << 24) + 4)])
+def test_fork_that_overlaps_in_part(lib, kw):
+    at = {name: i << 24 for name, i in FORK.items()} | kw
+    a = dict(parent=0, rows=3, ctx=0, requests=2, size=16, pages=8, ring=0, cap=8, state=0, state_out=0, table=0, stride=4, ctx_out=0,
+             table_out=0, src=0, dst=0, n=0, ws=0, wsb=64) | at
+    assert lib.exl3_kv_fork(*a.values(), None) == SHAPE

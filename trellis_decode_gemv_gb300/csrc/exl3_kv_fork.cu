@@ -326,6 +326,24 @@ extern "C" exl3_status exl3_kv_fork(const int32_t* parent, int rows, const int32
     if (!kv::aligned_to(q, 4)) return EXL3_ERR_ALIGN;
   if (workspace == nullptr || workspace_bytes < exl3_kv_fork_workspace_bytes(pages)) return EXL3_ERR_WORKSPACE;
   if (!aligned16(workspace)) return EXL3_ERR_ALIGN;
+  const long long word = sizeof(int32_t), table = word * table_stride;
+  const kv::Span all[] = {   // what is written first
+      kv::bytes(free_state_out, 3 * word),
+      kv::bytes(free_pages, word * free_capacity),
+      kv::bytes(workspace, static_cast<long long>(exl3_kv_fork_workspace_bytes(pages))),
+      kv::bytes(rows > 0 ? ctx_out : nullptr, word * rows),
+      kv::bytes(rows > 0 ? table_out : nullptr, table * rows),
+      kv::bytes(rows > 0 ? copy_from : nullptr, word * rows),
+      kv::bytes(rows > 0 ? copy_to : nullptr, word * rows),
+      kv::bytes(rows > 0 ? copy_tokens : nullptr, word * rows),
+      kv::bytes(free_state, 2 * word),
+      kv::bytes(rows > 0 ? parent : nullptr, word * rows),
+      kv::bytes(requests > 0 ? ctx_len : nullptr, word * requests),
+      kv::bytes(requests > 0 ? block_table : nullptr, table * requests)};
+  constexpr int kSpans = sizeof(all) / sizeof(all[0]), kWritten = kSpans - 4;
+  for (int i = 0; i < kWritten; ++i)
+    for (int j = i + 1; j < kSpans; ++j)
+      if (kv::meet(all[i], all[j])) return EXL3_ERR_SHAPE;
   kv::ForkParams p{};
   p.parent = parent;
   p.ctx_len = ctx_len;
