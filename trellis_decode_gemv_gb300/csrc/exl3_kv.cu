@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   const int b0 = min(tid * per, p.requests);
   const int b1 = min(b0 + per, p.requests);
   const int cap = p.capacity;
-  const int head = cap > 0 ? ((p.state[0] % cap) + cap) % cap : 0;
+  const int head = ring_head(p.state[0], cap);
   const int count = min(max(p.state[1], 0), cap);
 
   long long mine = 0, total;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         if (idx < r.have) {
           pg = *cell;
         } else {
-          pg = p.ring[(head + first[lo] + (idx - r.have)) % cap];
+          pg = p.ring[(static_cast<long long>(head) + first[lo] + (idx - r.have)) % cap];
           if ((at & (page - 1)) == 0) *cell = pg;
         }
         slot = static_cast<long long>(pg) * page + (at & (page - 1));

@@ -70,6 +70,13 @@ inline exl3_status check_cache(const exl3_kv_cache* c) {
   return EXL3_OK;
 }
 
+// The place of a ring's head, whatever number the caller keeps (rings may have more than 2^30 places).
+__device__ __forceinline__ int ring_head(int state, int capacity) {
+  if (capacity <= 0) return 0;
+  const int r = state % capacity;
+  return r < 0 ? r + capacity : r;
+}
+
 // `rows` rows of `len` bytes, `stride` bytes apart, that a call reads or writes.
 struct Span {
   const void* at;

@@ -98,9 +98,10 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
   const int tid = threadIdx.x;
   const int lane = tid & 31;
   const int cap = p.capacity;
-  const int head = cap > 0 ? ((p.state[0] % cap) + cap) % cap : 0;
+  const int head = ring_head(p.state[0], cap);
   const int count = min(max(p.state[1], 0), cap);
   const int size = 1 << p.page_shift;
+  const uint32_t stride = static_cast<uint32_t>(p.stride);   // (places up to 128 past its end fit in 32 bits)
 
   for (int b = tid; b < p.requests; b += threads) first[b] = kNobody;
   __syncthreads();
@@ -135,18 +136,19 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
     const bool live = b >= 0 && b < p.requests;
     const int r = rank[i];
     const int c = live && r < count ? tokens_of(p, b) : 0;
-    const int full = c >> p.page_shift, part = c & (size - 1);
+    const uint32_t full = static_cast<uint32_t>(c) >> p.page_shift;
+    const int part = c & (size - 1);
     const int32_t* old = p.table + static_cast<size_t>(live ? b : 0) * p.stride;
     const int fresh = r >= 0 && c > 0 ? p.ring[wrapped(head, r, cap)] : -1;   // a rank below `count`: cap is not 0
     int32_t* to = p.table_out + static_cast<size_t>(i) * p.stride;
-    const int copied = full + (part > 0 && r < 0 ? 1 : 0);
-    for (int j = lane; j < p.stride; j += 32 * kAtOnce) {
+    const uint32_t copied = full + (part > 0 && r < 0 ? 1 : 0);
+    for (uint32_t j = lane; j < stride; j += 32 * kAtOnce) {
       int v[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) v[k] = j + 32 * k < copied ? old[j + 32 * k] : -1;
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
-        if (j + 32 * k < p.stride) to[j + 32 * k] = j + 32 * k == full && r >= 0 && c > 0 ? fresh : v[k];
+        if (j + 32 * k < stride) to[j + 32 * k] = j + 32 * k == full && r >= 0 && c > 0 ? fresh : v[k];
     }
     if (lane == 0) {
       const bool copy = r >= 0 && c > 0;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kForkThreads) __cluster_dims__(kForkCluster, 1
     // (from the last warp on: the first ones have a row)
     for (int b = warps - 1 - warp; b < p.requests; b += warps) {
       unsigned char* flags = first[b] == kNobody ? p.gone : p.kept;
-      const int held = (tokens_of(p, b) + size - 1) >> p.page_shift;
+      const int held = static_cast<int>((static_cast<uint32_t>(tokens_of(p, b)) + size - 1) >> p.page_shift);
       const int32_t* old = p.table + static_cast<size_t>(b) * p.stride;
       for (int j = lane; j < held; j += 32 * kAtOnce) {
         int v[kAtOnce];
