@@ -29,3 +29,20 @@ def test_outputs_beside_and_over_the_inputs():
     assert torch.equal(wide, before)
     B.exl3_rotary(q, k, position, f, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_as_many_tokens_as_have_a_number():
+    tokens, dim = 2 ** 31 - 1, 16
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of free memory")
+    q = torch.empty((tokens, 1, dim), dtype=torch.float16, device="cuda")
+    position = torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    some = torch.cat([torch.arange(300), 2 ** 30 + torch.arange(300), tokens - 300 + torch.arange(300)]).cuda()
+    small = torch.randn((900, 1, dim), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").half()
+    where = torch.arange(900, dtype=torch.int32, device="cuda") * 7
+    q[some], position[some] = small, where
+    f = B.exl3_rotary_freqs(dim)
+    B.exl3_rotary(q, None, position, f, q_out=q)
+    assert torch.equal(q[some], B.exl3_rotary(small, None, where, f)[0])
+    del q, position
+    torch.cuda.empty_cache()

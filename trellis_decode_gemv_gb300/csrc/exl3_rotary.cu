@@ -165,7 +165,7 @@ extern "C" exl3_status exl3_rotary(const exl3_half* q, long long q_stride, exl3_
   while (p.each * units < 4 * rotary::kThreads && 2 * p.each * (rotary_dim / 2) <= rotary::kMostTable &&
          tokens / (2 * p.each) >= 4 * device_sm_count())
     p.each *= 2;
-  const unsigned blocks = static_cast<unsigned>((tokens + p.each - 1) / p.each);
+  const unsigned blocks = static_cast<unsigned>((tokens + (p.each - 1ll)) / p.each);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   return interleaved != 0 ? launch_chained(rotary::rotary_kernel<true>, dim3(blocks), rotary::kThreads, 0, cs, p)
                           : launch_chained(rotary::rotary_kernel<false>, dim3(blocks), rotary::kThreads, 0, cs, p);
