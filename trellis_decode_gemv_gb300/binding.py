@@ -12,6 +12,8 @@ import ctypes
 import math
 import os
 import re
+from decimal import Decimal, localcontext
+from fractions import Fraction
 
 import torch
 
@@ -1073,14 +1075,20 @@ def exl3_rms_norm_i8(x, weight, eps, signs, residual=None, q=None, qscale=None, 
     return q, qscale, h
 
 
+_PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
 class Exl3RotaryFreqs:
     """What exl3_rotary takes of a model's rotary positions: freqs int64 [rotary_dim / 2],
     each pair's angle a position as a 64-bit fraction of a turn, and the factor on
     cosines and sines."""
 
     def __init__(self, radians, factor=1.0, device="cuda"):
-        """radians: the angle of each pair at position 1 (floats)."""
-        turns = [int(round(float(r) / (2 * math.pi) * 2.0 ** 64)) & (2 ** 64 - 1) for r in radians]
+        """radians: the angle of each pair at position 1, floats (taken as exactly what they are),
+        decimals or fractions.  (A float from rounded arithmetic is off by 2^-53 of itself and more, so
+        at position 2^31 a fast pair's angle by 2^-24 of a turn.)"""
+        to_turns = Fraction(2 ** 64) / (2 * Fraction(_PI))
+        turns = [round(Fraction(r if isinstance(r, (Decimal, Fraction)) else float(r)) * to_turns) & (2 ** 64 - 1) for r in radians]
         signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
         self.rotary_dim = 2 * len(signed)
         self.factor = float(factor)
@@ -1096,29 +1104,32 @@ def exl3_rotary_freqs(rotary_dim, base=10000.0, scaling="none", scale=1.0, origi
         scale, more than `high` times as they are, between them a mixture;
       yarn: the same between `slow` and `fast` turns, linear in the pair's number, and a
         factor of 0.1 ln(scale) + 1 on cosine and sine.
-    factor: another factor on cosine and sine than the scaling's own."""
+    factor: another factor on cosine and sine than the scaling's own.  Computed in decimals of 60
+    digits, so that the fractions of a turn are rounded once."""
     if rotary_dim < 2 or rotary_dim % 2 or base <= 1.0 or scale < 1.0:
         raise ValueError(f"rotary_dim {rotary_dim}, base {base}, scale {scale}: expected an even number, more than 1, at least 1")
-    if scaling == "ntk" and rotary_dim > 2:
-        base = base * scale ** (rotary_dim / (rotary_dim - 2))
-    radians = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
-    own_factor = 1.0
-    if scaling == "linear":
-        radians = [r / scale for r in radians]
-    elif scaling == "llama3":
-        if high <= low:
-            raise ValueError(f"low {low} and high {high}: expected low < high")
-        mix = [min(max((original * r / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for r in radians]
-        radians = [r / scale * (1 - k) + r * k for r, k in zip(radians, mix)]
-    elif scaling == "yarn":
-        def pair(turns):
-            return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
-        first, last = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary_dim - 1)
-        drop = [min(max((i - first) / max(last - first, 0.001), 0.0), 1.0) for i in range(len(radians))]
-        radians = [r / scale * k + r * (1 - k) for r, k in zip(radians, drop)]
-        own_factor = 0.1 * math.log(scale) + 1.0
-    elif scaling not in ("none", "ntk"):
+    if scaling not in ("none", "linear", "ntk", "llama3", "yarn"):
         raise ValueError(f"scaling {scaling!r}: expected none, linear, ntk, llama3 or yarn")
+    if scaling == "llama3" and high <= low:
+        raise ValueError(f"low {low} and high {high}: expected low < high")
+    own_factor = 0.1 * math.log(scale) + 1.0 if scaling == "yarn" else 1.0
+    with localcontext() as context:
+        context.prec = 60
+        base, scale, original, low, high, fast, slow = (Decimal(float(v)) for v in (base, scale, original, low, high, fast, slow))
+        if scaling == "ntk" and rotary_dim > 2:
+            base *= scale ** (Decimal(rotary_dim) / (rotary_dim - 2))
+        radians = [base ** (Decimal(-2 * i) / rotary_dim) for i in range(rotary_dim // 2)]
+        if scaling == "linear":
+            radians = [r / scale for r in radians]
+        elif scaling == "llama3":
+            mix = [min(max((original * r / (2 * _PI) - low) / (high - low), Decimal(0)), Decimal(1)) for r in radians]
+            radians = [r / scale * (1 - k) + r * k for r, k in zip(radians, mix)]
+        elif scaling == "yarn":
+            def pair(turns):
+                return rotary_dim * (original / (turns * 2 * _PI)).ln() / (2 * base.ln())
+            first, last = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary_dim - 1)
+            drop = [min(max((i - first) / max(Decimal(last - first), Decimal("0.001")), Decimal(0)), Decimal(1)) for i in range(len(radians))]
+            radians = [r / scale * k + r * (1 - k) for r, k in zip(radians, drop)]
     return Exl3RotaryFreqs(radians, own_factor if factor is None else factor, device)
 
 
