@@ -793,7 +793,8 @@ exl3_status exl3_attention_shared(const exl3_kv_cache *cache, const exl3_half *q
  * copied with the table and never returned.
  * From then on rows may hold the same pages: a row that does is ended by a fork that
  * does not continue it, not by exl3_kv_plan's new_len < 0, which gives a row's pages
- * back whoever else holds them.
+ * back whoever else holds them; and a row's ctx_len is not lowered into a page that another
+ * row holds too: the tokens that follow would go over what that row has there.
  * workspace: exl3_kv_fork_workspace_bytes(pages) bytes (0 for pages < 1),
  * zero-filled once after allocation; every call leaves it zero again.  Calls that
  * may run concurrently must not share one.  One launch.

@@ -62,9 +62,10 @@ __device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
 
 // sqrt(128) times the 128-point transform of the values of 16 lanes, 8 each in order, two to a
 // register pair.  Instructions bound a large call with rotations, so: two values to an
-// addition, and shuffles whose sums are one fused operation.  (Exchanging half of the
-// registers halves the shuffles, but its selections cost more: 43 us where this takes 27, 2000 rows
-// of 4096 for three projections.)
+// addition, and shuffles whose sums are one fused operation.  With the quantizer's one quotient
+// for a block's values, 2000 rows of 4096 for three projections take 27 us; single additions and a
+// division for each value took 43, and no less with half of the registers exchanged in place of
+// all shuffled, whose selections cost what it saves.
 __device__ __forceinline__ void hadamard128(uint64_t (&f)[4], int lane) {
   const uint64_t minus = pair(-1.f, -1.f);
 #pragma unroll
