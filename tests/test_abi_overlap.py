@@ -63,3 +63,18 @@ def test_fork_that_overlaps_in_part(lib, kw):
     a = dict(parent=0, rows=3, ctx=0, requests=2, size=16, pages=8, ring=0, cap=8, state=0, state_out=0, table=0, stride=4, ctx_out=0,
              table_out=0, src=0, dst=0, n=0, ws=0, wsb=64) | at
     assert lib.exl3_kv_fork(*a.values(), None) == SHAPE
+
+
+@pytest.mark.parametrize("by", [4, 8])
+def test_nothing_overlaps_an_empty_ring(lib, by):
+    """A ring of no places may lie anywhere (the call is refused for what overlaps besides)."""
+    at = {name: i << 24 for name, i in FORK.items()} | dict(ring=(5 << 24) + by, dst=9 << 24)
+    a = dict(parent=0, rows=3, ctx=0, requests=2, size=16, pages=8, ring=0, cap=0, state=0, state_out=0, table=0, stride=4, ctx_out=0,
+             table_out=0, src=0, dst=0, n=0, ws=0, wsb=64) | at
+    assert lib.exl3_kv_fork(*a.values(), None) == SHAPE
+
+
+def test_the_stride_of_one_row_says_nothing(lib):
+    """(Refused for two outputs in one place, not for an arithmetic of strides.)"""
+    a = dict(x=X, xs=(1 << 63) - 8, r=R, rs=1 << 62, w=W, eps=1e-5, rows=1, n=256, y=Y, h=Y)
+    assert lib.exl3_rms_norm(*a.values(), None) == SHAPE

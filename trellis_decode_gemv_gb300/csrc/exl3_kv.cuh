@@ -82,12 +82,12 @@ struct Span {
   const void* at;
   long long rows, len, stride;
 };
-inline Span halves(const void* at, long long rows, long long n, long long stride) { return {at, rows, 2 * n, 2 * stride}; }
+inline Span halves(const void* at, long long rows, long long n, long long stride) { return {at, rows, 2 * n, 2 * (rows > 1 ? stride : n)}; }
 inline Span bytes(const void* at, long long len) { return {at, 1, len, len}; }
 // Whether any of their bytes are the same.  (Rows of different strides that lie between one
 // another count as that.)
 inline bool meet(const Span& a, const Span& b) {
-  if (a.at == nullptr || b.at == nullptr) return false;
+  if (a.at == nullptr || b.at == nullptr || a.len == 0 || b.len == 0) return false;
   const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b.at)) - static_cast<long long>(reinterpret_cast<uintptr_t>(a.at));
   if (d >= (a.rows - 1) * a.stride + a.len || -d >= (b.rows - 1) * b.stride + b.len) return false;
   if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
